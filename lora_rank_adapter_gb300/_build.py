@@ -1,4 +1,4 @@
-"""Builds liblora.so (the C ABI of include/lora.h) in-tree for sm_103a.
+"""Builds liblora.so (the C ABI of include/lora.h and include/lora_train.h) in-tree for sm_103a.
 
 Each CUDA translation unit is compiled in parallel with nvcc, then linked into
 lora_rank_adapter_gb300/_lib/liblora.so with the static CUDA runtime (so the
@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIB_DIR, "liblora.so")
-SOURCES = ["api.cu", "single_common.cu", "single_tc.cu", "single_f32.cu", "multi.cu", "decode.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "single_common.cu", "single_tc.cu", "single_f32.cu", "multi.cu", "decode.cu", "noalloc.cu",
+           "loss.cu", "adamw.cu", "train_api.cu"]
 ARCH = "arch=compute_103a,code=sm_103a"
 NVCC_FLAGS = ["-std=c++17", "-O3", "-gencode", ARCH, "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden"]
@@ -31,7 +32,8 @@ def _nvcc():
 
 def _deps():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files.append(os.path.join(os.path.dirname(HERE), "include", "lora.h"))
+    include = os.path.join(os.path.dirname(HERE), "include")
+    files += [os.path.join(include, f) for f in sorted(os.listdir(include))]
     return files
 
 

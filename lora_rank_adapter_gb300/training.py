@@ -1,0 +1,326 @@
+"""Thin Python binding of the training operators (include/lora_train.h): the
+log-probabilities of labels, the preference loss and the clipped policy loss with
+their gradients, and the AdamW step over an adapter's many tensors.
+
+Like `binding`, each function has the name of the C entry point it calls, takes
+torch tensors that already live on the GPU, checks and marshals them, allocates
+the workspace the C side asks for and passes the current CUDA stream; outputs are
+tensors of the caller.  All arithmetic runs in the library's CUDA kernels.
+
+    from lora_rank_adapter_gb300 import training
+    training.lora_preference_loss(logits, labels, cu_seqlens, ref_logps, 0.1,
+                                  token_logps, seq_logps, pair_loss, loss, dlogits=dlogits)
+    plan = training.lora_adamw_plan(params, grads, exp_avg, exp_avg_sq)   # once
+    training.lora_grad_norm(plan, 1.0, norm)                              # each step
+    training.lora_adamw(plan, lr=1e-4, step=k, grad_factor=norm[1:])
+
+`torch_ops` holds the differentiable forms.
+"""
+import ctypes
+
+import torch
+
+from . import binding
+from .binding import _check, _dtype, _ptr, _stream, _ws_args
+
+TRAIN_EXPORTS = ["lora_train_workspace_size", "lora_token_logps", "lora_token_logps_backward",
+                 "lora_preference_loss", "lora_policy_loss", "lora_scale_gradient", "lora_adamw_table_size",
+                 "lora_adamw_build", "lora_grad_norm", "lora_adamw"]
+TRAIN_PREFERENCE_LOSS, TRAIN_POLICY_LOSS, TRAIN_GRAD_NORM = 0, 1, 2
+PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+PREF_LENGTH_NORMALIZE = 1
+ADAMW_STATE_8BIT, ADAMW_MASTER = 1, 2
+ADAMW_BLOCK, ADAMW_CHUNK = 256, 2048
+
+
+class AdamWTensor(ctypes.Structure):
+    """lora_adamw_tensor_t: the device addresses of one tensor and its size."""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("master", ctypes.c_void_p), ("numel", ctypes.c_int64)]
+
+
+class AdamWPlanStruct(ctypes.Structure):
+    """lora_adamw_plan_t."""
+    _fields_ = [("table", ctypes.c_void_p), ("chunks", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class AdamWHyper(ctypes.Structure):
+    """lora_adamw_hyper_t."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64)]
+
+
+_lib = None
+
+
+def lib():
+    """The loaded liblora.so with the signatures of include/lora_train.h."""
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = binding.lib()
+    i32, i64, u32, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
+    P, sz = ctypes.c_void_p, ctypes.c_size_t
+    TP, PP, HP = ctypes.POINTER(AdamWTensor), ctypes.POINTER(AdamWPlanStruct), ctypes.POINTER(AdamWHyper)
+    sig = {
+        "lora_train_workspace_size": (sz, [i32, i64, i64]),
+        "lora_token_logps": (i32, [i32, i64, i64, P, i64, P, f32, P, P, P]),
+        "lora_token_logps_backward": (i32, [i32, i64, i64, P, i64, P, f32, P, P, P, i64, P]),
+        "lora_preference_loss": (i32, [i32, i64, i64, i32, P, i64, P, P, P, i32, f32, f32, u32, f32, P, P, P, P,
+                                       P, i64, f32, P, sz, P]),
+        "lora_policy_loss": (i32, [i32, i64, i64, P, i64, P, P, P, P, P, f32, f32, f32, f32, P, P, P, i64, f32,
+                                   P, sz, P]),
+        "lora_scale_gradient": (i32, [i32, i64, i64, P, i64, P, P]),
+        "lora_adamw_table_size": (sz, [TP, i32]),
+        "lora_adamw_build": (i32, [TP, i32, i32, i32, u32, P, sz, PP, P]),
+        "lora_grad_norm": (i32, [PP, f32, P, P, sz, P]),
+        "lora_adamw": (i32, [PP, HP, P, P]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(L, name)
+        fn.restype = res
+        fn.argtypes = args
+    _lib = L
+    return L
+
+
+def _expect(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _vector(t, n, dtype, name, device):
+    """A contiguous vector of n elements on the logits' device."""
+    _expect(t.dtype == dtype and t.device == device, f"{name} has to be {dtype} on {device}")
+    _expect(t.numel() == n and t.is_contiguous(), f"{name} has to hold {n} contiguous elements")
+    return t
+
+
+def _rows(logits, labels):
+    _expect(logits.dim() == 2, "logits have to be [T, V]")
+    _expect(logits.is_cuda, "logits have to be on a GPU")
+    T, V = logits.shape
+    _expect(V <= 1 or T == 0 or logits.stride(1) == 1, "logits need unit column stride")
+    _vector(labels, T, torch.int64, "labels", logits.device)
+    return T, V
+
+
+def _ld(t):
+    """Row stride of a [T, V] tensor (of one row: any that fits)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _gradient(dlogits, logits):
+    if dlogits is None:
+        return None, 0
+    _expect(dlogits.shape == logits.shape and dlogits.dtype == logits.dtype and dlogits.device == logits.device,
+            "dlogits have to be like the logits")
+    _expect(dlogits.shape[1] <= 1 or dlogits.shape[0] == 0 or dlogits.stride(1) == 1,
+            "dlogits need unit column stride")
+    return dlogits, _ld(dlogits)
+
+
+def train_workspace(op, n, pairs=0, device="cuda", stream=None):
+    """A uint8 workspace of lora_train_workspace_size() bytes (None when zero),
+    kept by the caching allocator until `stream` is done with it."""
+    size = lib().lora_train_workspace_size(op, n, pairs)
+    if size == 0:
+        return None
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+# ----------------------------------------------------------------------------- log-probabilities and losses
+def lora_token_logps(logits, labels, logps, temperature=1.0, stats=None, stream=None):
+    """logps[t] = log_softmax(logits[t] / temperature)[labels[t]] (fp32; 0 where the
+    label is outside [0, V)).  stats: fp32 [T, 2] for lora_token_logps_backward."""
+    T, V = _rows(logits, labels)
+    _vector(logps, T, torch.float32, "logps", logits.device)
+    if stats is not None:
+        _vector(stats, 2 * T, torch.float32, "stats", logits.device)
+    st = lib().lora_token_logps(_dtype(logits), T, V, _ptr(logits), _ld(logits), _ptr(labels), float(temperature),
+                                _ptr(logps), _ptr(stats), _stream(stream))
+    _check(st, "lora_token_logps")
+    return logps
+
+
+def lora_token_logps_backward(logits, labels, stats, dlogps, dlogits, temperature=1.0, stream=None):
+    """dlogits of lora_token_logps from its stats and the log-probabilities' gradient
+    dlogps (fp32 [T]); dlogits may be the logits themselves."""
+    T, V = _rows(logits, labels)
+    _vector(stats, 2 * T, torch.float32, "stats", logits.device)
+    _vector(dlogps, T, torch.float32, "dlogps", logits.device)
+    _expect(dlogits is not None, "dlogits are missing")
+    dlogits, ldd = _gradient(dlogits, logits)
+    st = lib().lora_token_logps_backward(_dtype(logits), T, V, _ptr(logits), _ld(logits), _ptr(labels),
+                                         float(temperature), _ptr(stats), _ptr(dlogps), _ptr(dlogits), ldd,
+                                         _stream(stream))
+    _check(st, "lora_token_logps_backward")
+    return dlogits
+
+
+def lora_preference_loss(logits, labels, cu_seqlens, ref_logps, beta, token_logps, seq_logps, pair_loss, loss,
+                         dlogits=None, kind="sigmoid", label_smoothing=0.0, length_normalize=False, temperature=1.0,
+                         grad_scale=1.0, ws=None, stream=None):
+    """The paired log-ratio loss over packed sequences (int32 cu_seqlens [2P + 1]; pair p
+    prefers sequence p to sequence P + p); with dlogits also its gradient.  ref_logps
+    [2P] or None; token_logps [T], seq_logps [2P], pair_loss [P] and loss [1] are written."""
+    T, V = _rows(logits, labels)
+    dev = logits.device
+    _expect(kind in PREFERENCE_KINDS, f"kind has to be one of {sorted(PREFERENCE_KINDS)}")
+    _expect(cu_seqlens.numel() % 2 == 1, "cu_seqlens have to hold 2 P + 1 offsets")
+    P = cu_seqlens.numel() // 2
+    _vector(cu_seqlens, 2 * P + 1, torch.int32, "cu_seqlens", dev)
+    if ref_logps is not None:
+        _vector(ref_logps, 2 * P, torch.float32, "ref_logps", dev)
+    _vector(token_logps, T, torch.float32, "token_logps", dev)
+    _vector(seq_logps, 2 * P, torch.float32, "seq_logps", dev)
+    _vector(pair_loss, P, torch.float32, "pair_loss", dev)
+    _vector(loss, 1, torch.float32, "loss", dev)
+    dlogits, ldd = _gradient(dlogits, logits)
+    if ws is None:
+        ws = train_workspace(TRAIN_PREFERENCE_LOSS, T, P, dev, stream)
+    st = lib().lora_preference_loss(_dtype(logits), T, V, P, _ptr(logits), _ld(logits), _ptr(labels),
+                                    _ptr(cu_seqlens), _ptr(ref_logps), PREFERENCE_KINDS[kind], float(beta),
+                                    float(label_smoothing), PREF_LENGTH_NORMALIZE if length_normalize else 0,
+                                    float(temperature), _ptr(token_logps), _ptr(seq_logps), _ptr(pair_loss),
+                                    _ptr(loss), _ptr(dlogits), ldd, float(grad_scale), *_ws_args(ws),
+                                    _stream(stream))
+    _check(st, "lora_preference_loss")
+    return loss
+
+
+def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps, metrics, ref_logps=None,
+                     dlogits=None, clip_low=0.2, clip_high=0.2, kl_beta=0.0, temperature=1.0, grad_scale=1.0,
+                     ws=None, stream=None):
+    """The clipped policy loss with a KL term, summed with the tokens' weights (None: 1);
+    with dlogits also its gradient.  old_logps, ref_logps: fp32 [T] or None.  token_logps
+    [T] and metrics [3] (loss, weighted KL, weight of the clipped tokens) are written."""
+    T, V = _rows(logits, labels)
+    dev = logits.device
+    for name, t in (("old_logps", old_logps), ("ref_logps", ref_logps), ("weights", weights)):
+        if t is not None:
+            _vector(t, T, torch.float32, name, dev)
+    _vector(advantages, T, torch.float32, "advantages", dev)
+    _vector(token_logps, T, torch.float32, "token_logps", dev)
+    _vector(metrics, 3, torch.float32, "metrics", dev)
+    dlogits, ldd = _gradient(dlogits, logits)
+    if ws is None:
+        ws = train_workspace(TRAIN_POLICY_LOSS, T, 0, dev, stream)
+    st = lib().lora_policy_loss(_dtype(logits), T, V, _ptr(logits), _ld(logits), _ptr(labels), _ptr(old_logps),
+                                _ptr(ref_logps), _ptr(advantages), _ptr(weights), float(clip_low), float(clip_high),
+                                float(kl_beta), float(temperature), _ptr(token_logps), _ptr(metrics), _ptr(dlogits),
+                                ldd, float(grad_scale), *_ws_args(ws), _stream(stream))
+    _check(st, "lora_policy_loss")
+    return metrics
+
+
+def lora_scale_gradient(x, factor, stream=None):
+    """x *= factor (fp32 device scalar) in place for a [T, V] gradient; no pass over x when it is 1."""
+    _expect(x.dim() == 2 and x.is_cuda and (x.shape[1] <= 1 or x.shape[0] == 0 or x.stride(1) == 1),
+            "x has to be [T, V] on a GPU with unit column stride")
+    _vector(factor, 1, torch.float32, "factor", x.device)
+    st = lib().lora_scale_gradient(_dtype(x), x.shape[0], x.shape[1], _ptr(x), _ld(x), _ptr(factor), _stream(stream))
+    _check(st, "lora_scale_gradient")
+    return x
+
+
+# ----------------------------------------------------------------------------- optimizer
+class AdamWPlan:
+    """The addresses of an optimizer's tensors, laid out once on the device.  Holds
+    the tensors; build it again when one of them is replaced."""
+
+    def __init__(self, struct, table, tensors):
+        self.struct, self.table, self.tensors = struct, table, tensors
+        self.ref = ctypes.byref(struct)
+
+    @property
+    def chunks(self):
+        return self.struct.chunks
+
+
+def _dense(t):
+    """Whether the elements fill one stretch of memory in some order of the axes."""
+    want = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda x: (x[1], x[0])):
+        if size == 1:
+            continue
+        if stride != want:
+            return False
+        want *= size
+    return True
+
+
+def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
+                    stream=None):
+    """Lays out the tensors of lora_grad_norm and lora_adamw.  params and grads: lists of
+    bf16 or fp32 tensors (one dtype each).  States in 32 bits: fp32 tensors.  States in 8
+    bits: float8_e4m3fn (or uint8) codes of the same shape, with fp32 scales
+    [ceil(numel / 256)] in exp_avg_scales / exp_avg_sq_scales (exp_avg_sq then holds the
+    square root of the second moment).  masters: fp32 copies that the step updates, the
+    parameters being their rounding.  A tensor, its gradient, states and master share one
+    dense layout."""
+    n = len(params)
+    s8 = exp_avg_scales is not None
+    _expect(s8 == (exp_avg_sq_scales is not None), "8-bit states need both lists of scales")
+    lists = {"grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq, "masters": masters,
+             "exp_avg_scales": exp_avg_scales, "exp_avg_sq_scales": exp_avg_sq_scales}
+    for name, values in lists.items():
+        _expect(values is None or len(values) == n, f"{name} has to hold one tensor for each of the {n} params")
+    device = params[0].device if n else torch.device("cuda", torch.cuda.current_device())
+    _expect(device.type == "cuda", "params have to be on a GPU")
+    state = (torch.float8_e4m3fn, torch.uint8) if s8 else (torch.float32,)
+    kinds = {"grads": None, "exp_avg": state, "exp_avg_sq": state, "masters": (torch.float32,)}
+    table_in = (AdamWTensor * max(n, 1))()
+    for i, p in enumerate(params):
+        _expect(p.dtype == params[0].dtype and p.device == device, "params have to share dtype and device")
+        _expect(_dense(p), "params have to be dense")
+        for name, allowed in kinds.items():
+            if lists[name] is None:
+                continue
+            t = lists[name][i]
+            allowed = allowed or (grads[0].dtype,)
+            _expect(t.dtype in allowed and t.device == device, f"{name}[{i}] has to be {allowed[0]} on {device}")
+            _expect(t.shape == p.shape and (t.stride() == p.stride() or (t.is_contiguous() and p.is_contiguous())),
+                    f"{name}[{i}] has to have its parameter's shape and strides")
+        for name in ("exp_avg_scales", "exp_avg_sq_scales"):
+            if s8:
+                _vector(lists[name][i], -(-p.numel() // ADAMW_BLOCK), torch.float32, name, device)
+        addr = lambda values: values[i].data_ptr() if values is not None and p.numel() else None  # noqa: E731
+        table_in[i] = AdamWTensor(addr(params), addr(grads), addr(exp_avg), addr(exp_avg_sq), addr(exp_avg_scales),
+                                  addr(exp_avg_sq_scales), addr(masters), p.numel())
+    flags = (ADAMW_STATE_8BIT if s8 else 0) | (ADAMW_MASTER if masters is not None else 0)
+    size = lib().lora_adamw_table_size(table_in, n)
+    table = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        table.record_stream(stream)
+    struct = AdamWPlanStruct()
+    st = lib().lora_adamw_build(table_in, n, _dtype(params[0]) if n else binding.LORA_F32,
+                                _dtype(grads[0]) if n else binding.LORA_F32, flags, _ptr(table), table.numel(),
+                                ctypes.byref(struct), _stream(stream))
+    _check(st, "lora_adamw_build")
+    return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}))
+
+
+def lora_grad_norm(plan, max_norm, out, ws=None, stream=None):
+    """out[0] = the 2-norm of all gradients, out[1] = min(1, max_norm / (norm + 1e-6)) (fp32 [2])."""
+    _vector(out, 2, torch.float32, "out", plan.table.device)
+    if ws is None:
+        ws = train_workspace(TRAIN_GRAD_NORM, plan.chunks, 0, plan.table.device, stream)
+    st = lib().lora_grad_norm(plan.ref, float(max_norm), _ptr(out), *_ws_args(ws), _stream(stream))
+    _check(st, "lora_grad_norm")
+    return out
+
+
+def lora_adamw(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_factor=None, stream=None):
+    """One AdamW step over the plan's tensors; step counts from 1.  grad_factor: fp32
+    device scalar that the gradients are multiplied by (lora_grad_norm's out[1:])."""
+    if grad_factor is not None:
+        _vector(grad_factor, 1, torch.float32, "grad_factor", plan.table.device)
+    hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
+    st = lib().lora_adamw(plan.ref, ctypes.byref(hyper), _ptr(grad_factor), _stream(stream))
+    _check(st, "lora_adamw")
