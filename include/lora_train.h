@@ -16,8 +16,9 @@
  * need only the alignment of their element type: any row stride, any V.
  *
  * The loss operators work on T rows of logits, element (t, v) at
- * logits[t*ldl + v], LORA_BF16 or LORA_F32, 0 <= T, V < 2^31, ldl >= V, and on
- * labels[t] (int64): row t scores label labels[t].  (A causal model's caller
+ * logits[t*ldl + v], LORA_BF16 or LORA_F32, 0 <= T < 2^31, 0 <= V <= 2^30
+ * (above: LORA_ERR_UNSUPPORTED), ldl >= V, and on labels[t] (int64): row t scores
+ * label labels[t].  (A causal model's caller
  * passes the labels already moved by one.)  A label outside [0, V) marks an
  * IGNORED row: it contributes nothing, its log-probability and its gradient are
  * zero, and its logits are not read (they may hold anything, NaN included).

@@ -13,6 +13,7 @@
 #include "adamw.h"
 #include "common.cuh"
 #include "host_common.h"
+#include "sum2.cuh"
 
 namespace lora {
 namespace {
@@ -223,15 +224,15 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
 }
 
 // ----------------------------------------------------------------------------- the norm
-// Squares summed in 32 bits over a thread's elements of a chunk, in 64 bits
+// Squares summed in fp32 over a lane's elements of a chunk, in two fp32 parts
 // beyond that; the last block adds the blocks' sums in block order.
 template <typename G>
-__global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, int64_t chunks, double *part,
+__global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, int64_t chunks, Sum2 *part,
                                                         unsigned *ticket, float max_norm, float *out) {
-  __shared__ double sh[kThreads / 32];
+  __shared__ Sum2 sh[kThreads / 32];
   __shared__ unsigned before;
   pdl_wait();
-  double sum = 0.0;
+  Sum2 sum;
   for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
     const G *g = static_cast<const G *>(table[k].g);
     const int at = (int)threadIdx.x * kLane, n = min(max((int)table[k].count - at, 0), kLane);
@@ -239,20 +240,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
     load_lane(g + at, v, n, (reinterpret_cast<uintptr_t>(g) & 15u) == 0);
 #pragma unroll
     for (int i = 0; i < kLane; ++i) s += v[i] * v[i];
-    sum += s;
+    sum.add(s);
   }
-  auto block_sum = [&](double x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    __syncthreads();
-    if (lane_id() == 0) sh[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = sh[0];
-#pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) x += sh[i];
-    return x;
-  };
-  sum = block_sum(sum);
+  sum = block_sum<kThreads / 32>(sum, sh);
   if (threadIdx.x == 0) {
     part[blockIdx.x] = sum;
     __threadfence();
@@ -261,11 +251,17 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
   }
   __syncthreads();
   if (before != gridDim.x - 1) return;
-  sum = 0.0;
-  for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) sum += __ldcg(part + i);
-  sum = block_sum(sum);
+  sum = Sum2();
+  for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) {
+    const float2 p = __ldcg(reinterpret_cast<const float2 *>(part) + i);
+    Sum2 one;
+    one.hi = p.x;
+    one.lo = p.y;
+    sum.add(one);
+  }
+  sum = block_sum<kThreads / 32>(sum, sh);
   if (threadIdx.x == 0) {
-    const float norm = (float)sqrt(sum), f = max_norm / (norm + 1e-6f);
+    const float norm = sqrtf(sum.value()), f = max_norm / (norm + 1e-6f);
     out[0] = norm;
     out[1] = f >= 1.f ? 1.f : f;      // a NaN norm gives a NaN factor
   }
@@ -289,7 +285,7 @@ cudaError_t run_step(const lora_adamw_plan_t &plan, const StepArgs &a, cudaStrea
 static int64_t norm_blocks(int64_t chunks) { return std::max<int64_t>(1, std::min<int64_t>(chunks, kNormBlocks)); }
 
 size_t grad_norm_ws_bytes(int64_t chunks) {
-  return ws_round(sizeof(unsigned)) + ws_round(8 * (size_t)norm_blocks(chunks));
+  return ws_round(sizeof(unsigned)) + ws_round(sizeof(Sum2) * (size_t)norm_blocks(chunks));
 }
 
 lora_status_t adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, const lora_adamw_plan_t &plan,
@@ -323,7 +319,7 @@ lora_status_t grad_norm(const lora_adamw_plan_t &plan, float max_norm, float *ou
   WsCarver c(ws, ws_bytes);
   unsigned *ticket = static_cast<unsigned *>(c.take(sizeof(unsigned)));
   const int blocks = (int)std::min<int64_t>(norm_blocks(plan.chunks), 8 * (int64_t)num_sms());
-  double *part = static_cast<double *>(c.take(8 * (size_t)blocks));
+  Sum2 *part = static_cast<Sum2 *>(c.take(sizeof(Sum2) * (size_t)blocks));
   if (part == nullptr) return LORA_ERR_WORKSPACE;
   LORA_CUDA(cudaMemsetAsync(ticket, 0, sizeof(unsigned), st));
   const AdamChunk *table = static_cast<const AdamChunk *>(plan.table);

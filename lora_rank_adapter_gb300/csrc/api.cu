@@ -11,6 +11,7 @@
 #include <utility>
 
 #include "host_common.h"
+#include "loss.h"
 #include "multi.h"
 #include "single_common.h"
 #include "single_tc.h"
@@ -459,8 +460,8 @@ lora_status_t lora_gather_shrink(const lora_addressing_t *addr, const int32_t *r
 lora_status_t lora_device_error(int32_t *code) {
   if (code == nullptr) return LORA_ERR_INVALID_ARG;
   int v = 0;
-  int parts[5] = {read_clear_error_single_common(), read_clear_error_single_f32(), read_clear_error_multi(),
-                  read_clear_error_single_tc(), read_clear_error_decode()};
+  int parts[6] = {read_clear_error_single_common(), read_clear_error_single_f32(), read_clear_error_multi(),
+                  read_clear_error_single_tc(), read_clear_error_decode(), read_clear_error_loss()};
   for (int p : parts) {
     if (p < 0) return LORA_ERR_CUDA;
     v |= p;

@@ -9,9 +9,13 @@
 //   grad_kernel    d = c * ((v == label) - exp(z - m) / S), the row read again.
 #include <math.h>
 
+#include <algorithm>
+#include <mutex>
+
 #include "common.cuh"
 #include "host_common.h"
 #include "loss.h"
+#include "sum2.cuh"
 
 namespace lora {
 namespace {
@@ -25,6 +29,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 values in one 64-bit register: one instruction works on both.
+__device__ __forceinline__ uint64_t pk2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpk2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+  const float2 f = unpk2(v);
+  return pk2(ex2(f.x), ex2(f.y));
+}
+
 template <typename E>
 struct Elem;
 template <>
@@ -32,6 +62,25 @@ struct Elem<float> {
   static constexpr int kVec = 4;
   static __device__ __forceinline__ float load(const float *p) { return *p; }
   static __device__ __forceinline__ void store(float *p, float v) { *p = v; }
+  // a 16-byte piece as kVec / 2 pairs, and its largest value
+  static __device__ __forceinline__ void pairs(const uint4 &q, uint64_t *v) {
+    v[0] = pk2(__uint_as_float(q.x), __uint_as_float(q.y));
+    v[1] = pk2(__uint_as_float(q.z), __uint_as_float(q.w));
+  }
+  static __device__ __forceinline__ uint4 pack_pairs(const uint64_t *v) {
+    const float2 a = unpk2(v[0]), b = unpk2(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 (&q)[U]) {
+    float b = kNegInf;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      b = fmaxf(b, fmaxf(fmaxf(__uint_as_float(q[u].x), __uint_as_float(q[u].y)),
+                         fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w))));
+    return b;
+  }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
   static __device__ __forceinline__ void unpack(const uint4 &q, float *v) {
     v[0] = __uint_as_float(q.x);
     v[1] = __uint_as_float(q.y);
@@ -47,6 +96,31 @@ struct Elem<__nv_bfloat16> {
   static constexpr int kVec = 8;
   static __device__ __forceinline__ float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void pairs(const uint4 &q, uint64_t *v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 pack_pairs(const uint64_t *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpk2(v[i]);
+      w[i] = pack_bf16(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 (&q)[U]) {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+    __nv_bfloat162 b = two(0xff80ff80u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      b = __hmax2(b, __hmax2(__hmax2(two(q[u].x), two(q[u].y)), __hmax2(two(q[u].z), two(q[u].w))));
+    const float2 f = __bfloat1622float2(b);
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
   static __device__ __forceinline__ void unpack(const uint4 &q, float *v) {
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -61,16 +135,17 @@ struct Elem<__nv_bfloat16> {
 };
 
 // A row split at 16-byte boundaries: `head` elements before the first, `vecs`
-// whole 16-byte pieces, and the rest.
+// whole 16-byte pieces, and the rest.  (V < 2^31: places within a row are ints.)
 template <typename E>
 struct RowSpan {
-  int64_t head, vecs;
-  __device__ __forceinline__ RowSpan(const E *row, int64_t V) {
+  int head, vecs;
+  __device__ __forceinline__ RowSpan(const E *row, int V) {
     const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-    head = ((16u - off) & 15u) / sizeof(E);
+    head = (int)(((16u - off) & 15u) / sizeof(E));
     if (head > V) head = V;
     vecs = (V - head) / Elem<E>::kVec;
   }
+  __device__ __forceinline__ int tail() const { return head + vecs * Elem<E>::kVec; }
 };
 
 // Running (m, s): the largest value seen and s = sum exp((x - m) * inv_t), with
@@ -79,44 +154,72 @@ struct RowSpan {
 // exp(-inf - ref) is 0 and not NaN.
 __device__ __forceinline__ float ref_of(float m) { return m == kNegInf ? 0.f : m; }
 
-__device__ __forceinline__ void merge(float &m, float &s, float m2, float s2, float k) {
-  const float mm = fmaxf(m, m2), r = ref_of(mm);
-  s = s * ex2((m - r) * k) + s2 * ex2((m2 - r) * k);
+// One element into the running pair.
+__device__ __forceinline__ void absorb_one(float &m, float &s, float v, float k) {
+  const float mm = fmaxf(m, v), r = ref_of(mm);
+  s = s * ex2((m - r) * k) + ex2((v - r) * k);
   m = mm;
 }
 
-// One element / one 16-byte piece into the running pair.
-template <int N>
-__device__ __forceinline__ void absorb(float &m, float &s, const float *v, float k) {
-  float b = v[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) b = fmaxf(b, v[i]);
-  const float mm = fmaxf(m, b), r = ref_of(mm);
-  float add = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) add += ex2((v[i] - r) * k);
-  s = s * ex2((m - r) * k) + add;
+// U 16-byte pieces into a running maximum and a pair of partial sums.  The
+// reference moves once for all of them.
+template <typename E, int U>
+__device__ __forceinline__ void absorb(float &m, uint64_t &s, const uint4 (&q)[U], float k) {
+  const float mm = fmaxf(m, Elem<E>::largest(q)), r = ref_of(mm), f = ex2((m - r) * k);
+  const uint64_t r2 = pk2(-r, -r), k2 = pk2(k, k);
   m = mm;
+  s = mul2(s, pk2(f, f));
+  uint64_t t = 0;      // a second chain of sums: (0, 0)
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint64_t v[Elem<E>::kVec / 2];
+    Elem<E>::pairs(q[u], v);
+#pragma unroll
+    for (int j = 0; j < Elem<E>::kVec / 2; ++j) {
+      const uint64_t e = ex2_2(mul2(add2(v[j], r2), k2));
+      if (j & 1) t = add2(t, e); else s = add2(s, e);
+    }
+  }
+  s = add2(s, t);
 }
 
-// (m, s) of the whole block, known to every thread.  sh: 2 floats per warp.
+// Pieces [from, to) of a row, kThreads threads, four loads of each in flight.
+template <typename E, int kThreads>
+__device__ __forceinline__ void absorb_span(float &m, uint64_t &s, const uint4 *p, int from, int to, float k) {
+  int i = from + (int)threadIdx.x;
+  for (; to - i > 3 * kThreads; i += 4 * kThreads) {
+    const uint4 q[4] = {p[i], p[i + kThreads], p[i + 2 * kThreads], p[i + 3 * kThreads]};
+    absorb<E, 4>(m, s, q, k);
+  }
+  if (i < to) {
+    uint4 q[3];
+#pragma unroll
+    for (int u = 0; u < 3; ++u) q[u] = to - i > u * kThreads ? p[i + u * kThreads] : Elem<E>::lowest();
+    absorb<E, 3>(m, s, q, k);
+  }
+}
+
+// (m, s) of the warp's lanes: the largest m, then one rescaling of each s.
+__device__ __forceinline__ void warp_merge(float &m, float &s, float k) {
+  float mm;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mm) : "f"(m));
+  s *= ex2((m - ref_of(mm)) * k);
+  m = mm;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+}
+
+// (m, s) of the whole block, known to the threads of warp 0.
 template <int kWarps>
-__device__ __forceinline__ void block_merge(float &m, float &s, float k, float *sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    merge(m, s, m2, s2, k);
-  }
-  const int w = threadIdx.x >> 5;
-  if (lane_id() == 0) {
-    sh[2 * w] = m;
-    sh[2 * w + 1] = s;
-  }
+__device__ __forceinline__ void block_merge(float &m, float &s, float k, float2 *sh) {
+  warp_merge(m, s, k);
+  if (lane_id() == 0) sh[threadIdx.x >> 5] = make_float2(m, s);
   __syncthreads();
-  m = sh[0];
-  s = sh[1];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) merge(m, s, sh[2 * i], sh[2 * i + 1], k);
+  if (threadIdx.x >= 32) return;
+  const float2 v = threadIdx.x < kWarps ? sh[threadIdx.x] : make_float2(kNegInf, 0.f);
+  m = v.x;
+  s = v.y;
+  warp_merge(m, s, k);
 }
 
 // ----------------------------------------------------------------------------- row passes
@@ -137,114 +240,198 @@ struct RowArgs {
   float grad_scale;
 };
 
+constexpr int kMaxCluster = 8;
+
+// (m, s) of the blocks of a cluster, by warp 0 of each.  Each block writes its
+// pair to all the others; `ready` counts one arrival from each.  The caller has
+// let the cluster arrive and wait after `ready` was set up, once; exchanges
+// alternate between two sets of slots, the n-th of a set on parity n & 1.  (A
+// block reaches the exchange after next only when every block has arrived at the
+// next one, so after it has read this one's slots.)  False: the wait ran out.
+struct ClusterSlots {
+  uint64_t ready;
+  float2 pair[kMaxCluster];
+};
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_dsmem_f2(const void *local_ptr, uint32_t cta, float2 v) {
+  uint32_t local = smem_u32(local_ptr), remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(cta));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int rank, int C, ClusterSlots *slots,
+                                              uint32_t parity) {
+  const int lane = lane_id();
+  if (lane < C) {
+    st_dsmem_f2(&slots->pair[rank], lane, make_float2(m, s));
+    mbar_arrive_remote(&slots->ready, lane);
+  }
+  if (!__all_sync(0xffffffffu, mbar_wait<true>(&slots->ready, parity))) return false;
+  const float2 v = lane < C ? slots->pair[lane] : make_float2(kNegInf, 0.f);
+  m = v.x;
+  s = v.y;
+  warp_merge(m, s, k);
+  return true;
+}
+
+// The statistics of a row, read once from global memory by the C blocks of a
+// cluster, a slice of `slice` 16-byte pieces each.
 template <typename E>
-__global__ void __launch_bounds__(kRowThreads) stats_kernel(RowArgs a) {
-  __shared__ float sh[2 * (kRowThreads / 32)];
+__global__ void __launch_bounds__(kRowThreads) stats_kernel(RowArgs a, int C, int slice) {
+  __shared__ float2 sh[kRowThreads / 32];
+  __shared__ ClusterSlots slots;
   pdl_wait();
-  const int64_t t = blockIdx.x;
-  if (threadIdx.x == 0) {
+  const int64_t t = blockIdx.x / C;
+  const int rank = (int)(blockIdx.x % C);
+  if (rank == 0 && threadIdx.x == 0) {
     if (a.coef) a.coef[t] = 0.f;
     if (a.ticket && t == 0) *a.ticket = 0;
   }
   const int64_t label = a.labels[t];
   if (label < 0 || label >= a.V) {
-    if (threadIdx.x == 0) {
+    if (rank == 0 && threadIdx.x == 0) {
       a.logps[t] = 0.f;
       if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
     }
     return;
   }
+  if (C > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(&slots.ready, C);
+      fence_barrier_init();
+    }
+    __syncthreads();
+    cluster_arrive();
+  }
   const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
-  const RowSpan<E> sp(row, a.V);
+  const RowSpan<E> sp(row, (int)a.V);
   const float k = a.inv_t * kLog2e;
-  float m = kNegInf, s = 0.f;
-  constexpr int N = Elem<E>::kVec;
-  if (threadIdx.x < sp.head) {
-    const float v = Elem<E>::load(row + threadIdx.x);
-    absorb<1>(m, s, &v, k);
-  }
-  const uint4 *body = reinterpret_cast<const uint4 *>(row + sp.head);
-  for (int64_t i = threadIdx.x; i < sp.vecs; i += kRowThreads) {
-    float v[N];
-    Elem<E>::unpack(body[i], v);
-    absorb<N>(m, s, v, k);
-  }
-  const int64_t tail = sp.head + sp.vecs * N;
-  if (tail + threadIdx.x < a.V) {
-    const float v = Elem<E>::load(row + tail + threadIdx.x);
-    absorb<1>(m, s, &v, k);
+  const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
+  float label_value = 0.f, m = kNegInf;
+  if (rank == 0 && threadIdx.x == 0) label_value = Elem<E>::load(row + label);
+  uint64_t s2 = 0;
+  absorb_span<E, kRowThreads>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
+  const float2 both = unpk2(s2);
+  float s = both.x + both.y;
+  if (rank == C - 1) {      // the ragged ends
+    if ((int)threadIdx.x < sp.head) absorb_one(m, s, Elem<E>::load(row + threadIdx.x), k);
+    if ((int)threadIdx.x < a.V - tail) absorb_one(m, s, Elem<E>::load(row + tail + threadIdx.x), k);
   }
   block_merge<kRowThreads / 32>(m, s, k, sh);
-  if (threadIdx.x == 0) {
-    a.logps[t] = (Elem<E>::load(row + label) - m) * a.inv_t - logf(s);
+  if (C > 1) {
+    cluster_wait();
+    if (threadIdx.x < 32 && !cluster_merge(m, s, k, rank, C, &slots, 0)) return;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    a.logps[t] = (label_value - m) * a.inv_t - logf(s);
     if (a.stats) a.stats[t] = make_float2(m, s);
   }
 }
 
+// Zeros over elements [from, to) of an output row.
+template <typename E, int kThreads>
+__device__ __forceinline__ void zero_span(E *out, int from, int to) {
+  E *o = out + from;
+  const int tid = threadIdx.x;
+  const RowSpan<E> so(o, to - from);
+  if (tid < so.head) Elem<E>::store(o + tid, 0.f);
+  uint4 *body = reinterpret_cast<uint4 *>(o + so.head);
+  for (int i = tid; i < so.vecs; i += kThreads) __stcs(body + i, make_uint4(0, 0, 0, 0));
+  if (tid < to - from - so.tail()) Elem<E>::store(o + so.tail() + tid, 0.f);
+}
+
+// A row's gradient d_v = c [v == label] + f exp(z_v - m), f = -c / S.
+struct RowGrad {
+  float m, k, c, f;
+  __device__ __forceinline__ float operator()(float v) const { return f * ex2((v - m) * k); }
+  // a 16-byte piece; `at`: the label's place relative to its first element
+  template <typename E>
+  __device__ __forceinline__ uint4 piece(const uint4 &q, int at) const {
+    constexpr int N = Elem<E>::kVec;
+    uint64_t v[N / 2];
+    Elem<E>::pairs(q, v);
+    const uint64_t m2 = pk2(-m, -m), k2 = pk2(k, k), f2 = pk2(f, f);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) v[j] = mul2(ex2_2(mul2(add2(v[j], m2), k2)), f2);
+    if (at >= 0 && at < N) {      // one piece of the row
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j)
+        v[j] = add2(v[j], pk2(at == 2 * j ? c : 0.f, at == 2 * j + 1 ? c : 0.f));
+    }
+    return Elem<E>::pack_pairs(v);
+  }
+};
+
+// Elements [e0, e1) of the output row where it sits at another offset to a
+// 16-byte boundary than the logits: 4-byte words of the output, their elements
+// read one by one (src: element i of the row at src[i]).
+template <typename E, int kThreads>
+__device__ __forceinline__ void grad_words(E *out, const E *src, int e0, int e1, int label, const RowGrad &g) {
+  auto one = [&](int i) { return g(Elem<E>::load(src + i)) + (i == label ? g.c : 0.f); };
+  const int tid = threadIdx.x;
+  if (sizeof(E) == 4) {
+#pragma unroll 4
+    for (int i = e0 + tid; i < e1; i += kThreads) Elem<E>::store(out + i, one(i));
+  } else {
+    const int w0 = e0 + (int)((reinterpret_cast<uintptr_t>(out + e0) >> 1) & 1);      // the first whole word
+    const int words = e1 > w0 ? (e1 - w0) / 2 : 0;
+#pragma unroll 4
+    for (int i = tid; i < words; i += kThreads)
+      __stcs(reinterpret_cast<unsigned *>(out + w0) + i, pack_bf16(one(w0 + 2 * i), one(w0 + 2 * i + 1)));
+    if (tid == 0 && w0 > e0 && e0 < e1) Elem<E>::store(out + e0, one(e0));
+    if (tid == 1 && w0 + 2 * words < e1) Elem<E>::store(out + e1 - 1, one(e1 - 1));
+  }
+}
+
+// The gradient from saved statistics: `parts` blocks a row, a slice of `slice`
+// 16-byte pieces each.  Rows go last to first: the pass over the logits before
+// this one has left its last rows in L2.
 template <typename E>
-__global__ void __launch_bounds__(kRowThreads) grad_kernel(RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads) grad_kernel(RowArgs a, int parts, int slice) {
   pdl_wait();
-  const int64_t t = blockIdx.x;
+  const int64_t t = a.T - 1 - blockIdx.x / parts;
+  const int rank = (int)(blockIdx.x % parts);
   const int64_t label = a.labels[t];
+  const float c = a.coef[t] * a.grad_scale * a.inv_t;
+  const float2 st = a.stats[t];
   E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
   const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
+  const RowSpan<E> sp(row, (int)a.V);
   constexpr int N = Elem<E>::kVec;
-  const float c = a.coef[t] * a.grad_scale * a.inv_t;
-  if (label < 0 || label >= a.V || c == 0.f) {
-    const RowSpan<E> so(out, a.V);
-    uint4 *body = reinterpret_cast<uint4 *>(out + so.head);
-    if (threadIdx.x < so.head) Elem<E>::store(out + threadIdx.x, 0.f);
-    for (int64_t i = threadIdx.x; i < so.vecs; i += kRowThreads) body[i] = make_uint4(0, 0, 0, 0);
-    const int64_t tail = so.head + so.vecs * N;
-    if (tail + threadIdx.x < a.V) Elem<E>::store(out + tail + threadIdx.x, 0.f);
+  const int tid = threadIdx.x, V = (int)a.V;
+  const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
+  const int e0 = rank == 0 ? 0 : sp.head + v0 * N, e1 = rank == parts - 1 ? V : sp.head + v1 * N;
+  if (label < 0 || label >= V || c == 0.f) {
+    zero_span<E, kRowThreads>(out, e0, e1);
     return;
   }
-  const float2 st = a.stats[t];
-  const float k = a.inv_t * kLog2e, m = st.x, q = -c / st.y;
-  const RowSpan<E> sp(row, a.V);
-  auto one = [&](int64_t i) {
-    const float d = q * ex2((Elem<E>::load(row + i) - m) * k);
-    Elem<E>::store(out + i, i == label ? d + c : d);
-  };
-  if (threadIdx.x < sp.head) one(threadIdx.x);
-  const uint4 *body = reinterpret_cast<const uint4 *>(row + sp.head);
-  const bool wide = (reinterpret_cast<uintptr_t>(out + sp.head) & 15u) == 0;
-  for (int64_t i = threadIdx.x; i < sp.vecs; i += kRowThreads) {
-    float v[N];
-    Elem<E>::unpack(body[i], v);
-    const int64_t first = sp.head + i * N;
+  const RowGrad g = {st.x, a.inv_t * kLog2e, c, -c / st.y};
+  const int mark = (int)label;
+  if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) != 0) {
+    grad_words<E, kRowThreads>(out, row, e0, e1, mark, g);
+    return;
+  }
+  const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
+  uint4 *dst = reinterpret_cast<uint4 *>(out + sp.head);
+  int i = v0 + tid;
+  for (; v1 - i > 3 * kRowThreads; i += 4 * kRowThreads) {
+    uint4 q[4];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      v[j] = q * ex2((v[j] - m) * k);
-      if (first + j == label) v[j] += c;
-    }
-    if (wide) {
-      *reinterpret_cast<uint4 *>(out + first) = Elem<E>::pack(v);
-    } else {
+    for (int u = 0; u < 4; ++u) q[u] = src[i + u * kRowThreads];
 #pragma unroll
-      for (int j = 0; j < N; ++j) Elem<E>::store(out + first + j, v[j]);
+    for (int u = 0; u < 4; ++u) {
+      const int j = i + u * kRowThreads;
+      __stcs(dst + j, g.piece<E>(q[u], mark - sp.head - j * N));
     }
   }
-  const int64_t tail = sp.head + sp.vecs * N;
-  if (tail + threadIdx.x < a.V) one(tail + threadIdx.x);
+  for (; i < v1; i += kRowThreads) __stcs(dst + i, g.piece<E>(src[i], mark - sp.head - i * N));
+  auto one = [&](int j) { Elem<E>::store(out + j, g(Elem<E>::load(row + j)) + (j == mark ? c : 0.f)); };
+  if (rank == 0 && tid < sp.head) one(tid);
+  if (rank == parts - 1 && tid < V - tail) one(tail + tid);
 }
 
 // ----------------------------------------------------------------------------- per-token steps
 constexpr int kPairThreads = 256;
-
-// Sum over the block in a fixed order, known to every thread.
-template <int kWarps>
-__device__ __forceinline__ double block_sum(double v, double *sh) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (lane_id() == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = sh[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) v += sh[i];
-  return v;
-}
 
 // ln sigmoid(h) = min(h, 0) - ln(1 + exp(-|h|)), free of overflow and of cancellation
 __device__ __forceinline__ float log_sigmoid(float h) { return fminf(h, 0.f) - log1pf(expf(-fabsf(h))); }
@@ -262,13 +449,13 @@ __device__ __forceinline__ bool last_block(unsigned *ticket, unsigned blocks) {
   return before == blocks - 1;
 }
 
-// One block per pair: both sequences' sums (in 64 bits: their difference is what
+// One block per pair: both sequences' sums (exact to fp32: their difference is what
 // counts), the pair's loss, and each token's d loss / d logp.  The last block
 // takes the mean.
 __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, int64_t T, int64_t V,
                                                              const int64_t *labels, const float *logps, float *coef,
                                                              unsigned *ticket) {
-  __shared__ double sh[kPairThreads / 32];
+  __shared__ Sum2 sh[kPairThreads / 32];
   pdl_wait();
   const int pair = blockIdx.x;
   int64_t lo[2], hi[2];
@@ -278,15 +465,15 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, i
     const int seq = pair + side * p.P;
     lo[side] = min(max((int64_t)p.cu[seq], (int64_t)0), T);
     hi[side] = min(max((int64_t)p.cu[seq + 1], (int64_t)0), T);
-    double sum = 0.0, count = 0.0;
-    for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) sum += logps[t];
+    Sum2 sum, count;
+    for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) sum.add(logps[t]);
     if (p.normalize)
       for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads)
-        count += labels[t] >= 0 && labels[t] < V ? 1.0 : 0.0;
+        count.add(labels[t] >= 0 && labels[t] < V ? 1.f : 0.f);
     sum = block_sum<kPairThreads / 32>(sum, sh);
     n[side] = 1.f;
-    if (p.normalize) n[side] = fmaxf(1.f, (float)block_sum<kPairThreads / 32>(count, sh));
-    S[side] = (float)(sum / n[side]);
+    if (p.normalize) n[side] = fmaxf(1.f, block_sum<kPairThreads / 32>(count, sh).value());
+    S[side] = sum.value() / n[side];
     if (threadIdx.x == 0) p.seq_logps[seq] = S[side];
   }
   float d = S[0] - S[1];
@@ -316,21 +503,28 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, i
   }
   if (threadIdx.x == 0) p.pair_loss[pair] = loss;
   if (last_block(ticket, gridDim.x)) {
-    double sum = 0.0;
-    for (int i = threadIdx.x; i < p.P; i += kPairThreads) sum += __ldcg(p.pair_loss + i);
+    Sum2 sum;
+    for (int i = threadIdx.x; i < p.P; i += kPairThreads) sum.add(__ldcg(p.pair_loss + i));
     sum = block_sum<kPairThreads / 32>(sum, sh);
-    if (threadIdx.x == 0) p.loss[0] = (float)(sum / p.P);
+    if (threadIdx.x == 0) p.loss[0] = sum.value() / (float)p.P;
   }
 }
 
 // A token's part of the policy loss: the terms of the three metrics, and its
 // d loss / d logp.
+struct PolicyRow {
+  float A, w, old, ref;
+};
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs &p, int64_t t) {
+  return {p.advantages[t], p.weights ? p.weights[t] : 1.f, p.old_logps ? p.old_logps[t] : 0.f,
+          p.ref_logps ? p.ref_logps[t] : 0.f};
+}
 struct PolicyTerm {
   float loss, kl, clipped, coef;
 };
-__device__ __forceinline__ PolicyTerm policy_term(const PolicyArgs &p, int64_t t, float logp) {
-  const float A = p.advantages[t], w = p.weights ? p.weights[t] : 1.f;
-  const float r = p.old_logps ? expf(logp - p.old_logps[t]) : expf(logp - logp);
+__device__ __forceinline__ PolicyTerm policy_term(const PolicyArgs &p, const PolicyRow &in, float logp) {
+  const float A = in.A, w = in.w;
+  const float r = expf(logp - (p.old_logps ? in.old : logp));
   const float hi = 1.f + p.clip_high, lo = 1.f - p.clip_low;
   const bool clipped = (A > 0.f && r > hi) || (A < 0.f && r < lo);
   float pg = -A * r, coef = -A * r;
@@ -340,63 +534,233 @@ __device__ __forceinline__ PolicyTerm policy_term(const PolicyArgs &p, int64_t t
   }
   float kl = 0.f;
   if (p.ref_logps) {
-    const float d = p.ref_logps[t] - logp, e = expm1f(d);
+    const float d = in.ref - logp, e = expm1f(d);
     kl = e - d;
     coef -= p.kl_beta * e;
   }
   return {w * (pg + p.kl_beta * kl), w * kl, clipped ? w : 0.f, w * coef};
 }
 
-// Sums of the blocks' three partial sums, in block order, by the last block.
-__device__ __forceinline__ void policy_finish(const double *part, int blocks, float *metrics) {
-  if (threadIdx.x < 3) {
-    double s = 0.0;
-    for (int i = 0; i < blocks; ++i) s += __ldcg(part + 3 * i + threadIdx.x);
-    metrics[threadIdx.x] = (float)s;
+// The policy loss where a row does not fit on chip: the terms and coefficients
+// from the log-probabilities of the stats pass.
+__global__ void __launch_bounds__(kPairThreads) tokens_kernel(PolicyArgs p, int64_t T, int64_t V,
+                                                              const int64_t *labels, const float *logps, float *coef,
+                                                              float4 *terms) {
+  pdl_wait();
+  const int64_t t = blockIdx.x * (int64_t)kPairThreads + threadIdx.x;
+  if (t >= T) return;
+  PolicyTerm x = {0.f, 0.f, 0.f, 0.f};
+  if (labels[t] >= 0 && labels[t] < V) x = policy_term(p, policy_row(p, t), logps[t]);
+  coef[t] = x.coef;
+  terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
+}
+
+// ----------------------------------------------------------------------------- a row held on chip
+// One row is read once: the C blocks of a cluster take a slice each, hold it in
+// shared memory, and share their (m, s) through each other's shared memory.  The
+// policy loss's coefficient needs that row only, so its gradient is formed from
+// the held slice and the row is never read again (2 N bytes instead of 3 N).
+// The clusters stay for row after row: while one row is summed and written, the
+// next one's slice is already on its way into the other of two buffers.
+constexpr int kHeldThreads = 256;
+constexpr int kHeldChunks = 2;          // copies of a slice, each with a barrier: work starts on the first
+constexpr int kBodyAt = 128;            // the slice's first 16-byte piece; the row's head sits right before it
+
+struct HeldArgs {
+  RowArgs r;
+  PolicyArgs p;
+  float4 *terms;       // loss, kl and clipped weight of each row
+  int cluster;
+  int slice;           // 16-byte pieces of a block at most
+  int buffer;          // bytes of one of the two buffers
+};
+
+// A block's slice of a row.
+template <typename E>
+struct HeldSlice {
+  const E *row;
+  int head, vecs, v0, nv;
+  __device__ __forceinline__ HeldSlice(const HeldArgs &h, int64_t t, int rank) {
+    row = static_cast<const E *>(h.r.logits) + t * h.r.ldl;
+    const RowSpan<E> sp(row, (int)h.r.V);
+    head = sp.head;
+    vecs = sp.vecs;
+    v0 = min(rank * h.slice, vecs);
+    nv = min(v0 + h.slice, vecs) - v0;
+  }
+  __device__ __forceinline__ int chunk(int q) const { return min(q * ((nv + kHeldChunks - 1) / kHeldChunks), nv); }
+  __device__ __forceinline__ void load(E *held, uint64_t *loaded) const {
+    const uint4 *src = reinterpret_cast<const uint4 *>(row + head) + v0;
+    for (int q = 0; q < kHeldChunks; ++q) {
+      const int from = chunk(q), n = chunk(q + 1) - from;
+      mbar_arrive_expect_tx(&loaded[q], n * 16);
+      if (n > 0) bulk_load(held + from * Elem<E>::kVec, src + from, n * 16, &loaded[q]);
+    }
+  }
+};
+
+template <typename E>
+__global__ void __launch_bounds__(kHeldThreads) held_kernel(HeldArgs h) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ uint64_t loaded[2][kHeldChunks];
+  __shared__ ClusterSlots slots[2];
+  __shared__ float2 sh[kHeldThreads / 32];
+  __shared__ RowGrad shared_grad;
+  __shared__ int failed;
+  const RowArgs &a = h.r;
+  constexpr int N = Elem<E>::kVec;
+  const int tid = threadIdx.x, C = h.cluster;
+  const int rank = (int)(blockIdx.x % C);
+  const int64_t clusters = gridDim.x / C;
+  if (tid == 0) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      for (int q = 0; q < kHeldChunks; ++q) mbar_init(&loaded[i][q], 1);
+      mbar_init(&slots[i].ready, C);
+    }
+    failed = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (C > 1) {                                        // every block's barriers stand before any is written to
+    cluster_arrive();
+    cluster_wait();
+  }
+  pdl_wait();
+  auto counts = [&](int64_t label) { return label >= 0 && label < a.V; };
+  auto held_of = [&](uint32_t seq) { return reinterpret_cast<E *>(smem + (seq & 1) * h.buffer + kBodyAt); };
+  int64_t t = blockIdx.x / C;
+  int64_t label = t < a.T ? a.labels[t] : -1, label1 = t + clusters < a.T ? a.labels[t + clusters] : -1;
+  uint32_t seq = 0;                                   // rows that this block has held
+  if (tid == 0 && counts(label)) HeldSlice<E>(h, t, rank).load(held_of(0), loaded[0]);
+  for (; t < a.T; t += clusters) {
+    const int64_t now = label, t1 = t + clusters, t2 = t1 + clusters;
+    label = label1;
+    label1 = t2 < a.T ? a.labels[t2] : -1;
+    const bool valid = counts(now), next = counts(label);
+    const uint32_t other = seq + (valid ? 1 : 0);     // the next held row's number
+    __syncthreads();                                  // no thread reads the other buffer any more
+    if (tid == 0 && next) HeldSlice<E>(h, t1, rank).load(held_of(other), loaded[other & 1]);
+    const HeldSlice<E> sl(h, t, rank);
+    E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
+    const int nv = sl.nv, V = (int)a.V;
+    // the block's elements [e0, e1): the first block has the head, the last one the tail
+    const int tail = sl.head + sl.vecs * N;
+    const int e0 = rank == 0 ? 0 : sl.head + sl.v0 * N, e1 = rank == C - 1 ? V : sl.head + (sl.v0 + nv) * N;
+    if (!valid) {
+      if (rank == 0 && tid == 0) {
+        a.logps[t] = 0.f;
+        h.terms[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (a.dlogits) zero_span<E, kHeldThreads>(out, e0, e1);
+      continue;
+    }
+    const int mark = (int)now;
+    PolicyRow in = {0.f, 0.f, 0.f, 0.f};
+    float picked = 0.f;
+    if (tid == 0) {                                   // on their way while the row is summed
+      in = policy_row(h.p, t);
+      picked = Elem<E>::load(sl.row + mark);
+    }
+    // the ragged ends, at most seven elements each, beside the slice
+    E *held = held_of(seq);                           // element i of the row at held[i - head - v0 * N]
+    float edge = kNegInf;
+    const bool at_head = rank == 0 && tid < sl.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
+    const int edge_at = at_head ? tid : tail + tid - 16;
+    if (at_head || at_tail) {
+      edge = Elem<E>::load(sl.row + edge_at);
+      Elem<E>::store(at_head ? held - sl.head + tid : held + nv * N + tid - 16, edge);
+      fence_proxy_async_smem();                       // a later copy may land on the tail's place
+    }
+
+    const float k = a.inv_t * kLog2e;
+    float m = kNegInf;
+    uint64_t s2 = 0;
+    const uint4 *body = reinterpret_cast<const uint4 *>(held);
+    const uint32_t set = seq & 1, parity = (seq >> 1) & 1;
+    for (int q = 0; q < kHeldChunks; ++q) {
+      if (!mbar_wait(&loaded[set][q], parity)) failed = 1;
+      absorb_span<E, kHeldThreads>(m, s2, body, sl.chunk(q), sl.chunk(q + 1), k);
+    }
+    const float2 both = unpk2(s2);
+    float s = both.x + both.y;
+    if (edge != kNegInf) absorb_one(m, s, edge, k);
+    block_merge<kHeldThreads / 32>(m, s, k, sh);
+    if (tid < 32) {                                   // one warp finishes the row for the block
+      if (C > 1 && !cluster_merge(m, s, k, rank, C, &slots[set], parity)) failed = 1;
+      if (tid == 0) {
+        const float logp = (picked - m) * a.inv_t - logf(s);
+        const PolicyTerm x = policy_term(h.p, in, logp);
+        const float c = x.coef * a.grad_scale * a.inv_t;
+        shared_grad = {m, k, c, -c / s};
+        if (rank == 0) {
+          a.logps[t] = logp;
+          h.terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
+        }
+      }
+    }
+    __syncthreads();
+    if (failed) {                                     // a wait ran out: the error word is set
+      if (next)
+        for (int q = 0; q < kHeldChunks; ++q) mbar_wait(&loaded[other & 1][q], (other >> 1) & 1);
+      return;
+    }
+    ++seq;
+    if (a.dlogits == nullptr) continue;
+    const RowGrad g = shared_grad;
+    if (g.c == 0.f) {
+      zero_span<E, kHeldThreads>(out, e0, e1);
+    } else if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0) {
+      uint4 *dst = reinterpret_cast<uint4 *>(out + sl.head) + sl.v0;
+      const int at = mark - sl.head - sl.v0 * N;      // the label within the slice
+#pragma unroll 4
+      for (int i = tid; i < nv; i += kHeldThreads) __stcs(dst + i, g.piece<E>(body[i], at - i * N));
+      if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge) + (edge_at == mark ? g.c : 0.f));
+    } else {
+      grad_words<E, kHeldThreads>(out, held - sl.head - sl.v0 * N, e0, e1, mark, g);
+    }
   }
 }
 
-__global__ void __launch_bounds__(kPairThreads) tokens_kernel(PolicyArgs p, int64_t T, int64_t V,
-                                                              const int64_t *labels, const float *logps, float *coef,
-                                                              double *part, unsigned *ticket) {
-  __shared__ double sh[kPairThreads / 32];
+// The three metrics: sums of the rows' terms in a fixed order.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) terms_kernel(const float4 *terms, int64_t T, float *metrics) {
+  __shared__ Sum2 sh[kSumThreads / 32];
   pdl_wait();
-  double s[3] = {0.0, 0.0, 0.0};
-  const int64_t t = blockIdx.x * (int64_t)kPairThreads + threadIdx.x;
-  if (t < T && labels[t] >= 0 && labels[t] < V) {
-    const PolicyTerm x = policy_term(p, t, logps[t]);
-    if (coef) coef[t] = x.coef;
-    s[0] = x.loss;
-    s[1] = x.kl;
-    s[2] = x.clipped;
+  Sum2 s[3];
+#pragma unroll 4
+  for (int64_t t = threadIdx.x; t < T; t += kSumThreads) {
+    const float4 v = terms[t];
+    s[0].add(v.x);
+    s[1].add(v.y);
+    s[2].add(v.z);
   }
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    s[i] = block_sum<kPairThreads / 32>(s[i], sh);
-    if (threadIdx.x == 0) part[3 * (int64_t)blockIdx.x + i] = s[i];
+    const Sum2 all = block_sum<kSumThreads / 32>(s[i], sh);
+    if (threadIdx.x == 0) metrics[i] = all.value();
   }
-  if (last_block(ticket, gridDim.x)) policy_finish(part, gridDim.x, p.metrics);
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kRowThreads) scale_kernel(E *x, int64_t ldx, int64_t V, const float *factor) {
+__global__ void __launch_bounds__(kRowThreads) scale_kernel(E *x, int64_t ldx, int V, const float *factor) {
   pdl_wait();
   const float f = *factor;
   if (f == 1.f) return;
   E *row = x + (int64_t)blockIdx.x * ldx;
   const RowSpan<E> sp(row, V);
   constexpr int N = Elem<E>::kVec;
-  if (threadIdx.x < sp.head) Elem<E>::store(row + threadIdx.x, Elem<E>::load(row + threadIdx.x) * f);
+  const int tid = threadIdx.x, tail = sp.tail();
+  if (tid < sp.head) Elem<E>::store(row + tid, Elem<E>::load(row + tid) * f);
   uint4 *body = reinterpret_cast<uint4 *>(row + sp.head);
-  for (int64_t i = threadIdx.x; i < sp.vecs; i += kRowThreads) {
+  for (int i = tid; i < sp.vecs; i += kRowThreads) {
     float v[N];
     Elem<E>::unpack(body[i], v);
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] *= f;
     body[i] = Elem<E>::pack(v);
   }
-  const int64_t tail = sp.head + sp.vecs * N;
-  if (tail + threadIdx.x < V) Elem<E>::store(row + tail + threadIdx.x, Elem<E>::load(row + tail + threadIdx.x) * f);
+  if (tid < V - tail) Elem<E>::store(row + tail + tid, Elem<E>::load(row + tail + tid) * f);
 }
 
 RowArgs row_args(const LossArgs &a) {
@@ -414,21 +778,97 @@ RowArgs row_args(const LossArgs &a) {
   return r;
 }
 
+// How a row is cut for the held kernel.  Slices of 32 KB keep three blocks on an
+// SM (two buffers each); few rows are cut finer, down to 4 KB a block, until the
+// grid covers the SMs twice.  A row whose slice does not fit a buffer at eight
+// blocks (cluster 0) goes by the two-pass kernels.
+constexpr int kHeldSmem = 220 << 10;
+struct HeldPlan {
+  int cluster, slice, buffer;
+};
+HeldPlan plan_held(lora_dtype_t dtype, int64_t T, int64_t V) {
+  const int64_t e = dtype == LORA_BF16 ? 2 : 4, bytes = V * e;
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, 32 << 10));
+  c = std::max(c, std::min(ceil_div(2 * num_sms(), std::max<int64_t>(T, 1)), bytes / 4096));
+  c = std::min<int64_t>(c, kMaxCluster);
+  const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
+  const int64_t buffer = kBodyAt + 16 * slice + 128;      // the tail behind the slice, the next buffer on 128 bytes
+  if (2 * buffer > kHeldSmem) return {0, 0, 0};
+  return {(int)c, (int)slice, (int)buffer};
+}
+
+// Clusters of a kernel that the device holds at once; the last answers are kept.
+int max_clusters(const void *kernel, int cluster, int smem) {
+  struct Known {
+    const void *kernel;
+    int dev, cluster, smem, n;
+  };
+  static Known known[32];
+  static int used = 0;
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known &k : known)
+    if (k.n > 0 && k.kernel == kernel && k.dev == dev && k.cluster == cluster && k.smem == smem) return k.n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(kHeldThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+  known[used++ % 32] = {kernel, dev, cluster, smem, n};
+  return n;
+}
+
+template <typename E>
+cudaError_t launch_held(const HeldArgs &h, cudaStream_t st) {
+  const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
+  const int smem = 2 * h.buffer;
+  cudaError_t e = ensure_smem(kernel, kHeldSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t clusters = std::min<int64_t>(h.r.T, max_clusters(kernel, h.cluster, smem));
+  return launch(held_kernel<E>, dim3((unsigned)(clusters * h.cluster)), dim3(kHeldThreads), smem, st, h.cluster, true, h);
+}
+
+// Blocks for each row of a pass from global memory: enough that the grid fills
+// the SMs (eight blocks each) some eight times over, so that the last blocks to
+// run leave few SMs idle, with at least 16 KB a block; few rows are cut down to
+// 4 KB a block until the grid fills the SMs once.
+int parts_of(lora_dtype_t dtype, int64_t T, int64_t V, int most) {
+  const int64_t bytes = V * (dtype == LORA_BF16 ? 2 : 4), once = 8 * (int64_t)num_sms();
+  int64_t c = std::min(ceil_div(8 * once, T), bytes / (16 << 10));
+  c = std::max(c, std::min(ceil_div(once, T), bytes / (4 << 10)));
+  return (int)std::min<int64_t>(std::max<int64_t>(c, 1), most);
+}
+int slice_of(lora_dtype_t dtype, int64_t V, int parts) {
+  const int64_t pieces = V * (dtype == LORA_BF16 ? 2 : 4) / 16;
+  return (int)std::max<int64_t>(8, round_up(ceil_div(pieces, parts), 8));
+}
+
 lora_status_t run_stats(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0) return LORA_OK;
-  if (dtype == LORA_BF16)
-    LORA_CUDA(launch(stats_kernel<__nv_bfloat16>, dim3((unsigned)r.T), dim3(kRowThreads), 0, st, 1, true, r));
-  else
-    LORA_CUDA(launch(stats_kernel<float>, dim3((unsigned)r.T), dim3(kRowThreads), 0, st, 1, true, r));
+  const int c = parts_of(dtype, r.T, r.V, kMaxCluster);
+  const int slice = slice_of(dtype, r.V, c);
+  const dim3 grid((unsigned)(r.T * c)), block(kRowThreads);
+  LORA_CUDA(dtype == LORA_BF16 ? launch(stats_kernel<__nv_bfloat16>, grid, block, 0, st, c, true, r, c, slice)
+                               : launch(stats_kernel<float>, grid, block, 0, st, c, true, r, c, slice));
   return LORA_OK;
 }
 
 lora_status_t run_grad(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0 || r.V == 0) return LORA_OK;
-  if (dtype == LORA_BF16)
-    LORA_CUDA(launch(grad_kernel<__nv_bfloat16>, dim3((unsigned)r.T), dim3(kRowThreads), 0, st, 1, true, r));
-  else
-    LORA_CUDA(launch(grad_kernel<float>, dim3((unsigned)r.T), dim3(kRowThreads), 0, st, 1, true, r));
+  const int c = parts_of(dtype, r.T, r.V, 64);
+  const int slice = slice_of(dtype, r.V, c);
+  const dim3 grid((unsigned)(r.T * c)), block(kRowThreads);
+  LORA_CUDA(dtype == LORA_BF16 ? launch(grad_kernel<__nv_bfloat16>, grid, block, 0, st, 1, true, r, c, slice)
+                               : launch(grad_kernel<float>, grid, block, 0, st, 1, true, r, c, slice));
   return LORA_OK;
 }
 
@@ -438,8 +878,12 @@ int64_t token_blocks(int64_t T) { return ceil_div(T, kPairThreads); }
 
 // ----------------------------------------------------------------------------- host side
 size_t preference_ws_bytes(int64_t T, int64_t) { return ws_round(8 * T) + ws_round(4 * T) + ws_round(4); }
-size_t policy_ws_bytes(int64_t T) {
-  return ws_round(8 * T) + ws_round(4 * T) + ws_round(4) + ws_round(24 * token_blocks(T));
+size_t policy_ws_bytes(int64_t T) { return ws_round(16 * T) + ws_round(8 * T) + ws_round(4 * T); }
+int read_clear_error_loss() {
+  int v = 0, z = 0;
+  if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return -1;
+  if (v) cudaMemcpyToSymbol(g_device_error, &z, sizeof(int));
+  return v;
 }
 
 lora_status_t token_logps(const LossArgs &a, float *stats, cudaStream_t st) {
@@ -485,16 +929,22 @@ lora_status_t policy_loss(const LossArgs &a, const PolicyArgs &p, void *ws, size
   }
   WsCarver c(ws, ws_bytes);
   RowArgs r = row_args(a);
+  float4 *terms = static_cast<float4 *>(c.take(16 * a.T));
   r.stats = static_cast<float2 *>(c.take(8 * a.T));
   r.coef = static_cast<float *>(c.take(4 * a.T));
-  r.ticket = static_cast<unsigned *>(c.take(4));
-  const int64_t blocks = token_blocks(a.T);
-  double *part = static_cast<double *>(c.take(24 * blocks));
-  if (part == nullptr) return LORA_ERR_WORKSPACE;
-  LORA_TRY(run_stats(a.dtype, r, st));
-  LORA_CUDA(launch(tokens_kernel, dim3((unsigned)blocks), dim3(kPairThreads), 0, st, 1, true, p, a.T, a.V, a.labels,
-                   (const float *)a.logps, a.dlogits ? r.coef : (float *)nullptr, part, r.ticket));
-  return a.dlogits ? run_grad(a.dtype, r, st) : LORA_OK;
+  if (r.coef == nullptr) return LORA_ERR_WORKSPACE;
+  const HeldPlan hp = plan_held(a.dtype, a.T, a.V);
+  if (hp.cluster > 0) {
+    const HeldArgs h = {r, p, terms, hp.cluster, hp.slice, hp.buffer};
+    LORA_CUDA(a.dtype == LORA_BF16 ? launch_held<__nv_bfloat16>(h, st) : launch_held<float>(h, st));
+  } else {
+    LORA_TRY(run_stats(a.dtype, r, st));
+    LORA_CUDA(launch(tokens_kernel, dim3((unsigned)token_blocks(a.T)), dim3(kPairThreads), 0, st, 1, true, p, a.T, a.V,
+                     a.labels, (const float *)a.logps, r.coef, terms));
+    if (a.dlogits) LORA_TRY(run_grad(a.dtype, r, st));
+  }
+  LORA_CUDA(launch(terms_kernel, dim3(1), dim3(kSumThreads), 0, st, 1, true, (const float4 *)terms, a.T, p.metrics));
+  return LORA_OK;
 }
 
 lora_status_t scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void *x, int64_t ldx, const float *factor,
@@ -502,9 +952,9 @@ lora_status_t scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void *x, 
   if (T == 0 || V == 0) return LORA_OK;
   if (dtype == LORA_BF16)
     LORA_CUDA(launch(scale_kernel<__nv_bfloat16>, dim3((unsigned)T), dim3(kRowThreads), 0, st, 1, true,
-                     (__nv_bfloat16 *)x, ldx, V, factor));
+                     (__nv_bfloat16 *)x, ldx, (int)V, factor));
   else
-    LORA_CUDA(launch(scale_kernel<float>, dim3((unsigned)T), dim3(kRowThreads), 0, st, 1, true, (float *)x, ldx, V,
+    LORA_CUDA(launch(scale_kernel<float>, dim3((unsigned)T), dim3(kRowThreads), 0, st, 1, true, (float *)x, ldx, (int)V,
                      factor));
   return LORA_OK;
 }

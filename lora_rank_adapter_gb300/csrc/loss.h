@@ -37,6 +37,9 @@ struct PolicyArgs {
   float *metrics;         // [3]
 };
 
+// Reads and clears the error word of the waits in loss.cu (-1: the read failed).
+int read_clear_error_loss();
+
 size_t preference_ws_bytes(int64_t T, int64_t P);
 size_t policy_ws_bytes(int64_t T);
 

@@ -11,6 +11,7 @@ namespace lora {
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
+constexpr int64_t kMaxVocab = (int64_t)1 << 30;      // places within a row are 32-bit ints in the kernels
 
 bool size_ok(int64_t v) { return v >= 0 && v < kMaxDim; }
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -33,6 +34,7 @@ lora_status_t check_rows(lora_dtype_t dtype, int64_t T, int64_t V, const void *l
                          const int64_t *labels, float temperature, const void *dlogits, int64_t lddl) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_UNSUPPORTED;
   if (!size_ok(T) || !size_ok(V)) return LORA_ERR_INVALID_ARG;
+  if (V > kMaxVocab) return LORA_ERR_UNSUPPORTED;
   if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature)) return LORA_ERR_INVALID_ARG;
   const int e = dtype == LORA_BF16 ? 2 : 4;
   if (T > 0 && V > 0) {
@@ -168,6 +170,7 @@ lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void
                                   const float *factor, void *stream) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_UNSUPPORTED;
   if (!size_ok(T) || !size_ok(V)) return LORA_ERR_INVALID_ARG;
+  if (V > kMaxVocab) return LORA_ERR_UNSUPPORTED;
   if (T == 0 || V == 0) return LORA_OK;
   if (ldx < V) return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_ptr(x, 1, dtype == LORA_BF16 ? 2 : 4));

@@ -21,7 +21,7 @@ import ctypes
 import torch
 
 from . import binding
-from .binding import _check, _dtype, _ptr, _stream, _ws_args
+from .binding import _check, _dtype
 
 TRAIN_EXPORTS = ["lora_train_workspace_size", "lora_token_logps", "lora_token_logps_backward",
                  "lora_preference_loss", "lora_policy_loss", "lora_scale_gradient", "lora_adamw_table_size",
@@ -86,40 +86,50 @@ def lib():
     return L
 
 
-def _expect(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def _vector(t, n, dtype, name, device):
-    """A contiguous vector of n elements on the logits' device."""
-    _expect(t.dtype == dtype and t.device == device, f"{name} has to be {dtype} on {device}")
-    _expect(t.numel() == n and t.is_contiguous(), f"{name} has to hold {n} contiguous elements")
-    return t
+    """The address of a contiguous tensor of n elements on `device`."""
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} has to be {dtype} on {device}, not {t.dtype} on {t.device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} has to hold {n} contiguous elements")
+    return t.data_ptr()
+
+
+def _optional(t, n, dtype, name, device):
+    return None if t is None else _vector(t, n, dtype, name, device)
+
+
+def _matrix(x, name):
+    """(rows, columns, address, row stride) of a [T, V] tensor with unit column stride."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} have to be [T, V]")
+    if not x.is_cuda:
+        raise ValueError(f"{name} have to be on a GPU")
+    T, V = x.shape
+    ld, unit = x.stride()
+    if unit != 1 and V > 1 and T > 0:
+        raise ValueError(f"{name} need unit column stride")
+    return T, V, x.data_ptr(), ld if T > 1 else max(V, 1)
 
 
 def _rows(logits, labels):
-    _expect(logits.dim() == 2, "logits have to be [T, V]")
-    _expect(logits.is_cuda, "logits have to be on a GPU")
-    T, V = logits.shape
-    _expect(V <= 1 or T == 0 or logits.stride(1) == 1, "logits need unit column stride")
-    _vector(labels, T, torch.int64, "labels", logits.device)
-    return T, V
-
-
-def _ld(t):
-    """Row stride of a [T, V] tensor (of one row: any that fits)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    T, V, x, ld = _matrix(logits, "logits")
+    device = logits.device
+    return T, V, x, ld, _vector(labels, T, torch.int64, "labels", device), device
 
 
 def _gradient(dlogits, logits):
+    """(address, row stride) of the gradient of the logits."""
     if dlogits is None:
         return None, 0
-    _expect(dlogits.shape == logits.shape and dlogits.dtype == logits.dtype and dlogits.device == logits.device,
-            "dlogits have to be like the logits")
-    _expect(dlogits.shape[1] <= 1 or dlogits.shape[0] == 0 or dlogits.stride(1) == 1,
-            "dlogits need unit column stride")
-    return dlogits, _ld(dlogits)
+    if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or dlogits.device != logits.device:
+        raise ValueError("dlogits have to be like the logits")
+    return _matrix(dlogits, "dlogits")[2:]
+
+
+def _raw_stream(stream, device):
+    """The address of the given stream, or of the device's current one."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def train_workspace(op, n, pairs=0, device="cuda", stream=None):
@@ -134,16 +144,20 @@ def train_workspace(op, n, pairs=0, device="cuda", stream=None):
     return ws
 
 
+def _workspace(ws, op, n, pairs, device, stream):
+    if ws is None:
+        ws = train_workspace(op, n, pairs, device, stream)
+    return ws, (0 if ws is None else ws.data_ptr()), (0 if ws is None else ws.numel())
+
+
 # ----------------------------------------------------------------------------- log-probabilities and losses
 def lora_token_logps(logits, labels, logps, temperature=1.0, stats=None, stream=None):
     """logps[t] = log_softmax(logits[t] / temperature)[labels[t]] (fp32; 0 where the
     label is outside [0, V)).  stats: fp32 [T, 2] for lora_token_logps_backward."""
-    T, V = _rows(logits, labels)
-    _vector(logps, T, torch.float32, "logps", logits.device)
-    if stats is not None:
-        _vector(stats, 2 * T, torch.float32, "stats", logits.device)
-    st = lib().lora_token_logps(_dtype(logits), T, V, _ptr(logits), _ld(logits), _ptr(labels), float(temperature),
-                                _ptr(logps), _ptr(stats), _stream(stream))
+    T, V, x, ld, lab, dev = _rows(logits, labels)
+    f32 = torch.float32
+    st = lib().lora_token_logps(_dtype(logits), T, V, x, ld, lab, temperature, _vector(logps, T, f32, "logps", dev),
+                                _optional(stats, 2 * T, f32, "stats", dev), _raw_stream(stream, dev))
     _check(st, "lora_token_logps")
     return logps
 
@@ -151,14 +165,14 @@ def lora_token_logps(logits, labels, logps, temperature=1.0, stats=None, stream=
 def lora_token_logps_backward(logits, labels, stats, dlogps, dlogits, temperature=1.0, stream=None):
     """dlogits of lora_token_logps from its stats and the log-probabilities' gradient
     dlogps (fp32 [T]); dlogits may be the logits themselves."""
-    T, V = _rows(logits, labels)
-    _vector(stats, 2 * T, torch.float32, "stats", logits.device)
-    _vector(dlogps, T, torch.float32, "dlogps", logits.device)
-    _expect(dlogits is not None, "dlogits are missing")
-    dlogits, ldd = _gradient(dlogits, logits)
-    st = lib().lora_token_logps_backward(_dtype(logits), T, V, _ptr(logits), _ld(logits), _ptr(labels),
-                                         float(temperature), _ptr(stats), _ptr(dlogps), _ptr(dlogits), ldd,
-                                         _stream(stream))
+    T, V, x, ld, lab, dev = _rows(logits, labels)
+    f32 = torch.float32
+    if dlogits is None:
+        raise ValueError("dlogits are missing")
+    d, ldd = _gradient(dlogits, logits)
+    st = lib().lora_token_logps_backward(_dtype(logits), T, V, x, ld, lab, temperature,
+                                         _vector(stats, 2 * T, f32, "stats", dev),
+                                         _vector(dlogps, T, f32, "dlogps", dev), d, ldd, _raw_stream(stream, dev))
     _check(st, "lora_token_logps_backward")
     return dlogits
 
@@ -169,27 +183,24 @@ def lora_preference_loss(logits, labels, cu_seqlens, ref_logps, beta, token_logp
     """The paired log-ratio loss over packed sequences (int32 cu_seqlens [2P + 1]; pair p
     prefers sequence p to sequence P + p); with dlogits also its gradient.  ref_logps
     [2P] or None; token_logps [T], seq_logps [2P], pair_loss [P] and loss [1] are written."""
-    T, V = _rows(logits, labels)
-    dev = logits.device
-    _expect(kind in PREFERENCE_KINDS, f"kind has to be one of {sorted(PREFERENCE_KINDS)}")
-    _expect(cu_seqlens.numel() % 2 == 1, "cu_seqlens have to hold 2 P + 1 offsets")
-    P = cu_seqlens.numel() // 2
-    _vector(cu_seqlens, 2 * P + 1, torch.int32, "cu_seqlens", dev)
-    if ref_logps is not None:
-        _vector(ref_logps, 2 * P, torch.float32, "ref_logps", dev)
-    _vector(token_logps, T, torch.float32, "token_logps", dev)
-    _vector(seq_logps, 2 * P, torch.float32, "seq_logps", dev)
-    _vector(pair_loss, P, torch.float32, "pair_loss", dev)
-    _vector(loss, 1, torch.float32, "loss", dev)
-    dlogits, ldd = _gradient(dlogits, logits)
-    if ws is None:
-        ws = train_workspace(TRAIN_PREFERENCE_LOSS, T, P, dev, stream)
-    st = lib().lora_preference_loss(_dtype(logits), T, V, P, _ptr(logits), _ld(logits), _ptr(labels),
-                                    _ptr(cu_seqlens), _ptr(ref_logps), PREFERENCE_KINDS[kind], float(beta),
-                                    float(label_smoothing), PREF_LENGTH_NORMALIZE if length_normalize else 0,
-                                    float(temperature), _ptr(token_logps), _ptr(seq_logps), _ptr(pair_loss),
-                                    _ptr(loss), _ptr(dlogits), ldd, float(grad_scale), *_ws_args(ws),
-                                    _stream(stream))
+    T, V, x, ld, lab, dev = _rows(logits, labels)
+    f32 = torch.float32
+    if kind not in PREFERENCE_KINDS:
+        raise ValueError(f"kind has to be one of {sorted(PREFERENCE_KINDS)}")
+    n = cu_seqlens.numel()
+    if n % 2 != 1:
+        raise ValueError("cu_seqlens have to hold 2 P + 1 offsets")
+    P = n // 2
+    d, ldd = _gradient(dlogits, logits)
+    ws, w, wn = _workspace(ws, TRAIN_PREFERENCE_LOSS, T, P, dev, stream)
+    st = lib().lora_preference_loss(_dtype(logits), T, V, P, x, ld, lab,
+                                    _vector(cu_seqlens, n, torch.int32, "cu_seqlens", dev),
+                                    _optional(ref_logps, 2 * P, f32, "ref_logps", dev), PREFERENCE_KINDS[kind], beta,
+                                    label_smoothing, PREF_LENGTH_NORMALIZE if length_normalize else 0, temperature,
+                                    _vector(token_logps, T, f32, "token_logps", dev),
+                                    _vector(seq_logps, 2 * P, f32, "seq_logps", dev),
+                                    _vector(pair_loss, P, f32, "pair_loss", dev), _vector(loss, 1, f32, "loss", dev),
+                                    d, ldd, grad_scale, w, wn, _raw_stream(stream, dev))
     _check(st, "lora_preference_loss")
     return loss
 
@@ -200,31 +211,26 @@ def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps
     """The clipped policy loss with a KL term, summed with the tokens' weights (None: 1);
     with dlogits also its gradient.  old_logps, ref_logps: fp32 [T] or None.  token_logps
     [T] and metrics [3] (loss, weighted KL, weight of the clipped tokens) are written."""
-    T, V = _rows(logits, labels)
-    dev = logits.device
-    for name, t in (("old_logps", old_logps), ("ref_logps", ref_logps), ("weights", weights)):
-        if t is not None:
-            _vector(t, T, torch.float32, name, dev)
-    _vector(advantages, T, torch.float32, "advantages", dev)
-    _vector(token_logps, T, torch.float32, "token_logps", dev)
-    _vector(metrics, 3, torch.float32, "metrics", dev)
-    dlogits, ldd = _gradient(dlogits, logits)
-    if ws is None:
-        ws = train_workspace(TRAIN_POLICY_LOSS, T, 0, dev, stream)
-    st = lib().lora_policy_loss(_dtype(logits), T, V, _ptr(logits), _ld(logits), _ptr(labels), _ptr(old_logps),
-                                _ptr(ref_logps), _ptr(advantages), _ptr(weights), float(clip_low), float(clip_high),
-                                float(kl_beta), float(temperature), _ptr(token_logps), _ptr(metrics), _ptr(dlogits),
-                                ldd, float(grad_scale), *_ws_args(ws), _stream(stream))
+    T, V, x, ld, lab, dev = _rows(logits, labels)
+    f32 = torch.float32
+    d, ldd = _gradient(dlogits, logits)
+    ws, w, wn = _workspace(ws, TRAIN_POLICY_LOSS, T, 0, dev, stream)
+    st = lib().lora_policy_loss(_dtype(logits), T, V, x, ld, lab, _optional(old_logps, T, f32, "old_logps", dev),
+                                _optional(ref_logps, T, f32, "ref_logps", dev),
+                                _vector(advantages, T, f32, "advantages", dev),
+                                _optional(weights, T, f32, "weights", dev), clip_low, clip_high, kl_beta, temperature,
+                                _vector(token_logps, T, f32, "token_logps", dev),
+                                _vector(metrics, 3, f32, "metrics", dev), d, ldd, grad_scale, w, wn,
+                                _raw_stream(stream, dev))
     _check(st, "lora_policy_loss")
     return metrics
 
 
 def lora_scale_gradient(x, factor, stream=None):
     """x *= factor (fp32 device scalar) in place for a [T, V] gradient; no pass over x when it is 1."""
-    _expect(x.dim() == 2 and x.is_cuda and (x.shape[1] <= 1 or x.shape[0] == 0 or x.stride(1) == 1),
-            "x has to be [T, V] on a GPU with unit column stride")
-    _vector(factor, 1, torch.float32, "factor", x.device)
-    st = lib().lora_scale_gradient(_dtype(x), x.shape[0], x.shape[1], _ptr(x), _ld(x), _ptr(factor), _stream(stream))
+    T, V, p, ld = _matrix(x, "gradients")
+    st = lib().lora_scale_gradient(_dtype(x), T, V, p, ld, _vector(factor, 1, torch.float32, "factor", x.device),
+                                   _raw_stream(stream, x.device))
     _check(st, "lora_scale_gradient")
     return x
 
@@ -237,10 +243,12 @@ class AdamWPlan:
     def __init__(self, struct, table, tensors):
         self.struct, self.table, self.tensors = struct, table, tensors
         self.ref = ctypes.byref(struct)
+        self.device, self.chunks = table.device, int(struct.chunks)
 
-    @property
-    def chunks(self):
-        return self.struct.chunks
+
+def _expect(ok, what):
+    if not ok:
+        raise ValueError(what)
 
 
 def _dense(t):
@@ -284,9 +292,10 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
                 continue
             t = lists[name][i]
             allowed = allowed or (grads[0].dtype,)
-            _expect(t.dtype in allowed and t.device == device, f"{name}[{i}] has to be {allowed[0]} on {device}")
-            _expect(t.shape == p.shape and (t.stride() == p.stride() or (t.is_contiguous() and p.is_contiguous())),
-                    f"{name}[{i}] has to have its parameter's shape and strides")
+            if t.dtype not in allowed or t.device != device:
+                raise ValueError(f"{name}[{i}] has to be {allowed[0]} on {device}")
+            if t.shape != p.shape or not (t.stride() == p.stride() or (t.is_contiguous() and p.is_contiguous())):
+                raise ValueError(f"{name}[{i}] has to have its parameter's shape and strides")
         for name in ("exp_avg_scales", "exp_avg_sq_scales"):
             if s8:
                 _vector(lists[name][i], -(-p.numel() // ADAMW_BLOCK), torch.float32, name, device)
@@ -300,18 +309,17 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
         table.record_stream(stream)
     struct = AdamWPlanStruct()
     st = lib().lora_adamw_build(table_in, n, _dtype(params[0]) if n else binding.LORA_F32,
-                                _dtype(grads[0]) if n else binding.LORA_F32, flags, _ptr(table), table.numel(),
-                                ctypes.byref(struct), _stream(stream))
+                                _dtype(grads[0]) if n else binding.LORA_F32, flags, table.data_ptr(), table.numel(),
+                                ctypes.byref(struct), _raw_stream(stream, device))
     _check(st, "lora_adamw_build")
     return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}))
 
 
 def lora_grad_norm(plan, max_norm, out, ws=None, stream=None):
     """out[0] = the 2-norm of all gradients, out[1] = min(1, max_norm / (norm + 1e-6)) (fp32 [2])."""
-    _vector(out, 2, torch.float32, "out", plan.table.device)
-    if ws is None:
-        ws = train_workspace(TRAIN_GRAD_NORM, plan.chunks, 0, plan.table.device, stream)
-    st = lib().lora_grad_norm(plan.ref, float(max_norm), _ptr(out), *_ws_args(ws), _stream(stream))
+    ws, w, wn = _workspace(ws, TRAIN_GRAD_NORM, plan.chunks, 0, plan.device, stream)
+    st = lib().lora_grad_norm(plan.ref, max_norm, _vector(out, 2, torch.float32, "out", plan.device), w, wn,
+                              _raw_stream(stream, plan.device))
     _check(st, "lora_grad_norm")
     return out
 
@@ -319,8 +327,8 @@ def lora_grad_norm(plan, max_norm, out, ws=None, stream=None):
 def lora_adamw(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_factor=None, stream=None):
     """One AdamW step over the plan's tensors; step counts from 1.  grad_factor: fp32
     device scalar that the gradients are multiplied by (lora_grad_norm's out[1:])."""
-    if grad_factor is not None:
-        _vector(grad_factor, 1, torch.float32, "grad_factor", plan.table.device)
     hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
-    st = lib().lora_adamw(plan.ref, ctypes.byref(hyper), _ptr(grad_factor), _stream(stream))
+    st = lib().lora_adamw(plan.ref, ctypes.byref(hyper),
+                          _optional(grad_factor, 1, torch.float32, "grad_factor", plan.device),
+                          _raw_stream(stream, plan.device))
     _check(st, "lora_adamw")
