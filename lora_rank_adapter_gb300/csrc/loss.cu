@@ -344,20 +344,15 @@ __device__ __forceinline__ void zero_span(E *out, int from, int to) {
 struct RowGrad {
   float m, k, c, f;
   __device__ __forceinline__ float operator()(float v) const { return f * ex2((v - m) * k); }
-  // a 16-byte piece; `at`: the label's place relative to its first element
+  // a 16-byte piece, as if it did not hold the label
   template <typename E>
-  __device__ __forceinline__ uint4 piece(const uint4 &q, int at) const {
+  __device__ __forceinline__ uint4 piece(const uint4 &q) const {
     constexpr int N = Elem<E>::kVec;
     uint64_t v[N / 2];
     Elem<E>::pairs(q, v);
     const uint64_t m2 = pk2(-m, -m), k2 = pk2(k, k), f2 = pk2(f, f);
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) v[j] = mul2(ex2_2(mul2(add2(v[j], m2), k2)), f2);
-    if (at >= 0 && at < N) {      // one piece of the row
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j)
-        v[j] = add2(v[j], pk2(at == 2 * j ? c : 0.f, at == 2 * j + 1 ? c : 0.f));
-    }
     return Elem<E>::pack_pairs(v);
   }
 };
@@ -413,18 +408,20 @@ __global__ void __launch_bounds__(kRowThreads) grad_kernel(RowArgs a, int parts,
   }
   const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
   uint4 *dst = reinterpret_cast<uint4 *>(out + sp.head);
+  // the label's element goes after its piece, by the thread that wrote that
+  const int place = mark - sp.head - v0 * N;
+  const bool mine = place >= 0 && place < (v1 - v0) * N && place / N % kRowThreads == tid;
+  const float picked = mine ? Elem<E>::load(row + mark) : 0.f;
   int i = v0 + tid;
   for (; v1 - i > 3 * kRowThreads; i += 4 * kRowThreads) {
     uint4 q[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) q[u] = src[i + u * kRowThreads];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int j = i + u * kRowThreads;
-      __stcs(dst + j, g.piece<E>(q[u], mark - sp.head - j * N));
-    }
+    for (int u = 0; u < 4; ++u) __stcs(dst + i + u * kRowThreads, g.piece<E>(q[u]));
   }
-  for (; i < v1; i += kRowThreads) __stcs(dst + i, g.piece<E>(src[i], mark - sp.head - i * N));
+  for (; i < v1; i += kRowThreads) __stcs(dst + i, g.piece<E>(src[i]));
+  if (mine) Elem<E>::store(out + mark, g(picked) + c);
   auto one = [&](int j) { Elem<E>::store(out + j, g(Elem<E>::load(row + j)) + (j == mark ? c : 0.f)); };
   if (rank == 0 && tid < sp.head) one(tid);
   if (rank == parts - 1 && tid < V - tail) one(tail + tid);
@@ -560,19 +557,26 @@ __global__ void __launch_bounds__(kPairThreads) tokens_kernel(PolicyArgs p, int6
 // shared memory, and share their (m, s) through each other's shared memory.  The
 // policy loss's coefficient needs that row only, so its gradient is formed from
 // the held slice and the row is never read again (2 N bytes instead of 3 N).
-// The clusters stay for row after row: while one row is summed and written, the
-// next one's slice is already on its way into the other of two buffers.
-constexpr int kHeldThreads = 256;
-constexpr int kHeldChunks = 2;          // copies of a slice, each with a barrier: work starts on the first
-constexpr int kBodyAt = 128;            // the slice's first 16-byte piece; the row's head sits right before it
+//
+// The clusters stay for row after row.  A loader warp copies the slices, chunk by
+// chunk, through a ring of slots; a slot is free again when its chunk's gradient
+// has been formed, so the next rows' chunks are on their way all the time.  The
+// eight other warps go through the rows without a barrier of the block: each
+// sends its (m, s) to every block of the cluster, waits for all of them, and
+// works out the row's coefficient by itself.
+constexpr int kHeldWarps = 8;                            // that sum and write
+constexpr int kHeldWork = 32 * kHeldWarps;
+constexpr int kHeldThreads = kHeldWork + 32;             // and the loader warp
+constexpr int kChunk = 4 * kHeldWork;                    // 16-byte pieces of a chunk: four for each thread
+constexpr int kSlots = 6;                                // 96 KB: two blocks on an SM
+constexpr int kHeldSmem = kSlots * kChunk * 16;
 
 struct HeldArgs {
   RowArgs r;
   PolicyArgs p;
   float4 *terms;       // loss, kl and clipped weight of each row
   int cluster;
-  int slice;           // 16-byte pieces of a block at most
-  int buffer;          // bytes of one of the two buffers
+  int slice;           // 16-byte pieces of a block at most, up to kSlots chunks
 };
 
 // A block's slice of a row.
@@ -588,136 +592,166 @@ struct HeldSlice {
     v0 = min(rank * h.slice, vecs);
     nv = min(v0 + h.slice, vecs) - v0;
   }
-  __device__ __forceinline__ int chunk(int q) const { return min(q * ((nv + kHeldChunks - 1) / kHeldChunks), nv); }
-  __device__ __forceinline__ void load(E *held, uint64_t *loaded) const {
-    const uint4 *src = reinterpret_cast<const uint4 *>(row + head) + v0;
-    for (int q = 0; q < kHeldChunks; ++q) {
-      const int from = chunk(q), n = chunk(q + 1) - from;
-      mbar_arrive_expect_tx(&loaded[q], n * 16);
-      if (n > 0) bulk_load(held + from * Elem<E>::kVec, src + from, n * 16, &loaded[q]);
+};
+
+// A place in the ring, counting chunks: its slot, and the parity of the slot's phase.
+struct RingAt {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kSlots) {
+      slot = 0;
+      parity ^= 1;
     }
   }
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kHeldThreads) held_kernel(HeldArgs h) {
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ uint64_t loaded[2][kHeldChunks];
-  __shared__ ClusterSlots slots[2];
-  __shared__ float2 sh[kHeldThreads / 32];
-  __shared__ RowGrad shared_grad;
-  __shared__ int failed;
+__global__ void __launch_bounds__(kHeldThreads, 2) held_kernel(HeldArgs h) {
+  extern __shared__ __align__(128) uint4 ring[];
+  __shared__ uint64_t full[kSlots], empty[kSlots], ready[2];
+  __shared__ float2 pairs[2][kMaxCluster * kHeldWarps];  // (m, s) of every warp of the cluster, two exchanges
   const RowArgs &a = h.r;
   constexpr int N = Elem<E>::kVec;
-  const int tid = threadIdx.x, C = h.cluster;
+  const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, C = h.cluster;
   const int rank = (int)(blockIdx.x % C);
   const int64_t clusters = gridDim.x / C;
   if (tid == 0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      for (int q = 0; q < kHeldChunks; ++q) mbar_init(&loaded[i][q], 1);
-      mbar_init(&slots[i].ready, C);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kHeldWarps);
     }
-    failed = 0;
+    for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C * kHeldWarps);
     fence_barrier_init();
   }
   __syncthreads();
-  if (C > 1) {                                        // every block's barriers stand before any is written to
-    cluster_arrive();
-    cluster_wait();
-  }
+  cluster_arrive();                                      // every block's barriers stand before any is written to
+  cluster_wait();
   pdl_wait();
-  auto counts = [&](int64_t label) { return label >= 0 && label < a.V; };
-  auto held_of = [&](uint32_t seq) { return reinterpret_cast<E *>(smem + (seq & 1) * h.buffer + kBodyAt); };
   int64_t t = blockIdx.x / C;
-  int64_t label = t < a.T ? a.labels[t] : -1, label1 = t + clusters < a.T ? a.labels[t + clusters] : -1;
-  uint32_t seq = 0;                                   // rows that this block has held
-  if (tid == 0 && counts(label)) HeldSlice<E>(h, t, rank).load(held_of(0), loaded[0]);
+  int64_t label = t < a.T ? a.labels[t] : -1;
+  auto advance = [&](int64_t &mark) {                    // this row's label, with the next one's on its way
+    mark = label;
+    if (t + clusters < a.T) label = a.labels[t + clusters];
+    return mark >= 0 && mark < a.V;
+  };
+  RingAt at;
+
+  if (warp == kHeldWarps) {                              // the loader
+    if (lane != 0) return;
+    bool ok = true, again = false;                       // again: the ring has been filled once
+    int64_t mark;
+    for (; t < a.T && ok; t += clusters) {
+      if (!advance(mark)) continue;
+      const HeldSlice<E> sl(h, t, rank);
+      const uint4 *src = reinterpret_cast<const uint4 *>(sl.row + sl.head) + sl.v0;
+      for (int from = 0; from < sl.nv && ok; from += kChunk) {
+        const uint32_t bytes = (uint32_t)min(kChunk, sl.nv - from) * 16;
+        ok = !again || mbar_wait(&empty[at.slot], at.parity ^ 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&full[at.slot], bytes);
+        bulk_load(ring + at.slot * kChunk, src + from, bytes, &full[at.slot]);
+        at.next();
+        again = again || at.parity;
+      }
+    }
+    // A wait ran out: the copies in flight land before the block ends.
+    if (!ok)
+      for (int i = 0; i < kSlots; ++i)
+        if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
+    return;
+  }
+
+  uint32_t count = 0;                                    // exchanges so far
+  const float k = a.inv_t * kLog2e;
   for (; t < a.T; t += clusters) {
-    const int64_t now = label, t1 = t + clusters, t2 = t1 + clusters;
-    label = label1;
-    label1 = t2 < a.T ? a.labels[t2] : -1;
-    const bool valid = counts(now), next = counts(label);
-    const uint32_t other = seq + (valid ? 1 : 0);     // the next held row's number
-    __syncthreads();                                  // no thread reads the other buffer any more
-    if (tid == 0 && next) HeldSlice<E>(h, t1, rank).load(held_of(other), loaded[other & 1]);
+    int64_t mark64;
+    const bool valid = advance(mark64);
     const HeldSlice<E> sl(h, t, rank);
     E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
-    const int nv = sl.nv, V = (int)a.V;
-    // the block's elements [e0, e1): the first block has the head, the last one the tail
-    const int tail = sl.head + sl.vecs * N;
-    const int e0 = rank == 0 ? 0 : sl.head + sl.v0 * N, e1 = rank == C - 1 ? V : sl.head + (sl.v0 + nv) * N;
+    const int V = (int)a.V, nv = sl.nv, tail = sl.head + sl.vecs * N, first = sl.head + sl.v0 * N, mark = (int)mark64;
     if (!valid) {
       if (rank == 0 && tid == 0) {
         a.logps[t] = 0.f;
         h.terms[t] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      if (a.dlogits) zero_span<E, kHeldThreads>(out, e0, e1);
+      if (a.dlogits) zero_span<E, kHeldWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N);
       continue;
     }
-    const int mark = (int)now;
-    PolicyRow in = {0.f, 0.f, 0.f, 0.f};
-    float picked = 0.f;
-    if (tid == 0) {                                   // on their way while the row is summed
-      in = policy_row(h.p, t);
-      picked = Elem<E>::load(sl.row + mark);
-    }
-    // the ragged ends, at most seven elements each, beside the slice
-    E *held = held_of(seq);                           // element i of the row at held[i - head - v0 * N]
-    float edge = kNegInf;
+    // on their way while the row is summed (read before this warp's arrival lets
+    // any other write the row, where the gradient replaces it)
+    const PolicyRow in = policy_row(h.p, t);
+    const float picked = Elem<E>::load(sl.row + mark);
+    // the ragged ends, at most seven elements each: the first block's and the last one's
     const bool at_head = rank == 0 && tid < sl.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
     const int edge_at = at_head ? tid : tail + tid - 16;
-    if (at_head || at_tail) {
-      edge = Elem<E>::load(sl.row + edge_at);
-      Elem<E>::store(at_head ? held - sl.head + tid : held + nv * N + tid - 16, edge);
-      fence_proxy_async_smem();                       // a later copy may land on the tail's place
-    }
+    float edge = kNegInf;
+    if (at_head || at_tail) edge = Elem<E>::load(sl.row + edge_at);
 
-    const float k = a.inv_t * kLog2e;
     float m = kNegInf;
     uint64_t s2 = 0;
-    const uint4 *body = reinterpret_cast<const uint4 *>(held);
-    const uint32_t set = seq & 1, parity = (seq >> 1) & 1;
-    for (int q = 0; q < kHeldChunks; ++q) {
-      if (!mbar_wait(&loaded[set][q], parity)) failed = 1;
-      absorb_span<E, kHeldThreads>(m, s2, body, sl.chunk(q), sl.chunk(q + 1), k);
+    RingAt here = at;
+    bool ok = true;
+    for (int from = 0; from < nv; from += kChunk, here.next()) {
+      ok = mbar_wait(&full[here.slot], here.parity) && ok;
+      absorb_span<E, kHeldWork>(m, s2, ring + here.slot * kChunk, 0, min(kChunk, nv - from), k);
     }
     const float2 both = unpk2(s2);
     float s = both.x + both.y;
     if (edge != kNegInf) absorb_one(m, s, edge, k);
-    block_merge<kHeldThreads / 32>(m, s, k, sh);
-    if (tid < 32) {                                   // one warp finishes the row for the block
-      if (C > 1 && !cluster_merge(m, s, k, rank, C, &slots[set], parity)) failed = 1;
-      if (tid == 0) {
-        const float logp = (picked - m) * a.inv_t - logf(s);
-        const PolicyTerm x = policy_term(h.p, in, logp);
-        const float c = x.coef * a.grad_scale * a.inv_t;
-        shared_grad = {m, k, c, -c / s};
-        if (rank == 0) {
-          a.logps[t] = logp;
-          h.terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
+    warp_merge(m, s, k);
+    const uint32_t set = count & 1;
+    if (lane < C) {
+      st_dsmem_f2(&pairs[set][rank * kHeldWarps + warp], lane, make_float2(m, s));
+      mbar_arrive_remote(&ready[set], lane);
+    }
+    ok = mbar_wait<true>(&ready[set], (count >> 1) & 1) && ok;
+    if (!__all_sync(0xffffffffu, ok)) return;            // a wait ran out: the error word is set
+    ++count;
+    m = kNegInf;
+    s = 0.f;
+    for (int i = lane; i < C * kHeldWarps; i += 32) {
+      const float2 v = pairs[set][i];
+      const float mm = fmaxf(m, v.x), r = ref_of(mm);
+      s = s * ex2((m - r) * k) + v.y * ex2((v.x - r) * k);
+      m = mm;
+    }
+    warp_merge(m, s, k);
+    const float logp = (picked - m) * a.inv_t - logf(s);
+    const PolicyTerm x = policy_term(h.p, in, logp);
+    if (rank == 0 && tid == 0) {
+      a.logps[t] = logp;
+      h.terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
+    }
+    const float c = x.coef * a.grad_scale * a.inv_t;
+    const RowGrad g = {m, k, c, -c / s};
+    const bool write = a.dlogits != nullptr && c != 0.f;
+    const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0;
+    uint4 *dst = reinterpret_cast<uint4 *>(out + sl.head) + sl.v0;
+    for (int from = 0; from < nv; from += kChunk, at.next()) {
+      const int n = min(kChunk, nv - from);
+      const uint4 *src = ring + at.slot * kChunk;
+      if (write && same) {
+        if (n == kChunk) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) __stcs(dst + from + tid + u * kHeldWork, g.piece<E>(src[tid + u * kHeldWork]));
+        } else {
+          for (int i = tid; i < n; i += kHeldWork) __stcs(dst + from + i, g.piece<E>(src[i]));
         }
+      } else if (write) {
+        const int e = first + from * N;                  // the chunk's first element
+        grad_words<E, kHeldWork>(out, reinterpret_cast<const E *>(src) - e, e, e + n * N, mark, g);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[at.slot]);
     }
-    __syncthreads();
-    if (failed) {                                     // a wait ran out: the error word is set
-      if (next)
-        for (int q = 0; q < kHeldChunks; ++q) mbar_wait(&loaded[other & 1][q], (other >> 1) & 1);
-      return;
-    }
-    ++seq;
-    if (a.dlogits == nullptr) continue;
-    const RowGrad g = shared_grad;
-    if (g.c == 0.f) {
-      zero_span<E, kHeldThreads>(out, e0, e1);
-    } else if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0) {
-      uint4 *dst = reinterpret_cast<uint4 *>(out + sl.head) + sl.v0;
-      const int at = mark - sl.head - sl.v0 * N;      // the label within the slice
-#pragma unroll 4
-      for (int i = tid; i < nv; i += kHeldThreads) __stcs(dst + i, g.piece<E>(body[i], at - i * N));
-      if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge) + (edge_at == mark ? g.c : 0.f));
-    } else {
-      grad_words<E, kHeldThreads>(out, held - sl.head - sl.v0 * N, e0, e1, mark, g);
+    if (write) {
+      if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge) + (edge_at == mark ? c : 0.f));
+      // the label's element, by the thread that wrote its piece
+      const int place = mark - first;
+      if (same && place >= 0 && place < nv * N && place / N % kHeldWork == tid) Elem<E>::store(out + mark, g(picked) + c);
+    } else if (a.dlogits) {
+      zero_span<E, kHeldWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N);
     }
   }
 }
@@ -778,30 +812,28 @@ RowArgs row_args(const LossArgs &a) {
   return r;
 }
 
-// How a row is cut for the held kernel.  Slices of 32 KB keep three blocks on an
-// SM (two buffers each); few rows are cut finer, down to 4 KB a block, until the
-// grid covers the SMs twice.  A row whose slice does not fit a buffer at eight
-// blocks (cluster 0) goes by the two-pass kernels.
-constexpr int kHeldSmem = 220 << 10;
+// How a row is cut for the held kernel: slices of at most four chunks (64 KB), so
+// that a third of the ring is always ahead; few rows are cut finer, down to 4 KB
+// a block, until the grid covers the SMs twice.  A row that eight blocks' rings
+// do not hold (cluster 0) goes by the two-pass kernels.
 struct HeldPlan {
-  int cluster, slice, buffer;
+  int cluster, slice;
 };
 HeldPlan plan_held(lora_dtype_t dtype, int64_t T, int64_t V) {
   const int64_t e = dtype == LORA_BF16 ? 2 : 4, bytes = V * e;
-  int64_t c = std::max<int64_t>(1, ceil_div(bytes, 32 << 10));
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, 4 * kChunk * 16));
   c = std::max(c, std::min(ceil_div(2 * num_sms(), std::max<int64_t>(T, 1)), bytes / 4096));
   c = std::min<int64_t>(c, kMaxCluster);
   const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
-  const int64_t buffer = kBodyAt + 16 * slice + 128;      // the tail behind the slice, the next buffer on 128 bytes
-  if (2 * buffer > kHeldSmem) return {0, 0, 0};
-  return {(int)c, (int)slice, (int)buffer};
+  if (slice > kSlots * kChunk) return {0, 0};
+  return {(int)c, (int)slice};
 }
 
 // Clusters of a kernel that the device holds at once; the last answers are kept.
-int max_clusters(const void *kernel, int cluster, int smem) {
+int max_clusters(const void *kernel, int cluster) {
   struct Known {
     const void *kernel;
-    int dev, cluster, smem, n;
+    int dev, cluster, n;
   };
   static Known known[32];
   static int used = 0;
@@ -810,11 +842,11 @@ int max_clusters(const void *kernel, int cluster, int smem) {
   cudaGetDevice(&dev);
   std::lock_guard<std::mutex> lk(mu);
   for (const Known &k : known)
-    if (k.n > 0 && k.kernel == kernel && k.dev == dev && k.cluster == cluster && k.smem == smem) return k.n;
+    if (k.n > 0 && k.kernel == kernel && k.dev == dev && k.cluster == cluster) return k.n;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster);
   cfg.blockDim = dim3(kHeldThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kHeldSmem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
@@ -823,18 +855,18 @@ int max_clusters(const void *kernel, int cluster, int smem) {
   cfg.numAttrs = 1;
   int n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
-  known[used++ % 32] = {kernel, dev, cluster, smem, n};
+  known[used++ % 32] = {kernel, dev, cluster, n};
   return n;
 }
 
 template <typename E>
 cudaError_t launch_held(const HeldArgs &h, cudaStream_t st) {
   const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
-  const int smem = 2 * h.buffer;
   cudaError_t e = ensure_smem(kernel, kHeldSmem);
   if (e != cudaSuccess) return e;
-  const int64_t clusters = std::min<int64_t>(h.r.T, max_clusters(kernel, h.cluster, smem));
-  return launch(held_kernel<E>, dim3((unsigned)(clusters * h.cluster)), dim3(kHeldThreads), smem, st, h.cluster, true, h);
+  const int64_t clusters = std::min<int64_t>(h.r.T, max_clusters(kernel, h.cluster));
+  return launch(held_kernel<E>, dim3((unsigned)(clusters * h.cluster)), dim3(kHeldThreads), kHeldSmem, st, h.cluster,
+                true, h);
 }
 
 // Blocks for each row of a pass from global memory: enough that the grid fills
@@ -935,7 +967,7 @@ lora_status_t policy_loss(const LossArgs &a, const PolicyArgs &p, void *ws, size
   if (r.coef == nullptr) return LORA_ERR_WORKSPACE;
   const HeldPlan hp = plan_held(a.dtype, a.T, a.V);
   if (hp.cluster > 0) {
-    const HeldArgs h = {r, p, terms, hp.cluster, hp.slice, hp.buffer};
+    const HeldArgs h = {r, p, terms, hp.cluster, hp.slice};
     LORA_CUDA(a.dtype == LORA_BF16 ? launch_held<__nv_bfloat16>(h, st) : launch_held<float>(h, st));
   } else {
     LORA_TRY(run_stats(a.dtype, r, st));
