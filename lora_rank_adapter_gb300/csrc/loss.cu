@@ -183,19 +183,21 @@ __device__ __forceinline__ void absorb(float &m, uint64_t &s, const uint4 (&q)[U
   s = add2(s, t);
 }
 
-// Pieces [from, to) of a row, kThreads threads, four loads of each in flight.
-template <typename E, int kThreads>
+// Pieces [from, to) of a row, kThreads threads, U loads of each in flight.
+template <typename E, int kThreads, int U>
 __device__ __forceinline__ void absorb_span(float &m, uint64_t &s, const uint4 *p, int from, int to, float k) {
   int i = from + (int)threadIdx.x;
-  for (; to - i > 3 * kThreads; i += 4 * kThreads) {
-    const uint4 q[4] = {p[i], p[i + kThreads], p[i + 2 * kThreads], p[i + 3 * kThreads]};
-    absorb<E, 4>(m, s, q, k);
-  }
-  if (i < to) {
-    uint4 q[3];
+  for (; to - i > (U - 1) * kThreads; i += U * kThreads) {
+    uint4 q[U];
 #pragma unroll
-    for (int u = 0; u < 3; ++u) q[u] = to - i > u * kThreads ? p[i + u * kThreads] : Elem<E>::lowest();
-    absorb<E, 3>(m, s, q, k);
+    for (int u = 0; u < U; ++u) q[u] = p[i + u * kThreads];
+    absorb<E, U>(m, s, q, k);
+  }
+  if (U > 1 && i < to) {
+    uint4 q[U > 1 ? U - 1 : 1];
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u) q[u] = to - i > u * kThreads ? p[i + u * kThreads] : Elem<E>::lowest();
+    absorb<E, U - 1>(m, s, q, k);
   }
 }
 
@@ -259,6 +261,16 @@ __device__ __forceinline__ void st_dsmem_f2(const void *local_ptr, uint32_t cta,
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(cta));
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
 }
+// The same as one asynchronous store whose bytes complete `bar` of that block
+// (of a cluster: the kernel has been launched as one).
+__device__ __forceinline__ void st_async_f2(const void *local_ptr, const uint64_t *local_bar, uint32_t cta, float2 v) {
+  uint32_t p, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(smem_u32(local_ptr)), "r"(cta));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(local_bar)), "r"(cta));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(p),
+               "f"(v.x), "f"(v.y), "r"(b)
+               : "memory");
+}
 __device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int rank, int C, ClusterSlots *slots,
                                               uint32_t parity) {
   const int lane = lane_id();
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(kRowThreads) stats_kernel(RowArgs a, int C, in
   float label_value = 0.f, m = kNegInf;
   if (rank == 0 && threadIdx.x == 0) label_value = Elem<E>::load(row + label);
   uint64_t s2 = 0;
-  absorb_span<E, kRowThreads>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
+  absorb_span<E, kRowThreads, 4>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
   const float2 both = unpk2(s2);
   float s = both.x + both.y;
   if (rank == C - 1) {      // the ragged ends
@@ -561,14 +573,17 @@ __global__ void __launch_bounds__(kPairThreads) tokens_kernel(PolicyArgs p, int6
 // The clusters stay for row after row.  A loader warp copies the slices, chunk by
 // chunk, through a ring of slots; a slot is free again when its chunk's gradient
 // has been formed, so the next rows' chunks are on their way all the time.  The
-// eight other warps go through the rows without a barrier of the block: each
+// other warps go through the rows without a barrier of the block: each
 // sends its (m, s) to every block of the cluster, waits for all of them, and
 // works out the row's coefficient by itself.
-constexpr int kHeldWarps = 8;                            // that sum and write
+constexpr int kHeldWarps = 8;                           // that sum and write
 constexpr int kHeldWork = 32 * kHeldWarps;
 constexpr int kHeldThreads = kHeldWork + 32;             // and the loader warp
-constexpr int kChunk = 4 * kHeldWork;                    // 16-byte pieces of a chunk: four for each thread
+constexpr int kPer = 4;                                  // 16-byte pieces of a chunk for each thread
+constexpr int kChunk = kPer * kHeldWork;
 constexpr int kSlots = 6;                                // 96 KB: two blocks on an SM
+constexpr int kHeldBlocks = 2;
+constexpr int kSliceBytes = 64 << 10;                    // of a row for a block, where eight blocks suffice
 constexpr int kHeldSmem = kSlots * kChunk * 16;
 
 struct HeldArgs {
@@ -577,6 +592,7 @@ struct HeldArgs {
   float4 *terms;       // loss, kl and clipped weight of each row
   int cluster;
   int slice;           // 16-byte pieces of a block at most, up to kSlots chunks
+  uint32_t zero;
 };
 
 // A block's slice of a row.
@@ -607,7 +623,7 @@ struct RingAt {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kHeldThreads, 2) held_kernel(HeldArgs h) {
+__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArgs h) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ uint64_t full[kSlots], empty[kSlots], ready[2];
   __shared__ float2 pairs[2][kMaxCluster * kHeldWarps];  // (m, s) of every warp of the cluster, two exchanges
@@ -621,12 +637,14 @@ __global__ void __launch_bounds__(kHeldThreads, 2) held_kernel(HeldArgs h) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], kHeldWarps);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C * kHeldWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C == 1 ? kHeldWarps : 1);
     fence_barrier_init();
   }
   __syncthreads();
-  cluster_arrive();                                      // every block's barriers stand before any is written to
-  cluster_wait();
+  if (C > 1) {                                           // every block's barriers stand before any is written to
+    cluster_arrive();
+    cluster_wait();
+  }
   pdl_wait();
   int64_t t = blockIdx.x / C;
   int64_t label = t < a.T ? a.labels[t] : -1;
@@ -694,16 +712,27 @@ __global__ void __launch_bounds__(kHeldThreads, 2) held_kernel(HeldArgs h) {
     bool ok = true;
     for (int from = 0; from < nv; from += kChunk, here.next()) {
       ok = mbar_wait(&full[here.slot], here.parity) && ok;
-      absorb_span<E, kHeldWork>(m, s2, ring + here.slot * kChunk, 0, min(kChunk, nv - from), k);
+      absorb_span<E, kHeldWork, kPer>(m, s2, ring + here.slot * kChunk, 0, min(kChunk, nv - from), k);
     }
     const float2 both = unpk2(s2);
     float s = both.x + both.y;
     if (edge != kNegInf) absorb_one(m, s, edge, k);
     warp_merge(m, s, k);
     const uint32_t set = count & 1;
-    if (lane < C) {
-      st_dsmem_f2(&pairs[set][rank * kHeldWarps + warp], lane, make_float2(m, s));
-      mbar_arrive_remote(&ready[set], lane);
+    // In a cluster the pair's own bytes complete the others' barriers: an arrival
+    // with release semantics there would first wait for the last row's gradient to
+    // reach memory.  It is sent when `picked` has come (h.zero is 0): past the
+    // exchange any warp may write that element.
+    if (C == 1) {
+      if (lane == 0) {
+        pairs[set][warp] = make_float2(m, s);
+        mbar_arrive(&ready[set]);
+      }
+    } else {
+      if (tid == 0) mbar_arrive_expect_tx(&ready[set], C * kHeldWarps * 8);
+      if (lane < C)
+        st_async_f2(&pairs[set][rank * kHeldWarps + warp], &ready[set], lane + (__float_as_uint(picked) & h.zero),
+                    make_float2(m, s));
     }
     ok = mbar_wait<true>(&ready[set], (count >> 1) & 1) && ok;
     if (!__all_sync(0xffffffffu, ok)) return;            // a wait ran out: the error word is set
@@ -734,7 +763,7 @@ __global__ void __launch_bounds__(kHeldThreads, 2) held_kernel(HeldArgs h) {
       if (write && same) {
         if (n == kChunk) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) __stcs(dst + from + tid + u * kHeldWork, g.piece<E>(src[tid + u * kHeldWork]));
+          for (int u = 0; u < kPer; ++u) __stcs(dst + from + tid + u * kHeldWork, g.piece<E>(src[tid + u * kHeldWork]));
         } else {
           for (int i = tid; i < n; i += kHeldWork) __stcs(dst + from + i, g.piece<E>(src[i]));
         }
@@ -814,15 +843,15 @@ RowArgs row_args(const LossArgs &a) {
 
 // How a row is cut for the held kernel: slices of at most four chunks (64 KB), so
 // that a third of the ring is always ahead; few rows are cut finer, down to 4 KB
-// a block, until the grid covers the SMs twice.  A row that eight blocks' rings
+// a block, as long as all blocks run at once.  A row that eight blocks' rings
 // do not hold (cluster 0) goes by the two-pass kernels.
 struct HeldPlan {
   int cluster, slice;
 };
 HeldPlan plan_held(lora_dtype_t dtype, int64_t T, int64_t V) {
   const int64_t e = dtype == LORA_BF16 ? 2 : 4, bytes = V * e;
-  int64_t c = std::max<int64_t>(1, ceil_div(bytes, 4 * kChunk * 16));
-  c = std::max(c, std::min(ceil_div(2 * num_sms(), std::max<int64_t>(T, 1)), bytes / 4096));
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, kSliceBytes));
+  c = std::max(c, std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096));
   c = std::min<int64_t>(c, kMaxCluster);
   const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
   if (slice > kSlots * kChunk) return {0, 0};
@@ -967,7 +996,7 @@ lora_status_t policy_loss(const LossArgs &a, const PolicyArgs &p, void *ws, size
   if (r.coef == nullptr) return LORA_ERR_WORKSPACE;
   const HeldPlan hp = plan_held(a.dtype, a.T, a.V);
   if (hp.cluster > 0) {
-    const HeldArgs h = {r, p, terms, hp.cluster, hp.slice};
+    const HeldArgs h = {r, p, terms, hp.cluster, hp.slice, 0u};
     LORA_CUDA(a.dtype == LORA_BF16 ? launch_held<__nv_bfloat16>(h, st) : launch_held<float>(h, st));
   } else {
     LORA_TRY(run_stats(a.dtype, r, st));
