@@ -15,12 +15,20 @@ the fused pair forward_h_ / backward_ex:
     out = base + scale * (x @ A) @ B
 with gradients dx = scale * dout @ B^T @ A^T, dA = scale * x^T @ (dout @ B^T),
 dB = scale * (x @ A)^T @ dout and dbase = dout.
+
+`token_logps`, `preference_loss` and `policy_loss` are the differentiable forms of the
+loss operators of `training`, and `AdamW` an optimizer on lora_grad_norm / lora_adamw:
+    loss, pair_loss, seq_logps = preference_loss(logits, labels, cu_seqlens, ref_logps, beta=0.1)
+    loss.backward(); optimizer.step()
+The losses form their gradient with the forward pass, while a row is at hand; the
+backward pass multiplies it by the incoming gradient in place (no pass over it when
+that is 1) and hands it on, so it can be taken once.
 """
-from typing import List, Sequence
+from typing import List, Optional, Sequence
 
 import torch
 
-from . import binding
+from . import binding, training
 
 NS = "lora_gb300"
 
@@ -170,3 +178,213 @@ class LoraLinearFn(torch.autograd.Function):
 def lora_linear(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, base: torch.Tensor, scale: float):
     """Differentiable out = base + scale * (x @ A) @ B (x [M,K], A [K,r], B [r,L], base [M,L])."""
     return LoraLinearFn.apply(x, A, B, base, scale)
+
+
+# ----------------------------------------------------------------------------- losses over logits
+@torch.library.custom_op(f"{NS}::token_logps", mutates_args=(), device_types="cuda")
+def token_logps_op(logits: torch.Tensor, labels: torch.Tensor, temperature: float) -> List[torch.Tensor]:
+    """(logps, stats): the labels' log-probabilities, and what their gradient needs."""
+    T = logits.shape[0]
+    logps = torch.empty(T, dtype=torch.float32, device=logits.device)
+    stats = torch.empty((T, 2), dtype=torch.float32, device=logits.device)
+    training.lora_token_logps(logits, labels, logps, temperature=temperature, stats=stats)
+    return [logps, stats]
+
+
+@token_logps_op.register_fake
+def _(logits, labels, temperature):
+    T = logits.shape[0]
+    return [logits.new_empty((T,), dtype=torch.float32), logits.new_empty((T, 2), dtype=torch.float32)]
+
+
+@torch.library.custom_op(f"{NS}::token_logps_backward", mutates_args=(), device_types="cuda")
+def token_logps_backward_op(logits: torch.Tensor, labels: torch.Tensor, stats: torch.Tensor, dlogps: torch.Tensor,
+                            temperature: float) -> torch.Tensor:
+    """dlogits from the log-probabilities' gradient."""
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    training.lora_token_logps_backward(logits, labels, stats, dlogps, dlogits, temperature=temperature)
+    return dlogits
+
+
+@token_logps_backward_op.register_fake
+def _(logits, labels, stats, dlogps, temperature):
+    return logits.new_empty(logits.shape)
+
+
+@torch.library.custom_op(f"{NS}::preference_loss", mutates_args=(), device_types="cuda")
+def preference_loss_op(logits: torch.Tensor, labels: torch.Tensor, cu_seqlens: torch.Tensor,
+                       ref_logps: Optional[torch.Tensor], beta: float, kind: str, label_smoothing: float,
+                       length_normalize: bool, temperature: float, with_gradient: bool) -> List[torch.Tensor]:
+    """(loss [], pair_loss [P], seq_logps [2P], token_logps [T], dlogits: empty without a gradient)."""
+    T, P, f32 = logits.shape[0], cu_seqlens.numel() // 2, torch.float32
+    dev = logits.device
+    loss, pair = torch.empty((), dtype=f32, device=dev), torch.empty(P, dtype=f32, device=dev)
+    seq, tok = torch.empty(2 * P, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev)
+    d = torch.empty(logits.shape if with_gradient else (0, 0), dtype=logits.dtype, device=dev)
+    training.lora_preference_loss(logits, labels, cu_seqlens, ref_logps, beta, tok, seq, pair, loss,
+                                  dlogits=d if with_gradient else None, kind=kind, label_smoothing=label_smoothing,
+                                  length_normalize=length_normalize, temperature=temperature)
+    return [loss, pair, seq, tok, d]
+
+
+@preference_loss_op.register_fake
+def _(logits, labels, cu_seqlens, ref_logps, beta, kind, label_smoothing, length_normalize, temperature,
+      with_gradient):
+    T, P = logits.shape[0], cu_seqlens.numel() // 2
+    new = lambda *shape: logits.new_empty(shape, dtype=torch.float32)  # noqa: E731
+    return [new(), new(P), new(2 * P), new(T), logits.new_empty(logits.shape if with_gradient else (0, 0))]
+
+
+@torch.library.custom_op(f"{NS}::policy_loss", mutates_args=(), device_types="cuda")
+def policy_loss_op(logits: torch.Tensor, labels: torch.Tensor, old_logps: Optional[torch.Tensor],
+                   advantages: torch.Tensor, weights: Optional[torch.Tensor], ref_logps: Optional[torch.Tensor],
+                   clip_low: float, clip_high: float, kl_beta: float, temperature: float,
+                   with_gradient: bool) -> List[torch.Tensor]:
+    """(metrics [3]: loss, weighted KL, weight of the clipped tokens; token_logps [T]; dlogits)."""
+    T, dev = logits.shape[0], logits.device
+    metrics = torch.empty(3, dtype=torch.float32, device=dev)
+    tok = torch.empty(T, dtype=torch.float32, device=dev)
+    d = torch.empty(logits.shape if with_gradient else (0, 0), dtype=logits.dtype, device=dev)
+    training.lora_policy_loss(logits, labels, old_logps, advantages, weights, tok, metrics, ref_logps=ref_logps,
+                              dlogits=d if with_gradient else None, clip_low=clip_low, clip_high=clip_high,
+                              kl_beta=kl_beta, temperature=temperature)
+    return [metrics, tok, d]
+
+
+@policy_loss_op.register_fake
+def _(logits, labels, old_logps, advantages, weights, ref_logps, clip_low, clip_high, kl_beta, temperature,
+      with_gradient):
+    T = logits.shape[0]
+    return [logits.new_empty((3,), dtype=torch.float32), logits.new_empty((T,), dtype=torch.float32),
+            logits.new_empty(logits.shape if with_gradient else (0, 0))]
+
+
+class TokenLogpsFn(torch.autograd.Function):
+    """logps[t] = log_softmax(logits[t] / temperature)[labels[t]]."""
+
+    @staticmethod
+    def forward(ctx, logits, labels, temperature):
+        logps, stats = token_logps_op(logits, labels, temperature)
+        ctx.save_for_backward(logits, labels, stats)
+        ctx.temperature = temperature
+        return logps
+
+    @staticmethod
+    def backward(ctx, dlogps):
+        logits, labels, stats = ctx.saved_tensors
+        return token_logps_backward_op(logits, labels, stats, dlogps.contiguous(), ctx.temperature), None, None
+
+
+def _hand_on(ctx, dloss):
+    """The gradient that the forward pass made, times the loss's own: once."""
+    if ctx.dlogits is None:
+        raise RuntimeError("the gradient of this loss is made once, with its forward pass, and has been taken")
+    d, ctx.dlogits = ctx.dlogits, None
+    training.lora_scale_gradient(d, dloss.float().reshape(1))
+    return d
+
+
+class PreferenceLossFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, *args):
+        loss, pair, seq, tok, d = preference_loss_op(logits, *args, ctx.needs_input_grad[0])
+        ctx.dlogits = d if ctx.needs_input_grad[0] else None
+        ctx.mark_non_differentiable(pair, seq, tok)
+        return loss, pair, seq, tok
+
+    @staticmethod
+    def backward(ctx, dloss, *_):
+        return (_hand_on(ctx, dloss),) + (None,) * 8
+
+
+class PolicyLossFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, *args):
+        metrics, tok, d = policy_loss_op(logits, *args, ctx.needs_input_grad[0])
+        ctx.dlogits = d if ctx.needs_input_grad[0] else None
+        loss = metrics[0].clone()
+        ctx.mark_non_differentiable(metrics, tok)
+        return loss, metrics, tok
+
+    @staticmethod
+    def backward(ctx, dloss, *_):
+        return (_hand_on(ctx, dloss),) + (None,) * 9
+
+
+def token_logps(logits: torch.Tensor, labels: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
+    """Differentiable log-probabilities [T] of labels [T] (int64; 0 where a label is outside
+    [0, V)) under logits [T, V]."""
+    return TokenLogpsFn.apply(logits, labels, float(temperature))
+
+
+def preference_loss(logits, labels, cu_seqlens, ref_logps=None, beta=0.1, kind="sigmoid", label_smoothing=0.0,
+                    length_normalize=False, temperature=1.0):
+    """(loss, pair_loss [P], seq_logps [2P]) of P pairs of packed sequences, pair p preferring
+    sequence p to sequence P + p; the loss is differentiable in the logits."""
+    loss, pair, seq, _ = PreferenceLossFn.apply(logits, labels, cu_seqlens, ref_logps, float(beta), kind,
+                                                float(label_smoothing), bool(length_normalize), float(temperature))
+    return loss, pair, seq
+
+
+def policy_loss(logits, labels, old_logps, advantages, weights=None, ref_logps=None, clip_low=0.2, clip_high=0.2,
+                kl_beta=0.0, temperature=1.0):
+    """(loss, metrics [3], token_logps [T]) of the clipped policy loss with a KL term; the loss
+    is differentiable in the logits."""
+    return PolicyLossFn.apply(logits, labels, old_logps, advantages, weights, ref_logps, float(clip_low),
+                              float(clip_high), float(kl_beta), float(temperature))
+
+
+# ----------------------------------------------------------------------------- optimizer
+class AdamW:
+    """AdamW over an adapter's tensors (all of one dtype), one launch a step.
+
+    state_bits: 32, or 8 for e4m3 states with a scale for each 256 elements.  masters: keep
+    fp32 copies that the step updates (for bf16 parameters whose updates are smaller than
+    their rounding).  max_norm: clip the gradients' global norm to it; `norm` then holds
+    (norm, factor) of the last step.  Parameters without a gradient sit a step out."""
+
+    def __init__(self, params, lr=1e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, masters=False,
+                 max_norm=None):
+        self.params = [p for p in params]
+        if state_bits not in (8, 32):
+            raise ValueError("state_bits has to be 8 or 32")
+        self.lr, self.betas, self.eps, self.weight_decay, self.max_norm = lr, betas, eps, weight_decay, max_norm
+        self.step_count, self._plan, self._laid_out = 0, None, None
+        self.norm = torch.zeros(2, device=self.params[0].device) if max_norm is not None and self.params else None
+        zeros = lambda p, dt: torch.zeros_like(p, dtype=dt, requires_grad=False)  # noqa: E731
+        dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        self.exp_avg = [zeros(p, dt) for p in self.params]
+        self.exp_avg_sq = [zeros(p, dt) for p in self.params]
+        scales = lambda: [torch.zeros(-(-p.numel() // training.ADAMW_BLOCK), device=p.device)  # noqa: E731
+                          for p in self.params]
+        self.exp_avg_scale = scales() if state_bits == 8 else None
+        self.exp_avg_sq_scale = scales() if state_bits == 8 else None
+        self.masters = [p.detach().float().clone(memory_format=torch.preserve_format) for p in self.params] \
+            if masters else None
+
+    def zero_grad(self):
+        for p in self.params:
+            p.grad = None
+
+    @torch.no_grad()
+    def step(self):
+        """One step from the parameters' .grad; the tensors' addresses are laid out again when a
+        gradient has moved."""
+        at = [i for i, p in enumerate(self.params) if p.grad is not None]
+        if not at:
+            return
+        grads = [self.params[i].grad for i in at]
+        laid_out = [(i, g.data_ptr(), g.dtype, g.stride(), self.params[i].data_ptr()) for i, g in zip(at, grads)]
+        if self._plan is None or laid_out != self._laid_out:
+            pick = lambda v: None if v is None else [v[i] for i in at]  # noqa: E731
+            self._plan = training.lora_adamw_plan([self.params[i].detach() for i in at], grads, pick(self.exp_avg),
+                                                  pick(self.exp_avg_sq), masters=pick(self.masters),
+                                                  exp_avg_scales=pick(self.exp_avg_scale),
+                                                  exp_avg_sq_scales=pick(self.exp_avg_sq_scale))
+            self._plan.tensors = None        # gradients are not kept alive beyond the step that uses them
+            self._laid_out = laid_out
+        self.step_count += 1
+        if self.max_norm is not None:
+            training.lora_grad_norm(self._plan, self.max_norm, self.norm)
+        training.lora_adamw(self._plan, self.lr, self.step_count, self.betas[0], self.betas[1], self.eps,
+                            self.weight_decay, grad_factor=None if self.max_norm is None else self.norm[1:])
