@@ -161,7 +161,7 @@ LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_
  *   p, g    dtype param_dtype / grad_dtype of the plan, contiguous [numel]
  *   codes   uint8 (e4m3) [numel];  scales  float [ceil(numel / LORA_ADAMW_BLOCK)]
  * Elements need only the alignment of their type; tensors whose pointers are all
- * 16-byte aligned take wide loads (codes: 8-byte).
+ * 16-byte aligned take wide loads (codes: 4-byte).
  * -------------------------------------------------------------------------------- */
 #define LORA_ADAMW_BLOCK 256
 #define LORA_ADAMW_CHUNK 2048

@@ -4,14 +4,16 @@
 // An adapter has some hundred tensors of ten thousand to a million elements, so
 // the work is laid out once as a table of chunks (adamw_build) and a step is one
 // launch over all of them: a block takes a chunk of 2048 elements, a warp a block
-// of 256 (one scale of an 8-bit state), a lane 8 consecutive elements.
+// of 256 (one scale of an 8-bit state), a lane 8 elements.
 #include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "adamw.h"
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "host_common.h"
 #include "sum2.cuh"
 
@@ -56,113 +58,99 @@ __global__ void build_kernel(const __grid_constant__ BuildArgs a, AdamChunk *tab
   const uintptr_t state = reinterpret_cast<uintptr_t>(t.exp_avg) | reinterpret_cast<uintptr_t>(t.exp_avg_sq);
   const uintptr_t rest = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad) |
                          reinterpret_cast<uintptr_t>(t.master);
-  r.wide = (rest & 15u) == 0 && (state & (a.e_s == 1 ? 7u : 15u)) == 0;
+  r.wide = (rest & 15u) == 0 && (state & (a.e_s == 1 ? 3u : 15u)) == 0;
   table[c] = r;
 }
 
-// ----------------------------------------------------------------------------- 8 elements of a lane
-__device__ __forceinline__ void load8(const float *p, float *v) {
-  const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *v) {
-  const uint4 q = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack_bf16(w[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+// ----------------------------------------------------------------------------- 4 + 4 elements of a lane
+// A warp's 256 elements in two halves of 128, four consecutive ones of each for a
+// lane: every load and store of a warp covers whole stretches of memory, whatever
+// the type (16 bytes a lane in fp32, 8 in bf16, 4 of codes).
+template <typename T>
+struct Four;      // four elements as they lie in memory; as two pairs of fp32 values
+template <>
+struct Four<float> {
+  uint4 q;
+  __device__ __forceinline__ void get(uint64_t *v) const {
+    v[0] = pk2(__uint_as_float(q.x), __uint_as_float(q.y));
+    v[1] = pk2(__uint_as_float(q.z), __uint_as_float(q.w));
   }
-}
-__device__ __forceinline__ void store8(float *p, const float *v) {
-  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *v) {
-  *reinterpret_cast<uint4 *>(p) =
-      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-__device__ __forceinline__ float load1(const float *p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
-__device__ __forceinline__ void store1(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+  __device__ __forceinline__ void set(const uint64_t *v) {
+    const float2 a = unpk2(v[0]), b = unpk2(v[1]);
+    q = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 q;
+  __device__ __forceinline__ void get(uint64_t *v) const {
+    v[0] = pk2(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u));
+    v[1] = pk2(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
+  }
+  __device__ __forceinline__ void set(const uint64_t *v) {
+    const float2 a = unpk2(v[0]), b = unpk2(v[1]);
+    q = make_uint2(pack_bf16(a.x, a.y), pack_bf16(b.x, b.y));
+  }
+};
+template <>
+struct Four<uint8_t> {      // e4m3 codes
+  uint32_t q;
+  __device__ __forceinline__ void get(uint64_t *v) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(i == 0 ? q : q >> 16), __NV_E4M3);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+      v[i] = pk2(f.x, f.y);
+    }
+  }
+  __device__ __forceinline__ void set(const uint64_t *v) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(unpk2(v[0]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(unpk2(v[1]), __NV_SATFINITE, __NV_E4M3);
+    q = lo | (hi << 16);
+  }
+};
 
-// Elements [0, n) of a lane's eight; the others read as zero and are not written.
-template <typename E>
-__device__ __forceinline__ void load_lane(const E *p, float *v, int n, bool wide) {
-  if (wide && n == kLane) {
-    load8(p, v);
+// Four elements, kWhole: all there and at an aligned address; else elements
+// [0, n) one by one (n <= 4), the others read as zero and not written.
+template <bool kWhole, typename T>
+__device__ __forceinline__ Four<T> load4(const T *p, int n) {
+  Four<T> r;
+  if constexpr (kWhole) {
+    r.q = *reinterpret_cast<const decltype(r.q) *>(p);
   } else {
+    T *e = reinterpret_cast<T *>(&r.q);
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) v[i] = i < n ? load1(p + i) : 0.f;
+    for (int i = 0; i < 4; ++i) e[i] = i < n ? p[i] : T(0.f);
   }
+  return r;
 }
-template <typename E>
-__device__ __forceinline__ void store_lane(E *p, const float *v, int n, bool wide) {
-  if (wide && n == kLane) {
-    store8(p, v);
+template <bool kWhole, typename T>
+__device__ __forceinline__ void store4(T *p, const Four<T> &r, int n) {
+  if constexpr (kWhole) {
+    *reinterpret_cast<decltype(r.q) *>(p) = r.q;
   } else {
+    const T *e = reinterpret_cast<const T *>(&r.q);
 #pragma unroll
-    for (int i = 0; i < kLane; ++i)
-      if (i < n) store1(p + i, v[i]);
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = e[i];
   }
 }
 
-// e4m3 codes: eight of a lane are 8 bytes.
-__device__ __forceinline__ void decode8(const uint8_t *c, float *v, float scale) {
-#pragma unroll
-  for (int i = 0; i < kLane; i += 2) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[i] | (c[i + 1] << 8)), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    v[i] = __fmul_rn(f.x, scale);
-    v[i + 1] = __fmul_rn(f.y, scale);
-  }
-}
-__device__ __forceinline__ void load_codes(const uint8_t *p, float *v, float scale, int n, bool wide) {
-  uint8_t c[kLane];
-  if (wide && n == kLane) {
-    *reinterpret_cast<uint2 *>(c) = *reinterpret_cast<const uint2 *>(p);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) c[i] = i < n ? p[i] : 0;
-  }
-  decode8(c, v, scale);
-}
-
-// The warp's 256 values as codes and one scale.  The largest magnitude is taken
-// on the bit patterns, whose order is that of the magnitudes with NaN above
-// infinity: a NaN makes the block's scale NaN.
-template <bool kRoot>
-__device__ __forceinline__ void store_codes(uint8_t *p, float *scale, const float *v, int n, bool wide) {
+// The factor 448 / a that brings the warp's 256 values to the codes' range, and
+// their scale a / 448.  The largest magnitude is taken on the bit patterns, whose
+// order is that of the magnitudes with NaN above infinity: a NaN makes the
+// block's scale NaN.
+__device__ __forceinline__ float code_range(const uint64_t *v, float &scale) {
   uint32_t top = __float_as_uint(1e-30f);
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  for (int i = 0; i < kLane / 2; ++i) {
+    const float2 f = unpk2(v[i]);
+    top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+  }
   top = __reduce_max_sync(0xffffffffu, top);
-  const float a = __uint_as_float(top), up = __fdiv_rn(448.f, a);
-  uint8_t c[kLane];
-#pragma unroll
-  for (int i = 0; i < kLane; i += 2) {
-    float q[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      q[j] = __fmul_rn(v[i + j], up);
-      // the smallest positive code, 2^-9, for a root that would round to zero
-      if (kRoot && v[i + j] > 0.f) q[j] = fmaxf(q[j], 0.001953125f);
-    }
-    const __nv_fp8x2_storage_t two = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
-    c[i] = (uint8_t)(two & 0xff);
-    c[i + 1] = (uint8_t)(two >> 8);
-  }
-  if (wide && n == kLane) {
-    *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(c);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLane; ++i)
-      if (i < n) p[i] = c[i];
-  }
-  if (lane_id() == 0) *scale = __fmul_rn(a, (float)(1.0 / 448.0));
+  const float a = __uint_as_float(top);
+  scale = __fmul_rn(a, (float)(1.0 / 448.0));
+  return __fdiv_rn(448.f, a);
 }
 
 // ----------------------------------------------------------------------------- the step
@@ -171,55 +159,133 @@ struct StepArgs {
   const float *factor;
   float b1, b1c, b2, b2c;      // beta1, 1 - beta1, beta2, 1 - beta2
   float decay;                 // 1 - lr * weight_decay
-  float rate;                  // lr / (1 - beta1^step)
+  float rate;                  // -lr / (1 - beta1^step)
   float root;                  // 1 / sqrt(1 - beta2^step)
   float eps;
+  float one;                   // 1
 };
 
-// The states' arithmetic is written in single IEEE roundings (no contraction to
-// multiply-add): equal inputs give equal 8-bit codes, whoever computes them.
+// A warp's 256 elements as they lie in memory.
 template <typename P, typename G, bool k8, bool kMaster>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(StepArgs a) {
+struct Block {
+  using S = std::conditional_t<k8, uint8_t, float>;
+  using W = std::conditional_t<kMaster, float, P>;
+  Four<G> g[2];
+  Four<S> m[2], v[2];
+  Four<W> w[2];
+  float ms, vs;
+
+  // `block`: its number in the chunk
+  template <bool kWhole>
+  __device__ __forceinline__ void load(const AdamChunk &c, int block) {
+    const int at = block * LORA_ADAMW_BLOCK + 4 * lane_id();
+    const W *wp = kMaster ? reinterpret_cast<const W *>(c.master) : static_cast<const W *>(c.p);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int o = at + 128 * h, n = min(max((int)c.count - o, 0), 4);
+      g[h] = load4<kWhole>(static_cast<const G *>(c.g) + o, n);
+      m[h] = load4<kWhole>(static_cast<const S *>(c.m) + o, n);
+      v[h] = load4<kWhole>(static_cast<const S *>(c.v) + o, n);
+      w[h] = load4<kWhole>(wp + o, n);
+    }
+    if (k8) {
+      ms = c.m_scale[block];
+      vs = c.v_scale[block];
+    }
+  }
+
+  // The step, and its results back to memory.  The states' arithmetic is in
+  // single IEEE roundings, on pairs of values; a sum of products is written
+  // fma(x, 1, y) with the 1 from memory, because the compiler contracts a packed
+  // product and sum to one rounding: equal inputs give equal 8-bit codes,
+  // whoever computes them.
+  template <bool kWhole>
+  __device__ __forceinline__ void step(const StepArgs &a, float factor, const AdamChunk &c, int block) {
+    constexpr int kPairs = kLane / 2;
+    auto both = [](float x) { return pk2(x, x); };
+    uint64_t pw[kPairs], pg[kPairs], pm[kPairs], pv[kPairs];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      g[h].get(pg + 2 * h);
+      m[h].get(pm + 2 * h);
+      v[h].get(pv + 2 * h);
+      w[h].get(pw + 2 * h);
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const uint64_t gi = mul2(pg[i], both(factor));
+      if (k8) {
+        pm[i] = mul2(pm[i], both(ms));
+        pv[i] = mul2(pv[i], both(vs));
+        pv[i] = mul2(pv[i], pv[i]);
+      }
+      pm[i] = fma2(mul2(pm[i], both(a.b1)), both(a.one), mul2(gi, both(a.b1c)));
+      pv[i] = fma2(mul2(pv[i], both(a.b2)), both(a.one), mul2(mul2(gi, gi), both(a.b2c)));
+      const float2 vv = unpk2(pv[i]), mm = unpk2(pm[i]);
+      const uint64_t u = pk2(__fsqrt_rn(vv.x), __fsqrt_rn(vv.y));
+      if (k8) pv[i] = u;
+      // the quotient is off by two roundings: far below a parameter's own
+      const float2 d = unpk2(fma2(u, both(a.root), both(a.eps)));
+      pw[i] = fma2(pk2(__fdividef(mm.x, d.x), __fdividef(mm.y, d.y)), both(a.rate), mul2(pw[i], both(a.decay)));
+    }
+    if (k8) {
+      const uint64_t mup = both(code_range(pm, ms)), vup = both(code_range(pv, vs));
+      if (lane_id() == 0) {
+        c.m_scale[block] = ms;
+        c.v_scale[block] = vs;
+      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        pm[i] = mul2(pm[i], mup);
+        // the smallest positive code, 2^-9, for a root that would round to zero
+        const float2 u = unpk2(pv[i]);
+        float2 q = unpk2(mul2(pv[i], vup));
+        if (u.x > 0.f) q.x = fmaxf(q.x, 0.001953125f);
+        if (u.y > 0.f) q.y = fmaxf(q.y, 0.001953125f);
+        pv[i] = pk2(q.x, q.y);
+      }
+    }
+    const int at = block * LORA_ADAMW_BLOCK + 4 * lane_id();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int o = at + 128 * h, n = min(max((int)c.count - o, 0), 4);
+      Four<P> rp;
+      rp.set(pw + 2 * h);
+      store4<kWhole>(static_cast<P *>(c.p) + o, rp, n);
+      if constexpr (kMaster) {
+        w[h].set(pw + 2 * h);
+        store4<kWhole>(c.master + o, w[h], n);
+      }
+      m[h].set(pm + 2 * h);
+      store4<kWhole>(static_cast<S *>(c.m) + o, m[h], n);
+      v[h].set(pv + 2 * h);
+      store4<kWhole>(static_cast<S *>(c.v) + o, v[h], n);
+    }
+  }
+};
+
+// A block of threads takes a chunk; with states in 8 bits (few bytes a warp) each
+// warp loads two blocks of it before it works on the first.
+constexpr int kEach8 = 2, kEach32 = 1;
+template <typename P, typename G, bool k8, bool kMaster>
+__global__ void __launch_bounds__(kThreads / (k8 ? kEach8 : kEach32)) adamw_kernel(StepArgs a) {
+  constexpr int kEach = k8 ? kEach8 : kEach32, kWarps = kThreads / 32 / kEach;
   pdl_wait();
   const AdamChunk c = a.table[blockIdx.x];
-  const int warp = threadIdx.x >> 5;
-  const int at = (int)threadIdx.x * kLane;
-  if (warp * LORA_ADAMW_BLOCK >= (int)c.count) return;      // whole warps: a block's scale needs all 32 lanes
-  const int n = min(max((int)c.count - at, 0), kLane);
-  const bool wide = c.wide != 0;
   const float factor = a.factor ? *a.factor : 1.f;
-  P *p = static_cast<P *>(c.p) + at;
-  float w[kLane], g[kLane], m[kLane], v[kLane];
-  load_lane(static_cast<const G *>(c.g) + at, g, n, wide);
-  if (kMaster)
-    load_lane(c.master + at, w, n, wide);
-  else
-    load_lane(p, w, n, wide);
-  if (k8) {
-    load_codes(static_cast<uint8_t *>(c.m) + at, m, c.m_scale[warp], n, wide);
-    load_codes(static_cast<uint8_t *>(c.v) + at, v, c.v_scale[warp], n, wide);
-  } else {
-    load_lane(static_cast<float *>(c.m) + at, m, n, wide);
-    load_lane(static_cast<float *>(c.v) + at, v, n, wide);
-  }
+  const int warp = threadIdx.x >> 5;
+  Block<P, G, k8, kMaster> b[kEach];
+  if (c.wide && c.count == LORA_ADAMW_CHUNK) {
 #pragma unroll
-  for (int i = 0; i < kLane; ++i) {
-    const float gi = __fmul_rn(g[i], factor);
-    if (k8) v[i] = __fmul_rn(v[i], v[i]);
-    m[i] = __fadd_rn(__fmul_rn(m[i], a.b1), __fmul_rn(gi, a.b1c));
-    v[i] = __fadd_rn(__fmul_rn(v[i], a.b2), __fmul_rn(__fmul_rn(gi, gi), a.b2c));
-    const float u = __fsqrt_rn(v[i]);
-    if (k8) v[i] = u;
-    w[i] = w[i] * a.decay - a.rate * (m[i] / (u * a.root + a.eps));
-  }
-  if (kMaster) store_lane(c.master + at, w, n, wide);
-  store_lane(p, w, n, wide);
-  if (k8) {
-    store_codes<false>(static_cast<uint8_t *>(c.m) + at, c.m_scale + warp, m, n, wide);
-    store_codes<true>(static_cast<uint8_t *>(c.v) + at, c.v_scale + warp, v, n, wide);
+    for (int i = 0; i < kEach; ++i) b[i].template load<true>(c, warp + i * kWarps);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) b[i].template step<true>(a, factor, c, warp + i * kWarps);
   } else {
-    store_lane(static_cast<float *>(c.m) + at, m, n, wide);
-    store_lane(static_cast<float *>(c.v) + at, v, n, wide);
+    // whole warps: a block's scale needs all 32 lanes
+    for (int i = warp; i * LORA_ADAMW_BLOCK < (int)c.count; i += kWarps) {
+      b[0].template load<false>(c, i);
+      b[0].template step<false>(a, factor, c, i);
+    }
   }
 }
 
@@ -235,12 +301,22 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
   Sum2 sum;
   for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
     const G *g = static_cast<const G *>(table[k].g);
-    const int at = (int)threadIdx.x * kLane, n = min(max((int)table[k].count - at, 0), kLane);
-    float v[kLane], s = 0.f;
-    load_lane(g + at, v, n, (reinterpret_cast<uintptr_t>(g) & 15u) == 0);
+    const int at = (int)(threadIdx.x >> 5) * LORA_ADAMW_BLOCK + 4 * lane_id(), count = (int)table[k].count;
+    Four<G> r[2];
+    uint64_t v[kLane / 2], s = 0;
+    if ((reinterpret_cast<uintptr_t>(g) & 15u) == 0 && count == LORA_ADAMW_CHUNK) {
 #pragma unroll
-    for (int i = 0; i < kLane; ++i) s += v[i] * v[i];
-    sum.add(s);
+      for (int h = 0; h < 2; ++h) r[h] = load4<true>(g + at + 128 * h, 4);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) r[h] = load4<false>(g + at + 128 * h, min(max(count - at - 128 * h, 0), 4));
+    }
+    r[0].get(v);
+    r[1].get(v + 2);
+#pragma unroll
+    for (int i = 0; i < kLane / 2; ++i) s = fma2(v[i], v[i], s);
+    const float2 two = unpk2(s);
+    sum.add(two.x + two.y);
   }
   sum = block_sum<kThreads / 32>(sum, sh);
   if (threadIdx.x == 0) {
@@ -269,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
 
 template <typename P, typename G, bool k8>
 cudaError_t run_step(const lora_adamw_plan_t &plan, const StepArgs &a, cudaStream_t st) {
-  const dim3 grid((unsigned)plan.chunks), block(kThreads);
+  const dim3 grid((unsigned)plan.chunks), block(kThreads / (k8 ? kEach8 : kEach32));
   return (plan.flags & LORA_ADAMW_MASTER) ? launch(adamw_kernel<P, G, k8, true>, grid, block, 0, st, 1, true, a)
                                           : launch(adamw_kernel<P, G, k8, false>, grid, block, 0, st, 1, true, a);
 }
@@ -343,9 +419,10 @@ lora_status_t adamw(const lora_adamw_plan_t &plan, const lora_adamw_hyper_t &h, 
   a.b2 = (float)h.beta2;
   a.b2c = (float)(1.0 - h.beta2);
   a.decay = (float)(1.0 - h.lr * h.weight_decay);
-  a.rate = (float)(h.lr / (1.0 - pow(h.beta1, (double)h.step)));
+  a.rate = (float)(-h.lr / (1.0 - pow(h.beta1, (double)h.step)));
   a.root = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
   a.eps = (float)h.eps;
+  a.one = 1.f;
   const bool p16 = plan.param_dtype == LORA_BF16, g16 = plan.grad_dtype == LORA_BF16;
   cudaError_t e;
   if (p16)
