@@ -112,11 +112,13 @@ struct Four<uint8_t> {      // e4m3 codes
 
 // Four elements, kWhole: all there and at an aligned address; else elements
 // [0, n) one by one (n <= 4), the others read as zero and not written.
-template <bool kWhole, typename T>
+// kOnce: nobody reads it again.
+template <bool kWhole, bool kOnce = true, typename T>
 __device__ __forceinline__ Four<T> load4(const T *p, int n) {
   Four<T> r;
   if constexpr (kWhole) {
-    r.q = *reinterpret_cast<const decltype(r.q) *>(p);
+    const decltype(r.q) *q = reinterpret_cast<const decltype(r.q) *>(p);
+    r.q = kOnce ? __ldcs(q) : *q;
   } else {
     T *e = reinterpret_cast<T *>(&r.q);
 #pragma unroll
@@ -127,7 +129,7 @@ __device__ __forceinline__ Four<T> load4(const T *p, int n) {
 template <bool kWhole, typename T>
 __device__ __forceinline__ void store4(T *p, const Four<T> &r, int n) {
   if constexpr (kWhole) {
-    *reinterpret_cast<decltype(r.q) *>(p) = r.q;
+    __stcs(reinterpret_cast<decltype(r.q) *>(p), r.q);
   } else {
     const T *e = reinterpret_cast<const T *>(&r.q);
 #pragma unroll
@@ -271,7 +273,8 @@ template <typename P, typename G, bool k8, bool kMaster>
 __global__ void __launch_bounds__(kThreads / (k8 ? kEach8 : kEach32)) adamw_kernel(StepArgs a) {
   constexpr int kEach = k8 ? kEach8 : kEach32, kWarps = kThreads / 32 / kEach;
   pdl_wait();
-  const AdamChunk c = a.table[blockIdx.x];
+  // last to first: the norm before this step has left the last gradients in L2
+  const AdamChunk c = a.table[gridDim.x - 1 - blockIdx.x];
   const float factor = a.factor ? *a.factor : 1.f;
   const int warp = threadIdx.x >> 5;
   Block<P, G, k8, kMaster> b[kEach];
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
     uint64_t v[kLane / 2], s = 0;
     if ((reinterpret_cast<uintptr_t>(g) & 15u) == 0 && count == LORA_ADAMW_CHUNK) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) r[h] = load4<true>(g + at + 128 * h, 4);
+      for (int h = 0; h < 2; ++h) r[h] = load4<true, false>(g + at + 128 * h, 4);
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) r[h] = load4<false>(g + at + 128 * h, min(max(count - at - 128 * h, 0), 4));
