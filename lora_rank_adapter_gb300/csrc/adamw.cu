@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
   __shared__ Sum2 sh[kThreads / 32];
   __shared__ unsigned before;
   pdl_wait();
-  Sum2 sum;
+  Sum2 sum[1];
   for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
     const G *g = static_cast<const G *>(table[k].g);
     const int at = (int)(threadIdx.x >> 5) * LORA_ADAMW_BLOCK + 4 * lane_id(), count = (int)table[k].count;
@@ -319,28 +319,28 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
 #pragma unroll
     for (int i = 0; i < kLane / 2; ++i) s = fma2(v[i], v[i], s);
     const float2 two = unpk2(s);
-    sum.add(two.x + two.y);
+    sum[0].add(two.x + two.y);
   }
-  sum = block_sum<kThreads / 32>(sum, sh);
+  block_sums<kThreads / 32, 1>(sum, sh);
   if (threadIdx.x == 0) {
-    part[blockIdx.x] = sum;
+    part[blockIdx.x] = sum[0];
     __threadfence();
     before = atomicAdd(ticket, 1u);
     __threadfence();
   }
   __syncthreads();
   if (before != gridDim.x - 1) return;
-  sum = Sum2();
+  sum[0] = Sum2();
   for (int i = threadIdx.x; i < (int)gridDim.x; i += kThreads) {
     const float2 p = __ldcg(reinterpret_cast<const float2 *>(part) + i);
     Sum2 one;
     one.hi = p.x;
     one.lo = p.y;
-    sum.add(one);
+    sum[0].add(one);
   }
-  sum = block_sum<kThreads / 32>(sum, sh);
+  block_sums<kThreads / 32, 1>(sum, sh);
   if (threadIdx.x == 0) {
-    const float norm = sqrtf(sum.value()), f = max_norm / (norm + 1e-6f);
+    const float norm = sqrtf(sum[0].value()), f = max_norm / (norm + 1e-6f);
     out[0] = norm;
     out[1] = f >= 1.f ? 1.f : f;      // a NaN norm gives a NaN factor
   }

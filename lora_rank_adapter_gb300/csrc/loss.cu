@@ -215,8 +215,8 @@ struct RowArgs {
   float inv_t;
   float *logps;        // stats pass
   float2 *stats;       // written by the stats pass (NULL: not wanted), read by the gradient pass
-  float *coef;         // stats pass: zeroed (NULL: none); gradient pass: d loss / d logp
-  unsigned *ticket;    // zeroed for the kernel that follows (NULL: none)
+  float *coef;         // d loss / d logp: zeroed by the statistics pass (NULL: none), read by the gradient pass
+  unsigned *ticket;    // zeroed by the statistics pass (NULL: none)
   void *dlogits;
   int64_t lddl;
   float grad_scale;
@@ -224,12 +224,10 @@ struct RowArgs {
 
 constexpr int kMaxCluster = 8;
 
-// (m, s) of the blocks of a cluster, by warp 0 of each.  Each block writes its
-// pair to all the others; `ready` counts one arrival from each.  The caller has
-// let the cluster arrive and wait after `ready` was set up, once; exchanges
-// alternate between two sets of slots, the n-th of a set on parity n & 1.  (A
-// block reaches the exchange after next only when every block has arrived at the
-// next one, so after it has read this one's slots.)  False: the wait ran out.
+// (m, s) of the blocks of a cluster, by warp 0 of each, once.  Each block writes
+// its pair to all the others; `ready` counts one arrival from each.  The caller
+// has let the cluster arrive and wait after `ready` was set up.  False: the wait
+// ran out.
 struct ClusterSlots {
   uint64_t ready;
   float2 pair[kMaxCluster];
@@ -241,8 +239,8 @@ __device__ __forceinline__ void st_dsmem_f2(const void *local_ptr, uint32_t cta,
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(cta));
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
 }
-// The same as one asynchronous store whose bytes complete `bar` of that block
-// (of a cluster: the kernel has been launched as one).
+// A pair stored to another block of the cluster, its bytes completing `bar` there
+// (only in a kernel that was launched as clusters).
 __device__ __forceinline__ void st_async_f2(const void *local_ptr, const uint64_t *local_bar, uint32_t cta, float2 v) {
   uint32_t p, b;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(smem_u32(local_ptr)), "r"(cta));
@@ -251,14 +249,13 @@ __device__ __forceinline__ void st_async_f2(const void *local_ptr, const uint64_
                "f"(v.x), "f"(v.y), "r"(b)
                : "memory");
 }
-__device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int rank, int C, ClusterSlots *slots,
-                                              uint32_t parity) {
+__device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int rank, int C, ClusterSlots *slots) {
   const int lane = lane_id();
   if (lane < C) {
     st_dsmem_f2(&slots->pair[rank], lane, make_float2(m, s));
     mbar_arrive_remote(&slots->ready, lane);
   }
-  if (!__all_sync(0xffffffffu, mbar_wait<true>(&slots->ready, parity))) return false;
+  if (!__all_sync(0xffffffffu, mbar_wait<true>(&slots->ready, 0))) return false;
   const float2 v = lane < C ? slots->pair[lane] : make_float2(kNegInf, 0.f);
   m = v.x;
   s = v.y;
@@ -267,56 +264,54 @@ __device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int r
 }
 
 // The statistics of a row, read once from global memory by the C blocks of a
-// cluster, a slice of `slice` 16-byte pieces each.
+// cluster, a slice of `slice` 16-byte pieces each.  An ignored row is not read,
+// but its blocks meet all the same: no block leaves before the others have sent
+// to it, whatever each has seen of labels that another stream may be writing.
 template <typename E>
 __global__ void __launch_bounds__(kRowThreads) stats_kernel(RowArgs a, int C, int slice) {
   __shared__ float2 sh[kRowThreads / 32];
   __shared__ ClusterSlots slots;
   pdl_wait();
   const int64_t t = blockIdx.x / C;
-  const int rank = (int)(blockIdx.x % C);
-  if (rank == 0 && threadIdx.x == 0) {
-    if (a.coef) a.coef[t] = 0.f;
-    if (a.ticket && t == 0) *a.ticket = 0;
-  }
+  const int rank = (int)(blockIdx.x % C), tid = threadIdx.x;
   const int64_t label = a.labels[t];
-  if (label < 0 || label >= a.V) {
-    if (rank == 0 && threadIdx.x == 0) {
-      a.logps[t] = 0.f;
-      if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
-    }
-    return;
-  }
   if (C > 1) {
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       mbar_init(&slots.ready, C);
       fence_barrier_init();
     }
     __syncthreads();
     cluster_arrive();
   }
-  const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
-  const RowSpan<E> sp(row, (int)a.V);
-  const float k = a.inv_t * kLog2e;
-  const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
-  float label_value = 0.f, m = kNegInf;
-  if (rank == 0 && threadIdx.x == 0) label_value = Elem<E>::load(row + label);
-  uint64_t s2 = 0;
-  absorb_span<E, kRowThreads, 4>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
-  const float2 both = unpk2(s2);
-  float s = both.x + both.y;
-  if (rank == C - 1) {      // the ragged ends
-    if ((int)threadIdx.x < sp.head) absorb_one(m, s, Elem<E>::load(row + threadIdx.x), k);
-    if ((int)threadIdx.x < a.V - tail) absorb_one(m, s, Elem<E>::load(row + tail + threadIdx.x), k);
+  if (rank == 0 && tid == 0) {
+    if (a.coef) a.coef[t] = 0.f;
+    if (a.ticket && t == 0) *a.ticket = 0;
   }
-  block_merge<kRowThreads / 32>(m, s, k, sh);
+  const bool counts = label >= 0 && label < a.V;
+  const float k = a.inv_t * kLog2e;
+  float picked = 0.f, m = kNegInf, s = 0.f;
+  if (counts) {
+    const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
+    const RowSpan<E> sp(row, (int)a.V);
+    const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
+    if (rank == 0 && tid == 0) picked = Elem<E>::load(row + label);
+    uint64_t s2 = 0;
+    absorb_span<E, kRowThreads, 4>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
+    const float2 both = unpk2(s2);
+    s = both.x + both.y;
+    if (rank == C - 1) {      // the ragged ends
+      if (tid < sp.head) absorb_one(m, s, Elem<E>::load(row + tid), k);
+      if (tid < (int)a.V - tail) absorb_one(m, s, Elem<E>::load(row + tail + tid), k);
+    }
+    block_merge<kRowThreads / 32>(m, s, k, sh);
+  }
   if (C > 1) {
     cluster_wait();
-    if (threadIdx.x < 32 && !cluster_merge(m, s, k, rank, C, &slots, 0)) return;
+    if (tid < 32 && !cluster_merge(m, s, k, rank, C, &slots)) return;
   }
-  if (rank == 0 && threadIdx.x == 0) {
-    a.logps[t] = (label_value - m) * a.inv_t - logf(s);
-    if (a.stats) a.stats[t] = make_float2(m, s);
+  if (rank == 0 && tid == 0) {
+    a.logps[t] = counts ? (picked - m) * a.inv_t - logf(s) : 0.f;
+    if (a.stats) a.stats[t] = counts ? make_float2(m, s) : make_float2(0.f, 1.f);
   }
 }
 
@@ -425,78 +420,83 @@ constexpr int kPairThreads = 256;
 // ln sigmoid(h) = min(h, 0) - ln(1 + exp(-|h|)), free of overflow and of cancellation
 __device__ __forceinline__ float log_sigmoid(float h) { return fminf(h, 0.f) - log1pf(expf(-fabsf(h))); }
 
-// The last block to get here, known to all its threads; the others' writes are visible to it.
-__device__ __forceinline__ bool last_block(unsigned *ticket, unsigned blocks) {
-  __shared__ unsigned before;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    before = atomicAdd(ticket, 1u);
-    __threadfence();
-  }
-  __syncthreads();
-  return before == blocks - 1;
-}
-
 // One block per pair: both sequences' sums (exact to fp32: their difference is what
-// counts), the pair's loss, and each token's d loss / d logp.  The last block
-// takes the mean.
+// counts), the pair's loss, and each of its tokens' d loss / d logp.  The last
+// block takes the mean.  A chain of short dependent steps: what can be on its way
+// together is.
 __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, int64_t T, int64_t V,
                                                              const int64_t *labels, const float *logps, float *coef,
                                                              unsigned *ticket) {
-  __shared__ Sum2 sh[kPairThreads / 32];
+  __shared__ Sum2 sh[4 * (kPairThreads / 32)];
+  __shared__ float slope_of[2];
+  __shared__ unsigned before;
+  const int pair = blockIdx.x, tid = threadIdx.x;
   pdl_wait();
-  const int pair = blockIdx.x;
-  int64_t lo[2], hi[2];
-  float S[2], n[2];
+  const int32_t *cu = p.cu;
+  const int32_t edge[4] = {cu[pair], cu[pair + 1], cu[pair + p.P], cu[pair + p.P + 1]};
+  const float ref = p.ref ? p.ref[pair] - p.ref[pair + p.P] : 0.f;
+  int64_t lo[2], n[2];
+  Sum2 sum[4];                     // sums and counts of both sides
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
-    const int seq = pair + side * p.P;
-    lo[side] = min(max((int64_t)p.cu[seq], (int64_t)0), T);
-    hi[side] = min(max((int64_t)p.cu[seq + 1], (int64_t)0), T);
-    Sum2 sum, count;
-    for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) sum.add(logps[t]);
-    if (p.normalize)
-      for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads)
-        count.add(labels[t] >= 0 && labels[t] < V ? 1.f : 0.f);
-    sum = block_sum<kPairThreads / 32>(sum, sh);
-    n[side] = 1.f;
-    if (p.normalize) n[side] = fmaxf(1.f, block_sum<kPairThreads / 32>(count, sh).value());
-    S[side] = sum.value() / n[side];
-    if (threadIdx.x == 0) p.seq_logps[seq] = S[side];
+    lo[side] = min(max((int64_t)edge[2 * side], (int64_t)0), T);
+    n[side] = max(min((int64_t)edge[2 * side + 1], T) - lo[side], (int64_t)0);
   }
-  float d = S[0] - S[1];
-  if (p.ref) d -= p.ref[pair] - p.ref[pair + p.P];
-  float loss, slope;
-  if (p.kind == LORA_PREF_SIGMOID) {
-    const float h = p.beta * d;
-    loss = -(1.f - p.smoothing) * log_sigmoid(h) - p.smoothing * log_sigmoid(-h);
-    // d loss / d h = sigmoid(h) - (1 - eps), written without cancellation at large |h|
-    slope = p.beta * (p.smoothing / (1.f + expf(-h)) - (1.f - p.smoothing) / (1.f + expf(h)));
-  } else if (p.kind == LORA_PREF_HINGE) {
-    loss = fmaxf(0.f, 1.f - p.beta * d);
-    if (d != d) loss = d;
-    slope = 1.f - p.beta * d > 0.f ? -p.beta : 0.f;
-    if (d != d) slope = d;
-  } else {
-    const float u = d - 0.5f / p.beta;
-    loss = u * u;
-    slope = 2.f * u;
-  }
-  if (coef) {
+  for (int64_t i = tid; i < max(n[0], n[1]); i += kPairThreads)
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+      if (i < n[side]) {
+        const int64_t t = lo[side] + i;
+        sum[side].add(logps[t]);
+        if (p.normalize) sum[2 + side].add(labels[t] >= 0 && labels[t] < V ? 1.f : 0.f);
+      }
+  block_sums<kPairThreads / 32, 4>(sum, sh);
+  if (tid == 0) {
+    float S[2], count[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      const float c = (side == 0 ? slope : -slope) / (float)p.P / n[side];
-      for (int64_t t = lo[side] + threadIdx.x; t < hi[side]; t += kPairThreads) coef[t] = c;
+      count[side] = p.normalize ? fmaxf(1.f, sum[2 + side].value()) : 1.f;
+      S[side] = sum[side].value() / count[side];
+      p.seq_logps[pair + side * p.P] = S[side];
+    }
+    const float d = S[0] - S[1] - ref;
+    float loss, slope;
+    if (p.kind == LORA_PREF_SIGMOID) {
+      const float h = p.beta * d;
+      loss = -(1.f - p.smoothing) * log_sigmoid(h) - p.smoothing * log_sigmoid(-h);
+      // d loss / d h = sigmoid(h) - (1 - eps), written without cancellation at large |h|
+      slope = p.beta * (p.smoothing / (1.f + expf(-h)) - (1.f - p.smoothing) / (1.f + expf(h)));
+    } else if (p.kind == LORA_PREF_HINGE) {
+      loss = fmaxf(0.f, 1.f - p.beta * d);
+      if (d != d) loss = d;
+      slope = 1.f - p.beta * d > 0.f ? -p.beta : 0.f;
+      if (d != d) slope = d;
+    } else {
+      const float u = d - 0.5f / p.beta;
+      loss = u * u;
+      slope = 2.f * u;
+    }
+    p.pair_loss[pair] = loss;
+    slope_of[0] = slope / (float)p.P / count[0];
+    slope_of[1] = -slope / (float)p.P / count[1];
+    if (gridDim.x == 1) {
+      p.loss[0] = loss;
+    } else {
+      __threadfence();
+      before = atomicAdd(ticket, 1u);
+      __threadfence();
     }
   }
-  if (threadIdx.x == 0) p.pair_loss[pair] = loss;
-  if (last_block(ticket, gridDim.x)) {
-    Sum2 sum;
-    for (int i = threadIdx.x; i < p.P; i += kPairThreads) sum.add(__ldcg(p.pair_loss + i));
-    sum = block_sum<kPairThreads / 32>(sum, sh);
-    if (threadIdx.x == 0) p.loss[0] = sum.value() / (float)p.P;
-  }
+  __syncthreads();
+  if (coef)
+#pragma unroll
+    for (int side = 0; side < 2; ++side)
+      for (int64_t i = tid; i < n[side]; i += kPairThreads) coef[lo[side] + i] = slope_of[side];
+  if (gridDim.x == 1 || before != gridDim.x - 1) return;
+  Sum2 all[1];
+  for (int i = tid; i < p.P; i += kPairThreads) all[0].add(__ldcg(p.pair_loss + i));
+  block_sums<kPairThreads / 32, 1>(all, sh);
+  if (tid == 0) p.loss[0] = all[0].value() / (float)p.P;
 }
 
 // A token's part of the policy loss: the terms of the three metrics, and its
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
 // The three metrics: sums of the rows' terms in a fixed order.
 constexpr int kSumThreads = 1024;
 __global__ void __launch_bounds__(kSumThreads) terms_kernel(const float4 *terms, int64_t T, float *metrics) {
-  __shared__ Sum2 sh[kSumThreads / 32];
+  __shared__ Sum2 sh[3 * (kSumThreads / 32)];
   pdl_wait();
   Sum2 s[3];
 #pragma unroll 4
@@ -778,10 +778,10 @@ __global__ void __launch_bounds__(kSumThreads) terms_kernel(const float4 *terms,
     s[1].add(v.y);
     s[2].add(v.z);
   }
+  block_sums<kSumThreads / 32, 3>(s, sh);
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const Sum2 all = block_sum<kSumThreads / 32>(s[i], sh);
-    if (threadIdx.x == 0) metrics[i] = all.value();
+    for (int i = 0; i < 3; ++i) metrics[i] = s[i].value();
   }
 }
 
@@ -893,9 +893,21 @@ int slice_of(lora_dtype_t dtype, int64_t V, int parts) {
   return (int)std::max<int64_t>(8, round_up(ceil_div(pieces, parts), 8));
 }
 
+// Blocks of a row in the statistics pass: one, where there is a row for each SM
+// (1415 rows of 50048 fp32: 44 us with one, 50 with two, 65 with eight; 4000 of
+// 32000 bf16: 42, 56); fewer rows are cut over clusters, down to 4 KB a block,
+// until there are four blocks for each SM (7 rows of 32003 fp32: 8 us with one
+// block each, 3 with eight).
+int stats_cluster(lora_dtype_t dtype, int64_t T, int64_t V) {
+  const int64_t bytes = V * (dtype == LORA_BF16 ? 2 : 4);
+  if (T >= num_sms()) return 1;
+  const int64_t c = std::min(4 * num_sms() / T, bytes / (4 << 10));
+  return (int)std::min<int64_t>(std::max<int64_t>(c, 1), kMaxCluster);
+}
+
 lora_status_t run_stats(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0) return LORA_OK;
-  const int c = parts_of(dtype, r.T, r.V, kMaxCluster);
+  const int c = stats_cluster(dtype, r.T, r.V);
   const int slice = slice_of(dtype, r.V, c);
   const dim3 grid((unsigned)(r.T * c)), block(kRowThreads);
   LORA_CUDA(dtype == LORA_BF16 ? launch(stats_kernel<__nv_bfloat16>, grid, block, 0, st, c, true, r, c, slice)
@@ -950,16 +962,17 @@ lora_status_t preference_loss(const LossArgs &a, const PreferenceArgs &p, void *
     r.stats = static_cast<float2 *>(c.take(8 * a.T));
     coef = static_cast<float *>(c.take(4 * a.T));
   }
-  r.ticket = static_cast<unsigned *>(c.take(4));
-  if (r.ticket == nullptr || (a.T > 0 && coef == nullptr)) return LORA_ERR_WORKSPACE;
+  unsigned *ticket = static_cast<unsigned *>(c.take(4));
+  if (ticket == nullptr || (a.T > 0 && coef == nullptr)) return LORA_ERR_WORKSPACE;
   r.coef = coef;
+  r.ticket = ticket;
   if (a.T == 0)
-    LORA_CUDA(cudaMemsetAsync(r.ticket, 0, sizeof(unsigned), st));
+    LORA_CUDA(cudaMemsetAsync(ticket, 0, sizeof(unsigned), st));
   else
     LORA_TRY(run_stats(a.dtype, r, st));
   if (p.P > 0)
     LORA_CUDA(launch(pairs_kernel, dim3((unsigned)p.P), dim3(kPairThreads), 0, st, 1, true, p, a.T, a.V, a.labels,
-                     (const float *)a.logps, a.dlogits ? coef : (float *)nullptr, r.ticket));
+                     (const float *)a.logps, a.dlogits ? coef : (float *)nullptr, ticket));
   return a.dlogits ? run_grad(a.dtype, r, st) : LORA_OK;
 }
 

@@ -26,30 +26,37 @@ struct Sum2 {
   __device__ __forceinline__ float value() const { return hi + lo; }
 };
 
-// Sum over the block in a fixed order, known to every thread.
-template <int kWarps>
-__device__ __forceinline__ Sum2 block_sum(Sum2 v, Sum2 *sh) {
-  auto warp_sum = [](Sum2 x) {
+// Sum over the warp's lanes, known to all of them.
+__device__ __forceinline__ Sum2 warp_sum(Sum2 x) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      Sum2 y;
-      y.hi = __shfl_xor_sync(0xffffffffu, x.hi, o);
-      y.lo = __shfl_xor_sync(0xffffffffu, x.lo, o);
-      // both lanes of a pair add in the same order
-      if (lane_id() & o) {
-        y.add(x);
-        x = y;
-      } else {
-        x.add(y);
-      }
+  for (int o = 16; o > 0; o >>= 1) {
+    Sum2 y;
+    y.hi = __shfl_xor_sync(0xffffffffu, x.hi, o);
+    y.lo = __shfl_xor_sync(0xffffffffu, x.lo, o);
+    // both lanes of a pair add in the same order
+    if (lane_id() & o) {
+      y.add(x);
+      x = y;
+    } else {
+      x.add(y);
     }
-    return x;
-  };
-  v = warp_sum(v);
+  }
+  return x;
+}
+
+// K sums over the block in a fixed order, known to warp 0.  sh: K per warp, not in
+// use by a call before this one.
+template <int kWarps, int K>
+__device__ __forceinline__ void block_sums(Sum2 (&v)[K], Sum2 *sh) {
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    v[i] = warp_sum(v[i]);
+    if (lane_id() == 0) sh[i * kWarps + (threadIdx.x >> 5)] = v[i];
+  }
   __syncthreads();
-  if (lane_id() == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_sum(lane_id() < kWarps ? sh[lane_id() % kWarps] : Sum2());
+  if (threadIdx.x >= 32) return;
+#pragma unroll
+  for (int i = 0; i < K; ++i) v[i] = warp_sum(lane_id() < kWarps ? sh[i * kWarps + lane_id() % kWarps] : Sum2());
 }
 
 }  // namespace lora
