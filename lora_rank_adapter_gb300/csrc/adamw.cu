@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
   __shared__ Sum2 sh[kThreads / 32];
   __shared__ unsigned before;
   pdl_wait();
+  pdl_launch_dependents();      // the step's blocks may take their places and wait there
   Sum2 sum[1];
   for (int64_t k = blockIdx.x; k < chunks; k += gridDim.x) {
     const G *g = static_cast<const G *>(table[k].g);

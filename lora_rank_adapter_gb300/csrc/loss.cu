@@ -267,11 +267,12 @@ __device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int r
 // cluster, a slice of `slice` 16-byte pieces each.  An ignored row is not read,
 // but its blocks meet all the same: no block leaves before the others have sent
 // to it, whatever each has seen of labels that another stream may be writing.
-template <typename E>
-__global__ void __launch_bounds__(kRowThreads) stats_kernel(RowArgs a, int C, int slice) {
-  __shared__ float2 sh[kRowThreads / 32];
+template <typename E, int kThreads>
+__global__ void __launch_bounds__(kThreads) stats_kernel(RowArgs a, int C, int slice) {
+  __shared__ float2 sh[kThreads / 32];
   __shared__ ClusterSlots slots;
   pdl_wait();
+  pdl_launch_dependents();      // the next kernel's blocks may take their places and wait there
   const int64_t t = blockIdx.x / C;
   const int rank = (int)(blockIdx.x % C), tid = threadIdx.x;
   const int64_t label = a.labels[t];
@@ -296,14 +297,14 @@ __global__ void __launch_bounds__(kRowThreads) stats_kernel(RowArgs a, int C, in
     const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
     if (rank == 0 && tid == 0) picked = Elem<E>::load(row + label);
     uint64_t s2 = 0;
-    absorb_span<E, kRowThreads, 4>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
+    absorb_span<E, kThreads, 4>(m, s2, reinterpret_cast<const uint4 *>(row + sp.head), v0, v1, k);
     const float2 both = unpk2(s2);
     s = both.x + both.y;
     if (rank == C - 1) {      // the ragged ends
       if (tid < sp.head) absorb_one(m, s, Elem<E>::load(row + tid), k);
       if (tid < (int)a.V - tail) absorb_one(m, s, Elem<E>::load(row + tail + tid), k);
     }
-    block_merge<kRowThreads / 32>(m, s, k, sh);
+    block_merge<kThreads / 32>(m, s, k, sh);
   }
   if (C > 1) {
     cluster_wait();
@@ -432,6 +433,7 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, i
   __shared__ unsigned before;
   const int pair = blockIdx.x, tid = threadIdx.x;
   pdl_wait();
+  pdl_launch_dependents();
   const int32_t *cu = p.cu;
   const int32_t edge[4] = {cu[pair], cu[pair + 1], cu[pair + p.P], cu[pair + p.P + 1]};
   const float ref = p.ref ? p.ref[pair] - p.ref[pair + p.P] : 0.f;
@@ -626,6 +628,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
     cluster_wait();
   }
   pdl_wait();
+  pdl_launch_dependents();
   int64_t t = blockIdx.x / C;
   int64_t label = t < a.T ? a.labels[t] : -1;
   auto advance = [&](int64_t &mark) {                    // this row's label, with the next one's on its way
@@ -878,47 +881,52 @@ cudaError_t launch_held(const HeldArgs &h, cudaStream_t st) {
                 true, h);
 }
 
-// Blocks for each row of a pass from global memory: enough that the grid fills
+// Blocks for each row of the gradient pass: enough that the grid fills
 // the SMs (eight blocks each) some eight times over, so that the last blocks to
 // run leave few SMs idle, with at least 16 KB a block; few rows are cut down to
 // 4 KB a block until the grid fills the SMs once.
-int parts_of(lora_dtype_t dtype, int64_t T, int64_t V, int most) {
-  const int64_t bytes = V * (dtype == LORA_BF16 ? 2 : 4), once = 8 * (int64_t)num_sms();
+int parts_of(int64_t T, int64_t bytes) {
+  const int64_t once = 8 * (int64_t)num_sms();
   int64_t c = std::min(ceil_div(8 * once, T), bytes / (16 << 10));
   c = std::max(c, std::min(ceil_div(once, T), bytes / (4 << 10)));
-  return (int)std::min<int64_t>(std::max<int64_t>(c, 1), most);
+  return (int)std::min<int64_t>(std::max<int64_t>(c, 1), 64);
 }
-int slice_of(lora_dtype_t dtype, int64_t V, int parts) {
-  const int64_t pieces = V * (dtype == LORA_BF16 ? 2 : 4) / 16;
-  return (int)std::max<int64_t>(8, round_up(ceil_div(pieces, parts), 8));
-}
+// 16-byte pieces of one of `parts` slices of a row.
+int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_up(ceil_div(bytes / 16, parts), 8)); }
 
-// Blocks of a row in the statistics pass: one, where there is a row for each SM
-// (1415 rows of 50048 fp32: 44 us with one, 50 with two, 65 with eight; 4000 of
-// 32000 bf16: 42, 56); fewer rows are cut over clusters, down to 4 KB a block,
-// until there are four blocks for each SM (7 rows of 32003 fp32: 8 us with one
-// block each, 3 with eight).
-int stats_cluster(lora_dtype_t dtype, int64_t T, int64_t V) {
-  const int64_t bytes = V * (dtype == LORA_BF16 ? 2 : 4);
-  if (T >= num_sms()) return 1;
-  const int64_t c = std::min(4 * num_sms() / T, bytes / (4 << 10));
-  return (int)std::min<int64_t>(std::max<int64_t>(c, 1), kMaxCluster);
+// The statistics pass: one block a row, with more threads to it the fewer rows
+// there are to fill the SMs; rows for less than half of the SMs are cut over
+// clusters, down to 4 KB a block.  Rows of 128256 bf16, 256 / 512 / 1024 threads:
+// 2000 rows 81.9 / 79.2 / 93.3 us, 200 rows 15.7 / 12.0 / 13.8, 100 rows 14.0 / 9.2
+// / 7.5; 40 rows over clusters of eight blocks of 256 threads 4.8 us, whole 5.8.
+// Clusters cost where blocks abound: 4000 rows of 32000 bf16 42.0 us with one
+// block each, 80 with four.
+template <typename E>
+cudaError_t launch_stats(const RowArgs &r, int64_t bytes, cudaStream_t st) {
+  const int64_t sms = num_sms();
+  if (2 * r.T < sms) {
+    const int c = (int)std::min<int64_t>({std::max<int64_t>(1, 4 * sms / r.T), std::max<int64_t>(1, bytes / (4 << 10)),
+                                          kMaxCluster});
+    return launch(stats_kernel<E, kRowThreads>, dim3((unsigned)(r.T * c)), dim3(kRowThreads), 0, st, c, true, r, c,
+                  slice_of(bytes, c));
+  }
+  const int slice = slice_of(bytes, 1);
+  const dim3 grid((unsigned)r.T);
+  if (bytes >= (32 << 10) && r.T <= sms) return launch(stats_kernel<E, 1024>, grid, dim3(1024), 0, st, 1, true, r, 1, slice);
+  if (bytes >= (32 << 10) && r.T <= 2 * sms) return launch(stats_kernel<E, 512>, grid, dim3(512), 0, st, 1, true, r, 1, slice);
+  return launch(stats_kernel<E, kRowThreads>, grid, dim3(kRowThreads), 0, st, 1, true, r, 1, slice);
 }
 
 lora_status_t run_stats(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0) return LORA_OK;
-  const int c = stats_cluster(dtype, r.T, r.V);
-  const int slice = slice_of(dtype, r.V, c);
-  const dim3 grid((unsigned)(r.T * c)), block(kRowThreads);
-  LORA_CUDA(dtype == LORA_BF16 ? launch(stats_kernel<__nv_bfloat16>, grid, block, 0, st, c, true, r, c, slice)
-                               : launch(stats_kernel<float>, grid, block, 0, st, c, true, r, c, slice));
+  LORA_CUDA(dtype == LORA_BF16 ? launch_stats<__nv_bfloat16>(r, r.V * 2, st) : launch_stats<float>(r, r.V * 4, st));
   return LORA_OK;
 }
 
 lora_status_t run_grad(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0 || r.V == 0) return LORA_OK;
-  const int c = parts_of(dtype, r.T, r.V, 64);
-  const int slice = slice_of(dtype, r.V, c);
+  const int64_t bytes = r.V * (dtype == LORA_BF16 ? 2 : 4);
+  const int c = parts_of(r.T, bytes), slice = slice_of(bytes, c);
   const dim3 grid((unsigned)(r.T * c)), block(kRowThreads);
   LORA_CUDA(dtype == LORA_BF16 ? launch(grad_kernel<__nv_bfloat16>, grid, block, 0, st, 1, true, r, c, slice)
                                : launch(grad_kernel<float>, grid, block, 0, st, 1, true, r, c, slice));

@@ -78,6 +78,17 @@ int64_t count_chunks(const lora_adamw_tensor_t *tensors, int32_t n) {
   return chunks;
 }
 
+// Nothing is thrown across the C boundary: the launch helpers keep small tables
+// that may have to allocate.
+template <typename F>
+lora_status_t guarded(F &&f) {
+  try {
+    return f();
+  } catch (...) {
+    return LORA_ERR_CUDA;
+  }
+}
+
 }  // namespace
 }  // namespace lora
 
@@ -100,8 +111,10 @@ lora_status_t lora_token_logps(lora_dtype_t dtype, int64_t T, int64_t V, const v
   LORA_TRY(check_rows(dtype, T, V, logits, ldl, labels, temperature, nullptr, 0));
   LORA_TRY(check_ptr(logps, T, 4));
   LORA_TRY(check_opt(stats, 8));
-  return token_logps(loss_args(dtype, T, V, logits, ldl, labels, temperature, logps, nullptr, 0, 1.f), stats,
-                     (cudaStream_t)stream);
+  return guarded([&] {
+    return token_logps(loss_args(dtype, T, V, logits, ldl, labels, temperature, logps, nullptr, 0, 1.f), stats,
+                       (cudaStream_t)stream);
+  });
 }
 
 lora_status_t lora_token_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
@@ -111,8 +124,10 @@ lora_status_t lora_token_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V
   LORA_TRY(check_ptr(dlogits, T * V, 1));
   LORA_TRY(check_ptr(stats, T, 8));
   LORA_TRY(check_ptr(dlogps, T, 4));
-  return token_logps_backward(loss_args(dtype, T, V, logits, ldl, labels, temperature, nullptr, dlogits, lddl, 1.f),
-                              stats, dlogps, (cudaStream_t)stream);
+  return guarded([&] {
+    return token_logps_backward(loss_args(dtype, T, V, logits, ldl, labels, temperature, nullptr, dlogits, lddl, 1.f),
+                                stats, dlogps, (cudaStream_t)stream);
+  });
 }
 
 lora_status_t lora_preference_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_t P, const void *logits,
@@ -139,8 +154,10 @@ lora_status_t lora_preference_loss(lora_dtype_t dtype, int64_t T, int64_t V, int
   p.P = P; p.cu = cu_seqlens; p.ref = ref_logps; p.kind = kind; p.beta = beta; p.smoothing = label_smoothing;
   p.normalize = (flags & LORA_PREF_LENGTH_NORMALIZE) != 0;
   p.seq_logps = seq_logps; p.pair_loss = pair_loss; p.loss = loss;
-  return preference_loss(loss_args(dtype, T, V, logits, ldl, labels, temperature, token_logps, dlogits, lddl,
-                                   grad_scale), p, ws, ws_bytes, (cudaStream_t)stream);
+  return guarded([&] {
+    return preference_loss(loss_args(dtype, T, V, logits, ldl, labels, temperature, token_logps, dlogits, lddl,
+                                     grad_scale), p, ws, ws_bytes, (cudaStream_t)stream);
+  });
 }
 
 lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
@@ -162,8 +179,10 @@ lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const v
   PolicyArgs p;
   p.old_logps = old_logps; p.ref_logps = ref_logps; p.advantages = advantages; p.weights = weights;
   p.clip_low = clip_low; p.clip_high = clip_high; p.kl_beta = kl_beta; p.metrics = metrics;
-  return policy_loss(loss_args(dtype, T, V, logits, ldl, labels, temperature, token_logps, dlogits, lddl, grad_scale),
-                     p, ws, ws_bytes, (cudaStream_t)stream);
+  return guarded([&] {
+    return policy_loss(loss_args(dtype, T, V, logits, ldl, labels, temperature, token_logps, dlogits, lddl,
+                                 grad_scale), p, ws, ws_bytes, (cudaStream_t)stream);
+  });
 }
 
 lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void *x, int64_t ldx,
@@ -175,7 +194,7 @@ lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void
   if (ldx < V) return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_ptr(x, 1, dtype == LORA_BF16 ? 2 : 4));
   LORA_TRY(check_ptr(factor, 1, 4));
-  return scale_gradient(dtype, T, V, x, ldx, factor, (cudaStream_t)stream);
+  return guarded([&] { return scale_gradient(dtype, T, V, x, ldx, factor, (cudaStream_t)stream); });
 }
 
 size_t lora_adamw_table_size(const lora_adamw_tensor_t *tensors, int32_t n) {
@@ -207,7 +226,9 @@ lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, lo
     if (flags & LORA_ADAMW_MASTER) LORA_TRY(check_ptr(t.master, t.numel, 4));
   }
   LORA_TRY(check_ws(table, table_bytes, (size_t)chunks * sizeof(AdamChunk)));
-  LORA_TRY(adamw_build(tensors, n, made, static_cast<AdamChunk *>(table), (cudaStream_t)stream));
+  LORA_TRY(guarded([&] {
+    return adamw_build(tensors, n, made, static_cast<AdamChunk *>(table), (cudaStream_t)stream);
+  }));
   *plan = made;
   return LORA_OK;
 }
@@ -218,7 +239,7 @@ lora_status_t lora_grad_norm(const lora_adamw_plan_t *plan, float max_norm, floa
   if (!(max_norm >= 0.f)) return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_ptr(out, 1, 4));
   LORA_TRY(check_ws(ws, ws_bytes, grad_norm_ws_bytes(plan->chunks)));
-  return grad_norm(*plan, max_norm, out, ws, ws_bytes, (cudaStream_t)stream);
+  return guarded([&] { return grad_norm(*plan, max_norm, out, ws, ws_bytes, (cudaStream_t)stream); });
 }
 
 lora_status_t lora_adamw(const lora_adamw_plan_t *plan, const lora_adamw_hyper_t *h, const float *grad_factor,
@@ -230,7 +251,7 @@ lora_status_t lora_adamw(const lora_adamw_plan_t *plan, const lora_adamw_hyper_t
       h->beta2 >= 1.0)
     return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_opt(grad_factor, 4));
-  return adamw(*plan, *h, grad_factor, (cudaStream_t)stream);
+  return guarded([&] { return adamw(*plan, *h, grad_factor, (cudaStream_t)stream); });
 }
 
 }  // extern "C"

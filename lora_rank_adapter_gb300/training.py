@@ -86,12 +86,16 @@ def lib():
     return L
 
 
+def _refuse(t, n, dtype, name, device):
+    if t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} has to be {dtype} on cuda:{device}, not {t.dtype} on {t.device}")
+    raise ValueError(f"{name} has to hold {n} contiguous elements, not {tuple(t.shape)} of strides {t.stride()}")
+
+
 def _vector(t, n, dtype, name, device):
-    """The address of a contiguous tensor of n elements on `device`."""
-    if t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name} has to be {dtype} on {device}, not {t.dtype} on {t.device}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} has to hold {n} contiguous elements")
+    """The address of a contiguous tensor of n elements on GPU `device` (its number)."""
+    if t.dtype is not dtype or t.get_device() != device or t.numel() != n or not t.is_contiguous():
+        _refuse(t, n, dtype, name, device)
     return t.data_ptr()
 
 
@@ -114,7 +118,7 @@ def _matrix(x, name):
 
 def _rows(logits, labels):
     T, V, x, ld = _matrix(logits, "logits")
-    device = logits.device
+    device = logits.get_device()
     return T, V, x, ld, _vector(labels, T, torch.int64, "labels", device), device
 
 
@@ -128,13 +132,13 @@ def _gradient(dlogits, logits):
 
 
 def _raw_stream(stream, device):
-    """The address of the given stream, or of the device's current one."""
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
+    """The address of the given stream, or of GPU `device`'s current one."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 def train_workspace(op, n, pairs=0, device="cuda", stream=None):
-    """A uint8 workspace of lora_train_workspace_size() bytes (None when zero),
-    kept by the caching allocator until `stream` is done with it."""
+    """A uint8 workspace of lora_train_workspace_size() bytes (None when zero) on
+    `device`, kept by the caching allocator until `stream` is done with it."""
     size = lib().lora_train_workspace_size(op, n, pairs)
     if size == 0:
         return None
@@ -229,8 +233,8 @@ def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps
 def lora_scale_gradient(x, factor, stream=None):
     """x *= factor (fp32 device scalar) in place for a [T, V] gradient; no pass over x when it is 1."""
     T, V, p, ld = _matrix(x, "gradients")
-    st = lib().lora_scale_gradient(_dtype(x), T, V, p, ld, _vector(factor, 1, torch.float32, "factor", x.device),
-                                   _raw_stream(stream, x.device))
+    st = lib().lora_scale_gradient(_dtype(x), T, V, p, ld, _vector(factor, 1, torch.float32, "factor", x.get_device()),
+                                   _raw_stream(stream, x.get_device()))
     _check(st, "lora_scale_gradient")
     return x
 
@@ -243,7 +247,7 @@ class AdamWPlan:
     def __init__(self, struct, table, tensors):
         self.struct, self.table, self.tensors = struct, table, tensors
         self.ref = ctypes.byref(struct)
-        self.device, self.chunks = table.device, int(struct.chunks)
+        self.device, self.chunks = table.get_device(), int(struct.chunks)
 
 
 def _expect(ok, what):
@@ -298,7 +302,7 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
                 raise ValueError(f"{name}[{i}] has to have its parameter's shape and strides")
         for name in ("exp_avg_scales", "exp_avg_sq_scales"):
             if s8:
-                _vector(lists[name][i], -(-p.numel() // ADAMW_BLOCK), torch.float32, name, device)
+                _vector(lists[name][i], -(-p.numel() // ADAMW_BLOCK), torch.float32, name, device.index)
         addr = lambda values: values[i].data_ptr() if values is not None and p.numel() else None  # noqa: E731
         table_in[i] = AdamWTensor(addr(params), addr(grads), addr(exp_avg), addr(exp_avg_sq), addr(exp_avg_scales),
                                   addr(exp_avg_sq_scales), addr(masters), p.numel())
@@ -310,7 +314,7 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
     struct = AdamWPlanStruct()
     st = lib().lora_adamw_build(table_in, n, _dtype(params[0]) if n else binding.LORA_F32,
                                 _dtype(grads[0]) if n else binding.LORA_F32, flags, table.data_ptr(), table.numel(),
-                                ctypes.byref(struct), _raw_stream(stream, device))
+                                ctypes.byref(struct), _raw_stream(stream, device.index))
     _check(st, "lora_adamw_build")
     return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}))
 

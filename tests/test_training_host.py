@@ -72,6 +72,11 @@ def test_rows_are_checked_by_every_loss_operator(L, change, status):
         assert call(L, **change) == status, call.__name__
 
 
+def test_vocabulary_limit(L):
+    for call in (logps, logps_bwd, pref, policy):
+        assert call(L, V=(1 << 30) + 1, ld=1 << 31) == UNSUPPORTED, call.__name__
+
+
 def test_token_logps_arguments(L):
     assert logps(L, out=NULL) == INVALID
     assert logps(L, out=ODD2) == ALIGNMENT

@@ -329,6 +329,25 @@ def test_policy_loss(T, V, pad, dtype):
         assert torch.equal(placed["d"], got["d"])
 
 
+@pytest.mark.parametrize("dtype,V", [(BF16, 17001), (F32, 9004), (BF16, 600), (F32, 60001)])
+@pytest.mark.parametrize("T", [33, 76, 100, 152, 200, 310, 700])
+def test_every_cut_of_the_rows(T, V, dtype):
+    """Row counts and sizes on both sides of every rule by which rows are cut over blocks."""
+    _, x, labels = make(T, V, dtype, seed=T, pad=1)
+    logps, stats = torch.empty(T, device=DEV), torch.empty((T, 2), device=DEV)
+    training.lora_token_logps(x, labels, logps, stats=stats)
+    want, p, ok = oracle_logps(x, labels)
+    check_logps(logps, want)
+    coef = torch.randn(T, generator=torch.Generator().manual_seed(3))
+    d = torch.empty_like(x)
+    training.lora_token_logps_backward(x, labels, stats, coef.to(DEV), d)
+    check_dlogits(d, oracle_dlogits(p, labels, ok, coef.double()), coef.double(), 0.0)
+    old, adv, w, ref = policy_inputs(x, labels, T)
+    check_policy(run_policy(x, labels, old, adv, w, ref=ref, kl_beta=0.1), x, labels, old, adv, w, ref, kl_beta=0.1)
+    cu = [0, T // 5, T // 2, T // 2, T - 1]
+    check_preference(run_preference(x, labels, cu, None), oracle_preference(x, labels, cu, None))
+
+
 def test_policy_loss_defaults_and_ignored_rows():
     _, x, labels = make(70, 500, F32, seed=8, ignored=0.5)
     old, adv, w, ref = policy_inputs(x, labels, 1)
