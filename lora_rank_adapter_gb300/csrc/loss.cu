@@ -428,7 +428,7 @@ __device__ __forceinline__ float log_sigmoid(float h) { return fminf(h, 0.f) - l
 __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, int64_t T, int64_t V,
                                                              const int64_t *labels, const float *logps, float *coef,
                                                              unsigned *ticket) {
-  __shared__ Sum2 sh[4 * (kPairThreads / 32)];
+  __shared__ Sum2 sh[2 * (kPairThreads / 32)], sh_n[2 * (kPairThreads / 32)];
   __shared__ float slope_of[2];
   __shared__ unsigned before;
   const int pair = blockIdx.x, tid = threadIdx.x;
@@ -438,7 +438,7 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, i
   const int32_t edge[4] = {cu[pair], cu[pair + 1], cu[pair + p.P], cu[pair + p.P + 1]};
   const float ref = p.ref ? p.ref[pair] - p.ref[pair + p.P] : 0.f;
   int64_t lo[2], n[2];
-  Sum2 sum[4];                     // sums and counts of both sides
+  Sum2 sum[2], counted[2];
 #pragma unroll
   for (int side = 0; side < 2; ++side) {
     lo[side] = min(max((int64_t)edge[2 * side], (int64_t)0), T);
@@ -450,14 +450,15 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, i
       if (i < n[side]) {
         const int64_t t = lo[side] + i;
         sum[side].add(logps[t]);
-        if (p.normalize) sum[2 + side].add(labels[t] >= 0 && labels[t] < V ? 1.f : 0.f);
+        if (p.normalize) counted[side].add(labels[t] >= 0 && labels[t] < V ? 1.f : 0.f);
       }
-  block_sums<kPairThreads / 32, 4>(sum, sh);
+  if (p.normalize) block_sums<kPairThreads / 32, 2>(counted, sh_n);
+  block_sums<kPairThreads / 32, 2>(sum, sh);
   if (tid == 0) {
     float S[2], count[2];
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      count[side] = p.normalize ? fmaxf(1.f, sum[2 + side].value()) : 1.f;
+      count[side] = p.normalize ? fmaxf(1.f, counted[side].value()) : 1.f;
       S[side] = sum[side].value() / count[side];
       p.seq_logps[pair + side * p.P] = S[side];
     }
