@@ -92,7 +92,7 @@ LORA_API lora_status_t lora_token_logps_backward(lora_dtype_t dtype, int64_t T, 
  *   ref_logps   device float [2P], or NULL for R = 0.
  *   token_logps float [T];  seq_logps float [2P];  pair_loss float [P];  loss float [1]
  *   dlogits     NULL, or grad_scale * d loss / d logits
- *   beta        finite, > 0;  label_smoothing in [0, 1] (LORA_PREF_SIGMOID only, else 0)
+ *   beta        finite, > 0;  label_smoothing in [0, 1], used by LORA_PREF_SIGMOID alone
  *   ws          lora_train_workspace_size(LORA_TRAIN_PREFERENCE_LOSS, T, P) bytes
  * -------------------------------------------------------------------------------- */
 typedef enum { LORA_PREF_SIGMOID = 0, LORA_PREF_HINGE = 1, LORA_PREF_IPO = 2 } lora_pref_kind_t;

@@ -141,7 +141,6 @@ lora_status_t lora_preference_loss(lora_dtype_t dtype, int64_t T, int64_t V, int
   if (kind != LORA_PREF_SIGMOID && kind != LORA_PREF_HINGE && kind != LORA_PREF_IPO) return LORA_ERR_UNSUPPORTED;
   if (!(beta > 0.f) || !isfinite(beta) || !isfinite(grad_scale)) return LORA_ERR_INVALID_ARG;
   if (!(label_smoothing >= 0.f && label_smoothing <= 1.f)) return LORA_ERR_INVALID_ARG;
-  if (kind != LORA_PREF_SIGMOID && label_smoothing != 0.f) return LORA_ERR_INVALID_ARG;
   if (flags & ~LORA_PREF_LENGTH_NORMALIZE) return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_ptr(cu_seqlens, P, 4));
   LORA_TRY(check_opt(ref_logps, 4));

@@ -94,7 +94,7 @@ def test_token_logps_arguments(L):
 def test_preference_arguments(L):
     for change, status in [({"P": -1}, INVALID), ({"kind": 3}, UNSUPPORTED), ({"beta": 0.0}, INVALID),
                            ({"beta": NAN}, INVALID), ({"eps": -0.1}, INVALID), ({"eps": 1.5}, INVALID),
-                           ({"eps": 0.1, "kind": 1}, INVALID), ({"flags": 2}, INVALID), ({"cu": NULL}, INVALID),
+                           ({"flags": 2}, INVALID), ({"cu": NULL}, INVALID),
                            ({"cu": ODD2}, ALIGNMENT), ({"tok": NULL}, INVALID), ({"seq": NULL}, INVALID),
                            ({"pair": NULL}, INVALID), ({"loss": NULL}, INVALID), ({"ref": ODD2}, ALIGNMENT),
                            ({"d": FAKE, "ldd": 5}, INVALID), ({"gs": INF}, INVALID)]:
@@ -102,6 +102,7 @@ def test_preference_arguments(L):
     need = L.lora_train_workspace_size(T.TRAIN_PREFERENCE_LOSS, 6, 2)
     assert need > 0
     assert pref(L) == WORKSPACE
+    assert pref(L, eps=0.1, kind=1) == WORKSPACE          # smoothing belongs to the sigmoid loss; the others pass it by
     assert pref(L, ws=FAKE, wsb=need - 1) == WORKSPACE
     assert pref(L, ws=ctypes.c_void_p(0x10080), wsb=need) == WORKSPACE
 

@@ -215,7 +215,7 @@ def check_preference(got, want):
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("kind,opts", [("sigmoid", {}), ("sigmoid", {"label_smoothing": 0.2, "temperature": 0.8}),
-                                       ("hinge", {"grad_scale": 0.25}), ("ipo", {"length_normalize": True}),
+                                       ("hinge", {"grad_scale": 0.25, "label_smoothing": 0.1}), ("ipo", {"length_normalize": True}),
                                        ("sigmoid", {"length_normalize": True, "temperature": 1.4})])
 def test_preference_loss(kind, opts, dtype):
     for V, cu, pad in ((61, [0, 4, 9, 9, 16], 0), (1003, [0, 30, 31], 1), (8200, [0, 1, 2, 3, 4, 5, 20], 8)):
