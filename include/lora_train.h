@@ -44,14 +44,14 @@ extern "C" {
 
 /* Bytes of workspace of the operators below (0: none, or arguments out of range).
  *   LORA_TRAIN_PREFERENCE_LOSS  (T, P)
- *   LORA_TRAIN_POLICY_LOSS      (T, 0)
+ *   LORA_TRAIN_POLICY_LOSS      (T, bytes of a row of logits; 0: a bound for any)
  *   LORA_TRAIN_GRAD_NORM        (chunks of the plan, 0) */
 typedef enum {
     LORA_TRAIN_PREFERENCE_LOSS = 0,
     LORA_TRAIN_POLICY_LOSS = 1,
     LORA_TRAIN_GRAD_NORM = 2
 } lora_train_op_t;
-LORA_API size_t lora_train_workspace_size(lora_train_op_t op, int64_t n, int64_t pairs);
+LORA_API size_t lora_train_workspace_size(lora_train_op_t op, int64_t n, int64_t m);
 
 /* --------------------------------------------------------------------------------
  * lora_token_logps:  logps[t] = z[t][label] - ln sum_v exp(z[t][v])
@@ -114,11 +114,12 @@ LORA_API lora_status_t lora_preference_loss(lora_dtype_t dtype, int64_t T, int64
  *   old_logps, ref_logps  device float [T] or NULL;  advantages  device float [T]
  *   weights     device float [T] or NULL for 1: the caller's mean (1 / number of
  *               rows that count, 1 / (sequences * rows of the sequence), ...)
- *   token_logps float [T];  metrics float [3]: the loss, sum weights * kl, and
- *               sum of weights over the clipped rows
+ *   token_logps float [T], not one of the inputs;  metrics float [3]: the loss,
+ *               sum weights * kl, and sum of weights over the clipped rows
  *   dlogits     NULL, or grad_scale * d loss / d logits
  *   clip_low in [0, 1], clip_high >= 0, kl_beta >= 0, all finite
- *   ws          lora_train_workspace_size(LORA_TRAIN_POLICY_LOSS, T, 0) bytes
+ *   ws          lora_train_workspace_size(LORA_TRAIN_POLICY_LOSS, T, row bytes) bytes:
+ *               none for rows up to 768 KB, or without dlogits
  * -------------------------------------------------------------------------------- */
 LORA_API lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
                            const int64_t *labels, const float *old_logps, const float *ref_logps,

@@ -532,18 +532,14 @@ __device__ __forceinline__ PolicyTerm policy_term(const PolicyArgs &p, const Pol
   return {w * (pg + p.kl_beta * kl), w * kl, clipped ? w : 0.f, w * coef};
 }
 
-// The policy loss where a row does not fit on chip: the terms and coefficients
-// from the log-probabilities of the stats pass.
+// The policy loss where a row does not fit on chip: the coefficients from the
+// log-probabilities of the statistics pass.
 __global__ void __launch_bounds__(kPairThreads) tokens_kernel(PolicyArgs p, int64_t T, int64_t V,
-                                                              const int64_t *labels, const float *logps, float *coef,
-                                                              float4 *terms) {
+                                                              const int64_t *labels, const float *logps, float *coef) {
   pdl_wait();
   const int64_t t = blockIdx.x * (int64_t)kPairThreads + threadIdx.x;
   if (t >= T) return;
-  PolicyTerm x = {0.f, 0.f, 0.f, 0.f};
-  if (labels[t] >= 0 && labels[t] < V) x = policy_term(p, policy_row(p, t), logps[t]);
-  coef[t] = x.coef;
-  terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
+  coef[t] = labels[t] >= 0 && labels[t] < V ? policy_term(p, policy_row(p, t), logps[t]).coef : 0.f;
 }
 
 // ----------------------------------------------------------------------------- short rows
@@ -553,7 +549,7 @@ __global__ void __launch_bounds__(kPairThreads) tokens_kernel(PolicyArgs p, int6
 enum ShortMode { kShortStats, kShortPolicy, kShortGrad };
 
 template <typename E, int kPieces, int kTeam, int kMode>
-__global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(RowArgs a, PolicyArgs p, float4 *terms) {
+__global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(RowArgs a, PolicyArgs p) {
   constexpr int kLanes = 32 * kTeam, kRows = kTeam == 1 ? 8 : 1, N = Elem<E>::kVec;
   __shared__ float2 sh[kTeam];
   pdl_wait();
@@ -580,7 +576,6 @@ __global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Ro
     if (kMode != kShortGrad && tid == 0) {
       a.logps[t] = 0.f;
       if (kMode == kShortStats && a.stats) a.stats[t] = make_float2(0.f, 1.f);
-      if (kMode == kShortPolicy) terms[t] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     if (kMode != kShortStats && a.dlogits) zero_span<E, kLanes>(out, 0, V, tid);
     return;
@@ -630,11 +625,8 @@ __global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Ro
       a.logps[t] = logp;
       if (kMode == kShortStats && a.stats) a.stats[t] = make_float2(m, s);
     }
-    if (kMode == kShortStats) return;
-    const PolicyTerm x = policy_term(p, in, logp);
-    if (tid == 0) terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
-    if (a.dlogits == nullptr) return;
-    c = x.coef * a.grad_scale * a.inv_t;
+    if (kMode == kShortStats || a.dlogits == nullptr) return;
+    c = policy_term(p, in, logp).coef * a.grad_scale * a.inv_t;
     if (c == 0.f) {
       zero_span<E, kLanes>(out, 0, V, tid);
       return;
@@ -687,7 +679,6 @@ constexpr int kHeldSmem = kSlots * kChunk * 16;
 struct HeldArgs {
   RowArgs r;
   PolicyArgs p;
-  float4 *terms;       // loss, kl and clipped weight of each row
   int cluster;
   int slice;           // 16-byte pieces of a block at most, up to kSlots chunks
   uint32_t zero;
@@ -788,10 +779,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
     E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
     const int V = (int)a.V, nv = sl.nv, tail = sl.head + sl.vecs * N, first = sl.head + sl.v0 * N, mark = (int)mark64;
     if (!valid) {
-      if (rank == 0 && tid == 0) {
-        a.logps[t] = 0.f;
-        h.terms[t] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      if (rank == 0 && tid == 0) a.logps[t] = 0.f;
       if (a.dlogits) zero_span<E, kHeldWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N, tid);
       continue;
     }
@@ -846,12 +834,8 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
     }
     warp_merge(m, s, k);
     const float logp = (picked - m) * a.inv_t - logf(s);
-    const PolicyTerm x = policy_term(h.p, in, logp);
-    if (rank == 0 && tid == 0) {
-      a.logps[t] = logp;
-      h.terms[t] = make_float4(x.loss, x.kl, x.clipped, 0.f);
-    }
-    const float c = x.coef * a.grad_scale * a.inv_t;
+    if (rank == 0 && tid == 0) a.logps[t] = logp;
+    const float c = policy_term(h.p, in, logp).coef * a.grad_scale * a.inv_t;
     const RowGrad g = {m, k, c, -c / s};
     const bool write = a.dlogits != nullptr && c != 0.f;
     const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0;
@@ -884,23 +868,27 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
   }
 }
 
-// The three metrics: sums of the rows' terms in a fixed order.
+// The three metrics from the log-probabilities, in a fixed order.  (The terms are
+// worked out again: they need a few values of a token, and no scratch memory.)
 constexpr int kSumThreads = 1024;
-__global__ void __launch_bounds__(kSumThreads) terms_kernel(const float4 *terms, int64_t T, float *metrics) {
+__global__ void __launch_bounds__(kSumThreads) metrics_kernel(PolicyArgs p, int64_t T, int64_t V, const int64_t *labels,
+                                                              const float *logps) {
   __shared__ Sum2 sh[3 * (kSumThreads / 32)];
   pdl_wait();
   Sum2 s[3];
-#pragma unroll 4
+#pragma unroll 2
   for (int64_t t = threadIdx.x; t < T; t += kSumThreads) {
-    const float4 v = terms[t];
-    s[0].add(v.x);
-    s[1].add(v.y);
-    s[2].add(v.z);
+    const int64_t label = labels[t];
+    if (label < 0 || label >= V) continue;
+    const PolicyTerm x = policy_term(p, policy_row(p, t), logps[t]);
+    s[0].add(x.loss);
+    s[1].add(x.kl);
+    s[2].add(x.clipped);
   }
   block_sums<kSumThreads / 32, 3>(s, sh);
   if (threadIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < 3; ++i) metrics[i] = s[i].value();
+    for (int i = 0; i < 3; ++i) p.metrics[i] = s[i].value();
   }
 }
 
@@ -947,8 +935,7 @@ RowArgs row_args(const LossArgs &a) {
 struct HeldPlan {
   int cluster, slice;
 };
-HeldPlan plan_held(lora_dtype_t dtype, int64_t T, int64_t V) {
-  const int64_t e = dtype == LORA_BF16 ? 2 : 4, bytes = V * e;
+HeldPlan plan_held(int64_t T, int64_t bytes) {
   int64_t c = std::max<int64_t>(1, ceil_div(bytes, kSliceBytes));
   c = std::max(c, std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096));
   c = std::min<int64_t>(c, kMaxCluster);
@@ -1018,12 +1005,12 @@ int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_
 // of 300 fp32 9.2 (36.3), of 8192 bf16 36.6 (52.1), of 16000 bf16 56.3 (74.3).
 constexpr int64_t kShortest = 2 << 10, kShort = 8 << 10, kShortTeam = 32 << 10;
 template <typename E, int kMode>
-cudaError_t launch_short_as(const RowArgs &r, const PolicyArgs &p, float4 *terms, int64_t bytes, cudaStream_t st) {
+cudaError_t launch_short_as(const RowArgs &r, const PolicyArgs &p, int64_t bytes, cudaStream_t st) {
   const dim3 grid((unsigned)ceil_div(r.T, 8));
-  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1, kMode>, grid, dim3(256), 0, st, 1, true, r, p, terms);
-  if (bytes <= kShort) return launch(short_kernel<E, 16, 1, kMode>, grid, dim3(256), 0, st, 1, true, r, p, terms);
+  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1, kMode>, grid, dim3(256), 0, st, 1, true, r, p);
+  if (bytes <= kShort) return launch(short_kernel<E, 16, 1, kMode>, grid, dim3(256), 0, st, 1, true, r, p);
   if constexpr (kMode != kShortGrad)
-    return launch(short_kernel<E, 16, 4, kMode>, dim3((unsigned)r.T), dim3(128), 0, st, 1, true, r, p, terms);
+    return launch(short_kernel<E, 16, 4, kMode>, dim3((unsigned)r.T), dim3(128), 0, st, 1, true, r, p);
   return cudaErrorInvalidValue;
 }
 template <int kMode>
@@ -1031,9 +1018,9 @@ bool short_rows(int64_t bytes) {
   return bytes <= (kMode == kShortGrad ? kShort : kShortTeam);
 }
 template <int kMode>
-cudaError_t launch_short(lora_dtype_t dtype, const RowArgs &r, const PolicyArgs &p, float4 *terms, cudaStream_t st) {
-  return dtype == LORA_BF16 ? launch_short_as<__nv_bfloat16, kMode>(r, p, terms, r.V * 2, st)
-                            : launch_short_as<float, kMode>(r, p, terms, r.V * 4, st);
+cudaError_t launch_short(lora_dtype_t dtype, const RowArgs &r, const PolicyArgs &p, cudaStream_t st) {
+  return dtype == LORA_BF16 ? launch_short_as<__nv_bfloat16, kMode>(r, p, r.V * 2, st)
+                            : launch_short_as<float, kMode>(r, p, r.V * 4, st);
 }
 
 // The statistics pass: one block a row, with more threads to it the fewer rows
@@ -1062,7 +1049,7 @@ cudaError_t launch_stats(const RowArgs &r, int64_t bytes, cudaStream_t st) {
 lora_status_t run_stats(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0) return LORA_OK;
   if (short_rows<kShortStats>(r.V * (dtype == LORA_BF16 ? 2 : 4))) {
-    LORA_CUDA(launch_short<kShortStats>(dtype, r, PolicyArgs{}, nullptr, st));
+    LORA_CUDA(launch_short<kShortStats>(dtype, r, PolicyArgs{}, st));
     return LORA_OK;
   }
   LORA_CUDA(dtype == LORA_BF16 ? launch_stats<__nv_bfloat16>(r, r.V * 2, st) : launch_stats<float>(r, r.V * 4, st));
@@ -1073,7 +1060,7 @@ lora_status_t run_grad(lora_dtype_t dtype, const RowArgs &r, cudaStream_t st) {
   if (r.T == 0 || r.V == 0) return LORA_OK;
   const int64_t bytes = r.V * (dtype == LORA_BF16 ? 2 : 4);
   if (short_rows<kShortGrad>(bytes)) {
-    LORA_CUDA(launch_short<kShortGrad>(dtype, r, PolicyArgs{}, nullptr, st));
+    LORA_CUDA(launch_short<kShortGrad>(dtype, r, PolicyArgs{}, st));
     return LORA_OK;
   }
   const int c = parts_of(r.T, bytes), slice = slice_of(bytes, c);
@@ -1089,7 +1076,10 @@ int64_t token_blocks(int64_t T) { return ceil_div(T, kPairThreads); }
 
 // ----------------------------------------------------------------------------- host side
 size_t preference_ws_bytes(int64_t T, int64_t) { return ws_round(8 * T) + ws_round(4 * T) + ws_round(4); }
-size_t policy_ws_bytes(int64_t T) { return ws_round(16 * T) + ws_round(8 * T) + ws_round(4 * T); }
+size_t policy_ws_bytes(int64_t T, int64_t row_bytes, bool grad) {
+  if (T == 0 || !grad || row_bytes <= (int64_t)kMaxCluster * kSlots * kChunk * 16) return 0;
+  return ws_round(8 * T) + ws_round(4 * T);
+}
 int read_clear_error_loss() {
   int v = 0, z = 0;
   if (cudaMemcpyFromSymbol(&v, g_device_error, sizeof(int)) != cudaSuccess) return -1;
@@ -1139,25 +1129,28 @@ lora_status_t policy_loss(const LossArgs &a, const PolicyArgs &p, void *ws, size
     LORA_CUDA(cudaMemsetAsync(p.metrics, 0, 3 * sizeof(float), st));
     return LORA_OK;
   }
-  WsCarver c(ws, ws_bytes);
   RowArgs r = row_args(a);
-  float4 *terms = static_cast<float4 *>(c.take(16 * a.T));
-  r.stats = static_cast<float2 *>(c.take(8 * a.T));
-  r.coef = static_cast<float *>(c.take(4 * a.T));
-  if (r.coef == nullptr) return LORA_ERR_WORKSPACE;
-  const HeldPlan hp = plan_held(a.dtype, a.T, a.V);
-  if (short_rows<kShortPolicy>(a.V * (a.dtype == LORA_BF16 ? 2 : 4))) {
-    LORA_CUDA(launch_short<kShortPolicy>(a.dtype, r, p, terms, st));
-  } else if (hp.cluster > 0) {
-    const HeldArgs h = {r, p, terms, hp.cluster, hp.slice, 0u};
+  const int64_t bytes = a.V * (a.dtype == LORA_BF16 ? 2 : 4);
+  if (short_rows<kShortPolicy>(bytes)) {
+    LORA_CUDA(launch_short<kShortPolicy>(a.dtype, r, p, st));
+  } else if (const HeldPlan hp = plan_held(a.T, bytes); hp.cluster > 0) {
+    const HeldArgs h = {r, p, hp.cluster, hp.slice, 0u};
     LORA_CUDA(a.dtype == LORA_BF16 ? launch_held<__nv_bfloat16>(h, st) : launch_held<float>(h, st));
-  } else {
+  } else if (a.dlogits == nullptr) {
     LORA_TRY(run_stats(a.dtype, r, st));
+  } else {
+    WsCarver c(ws, ws_bytes);
+    r.stats = static_cast<float2 *>(c.take(8 * a.T));
+    float *coef = static_cast<float *>(c.take(4 * a.T));
+    if (coef == nullptr) return LORA_ERR_WORKSPACE;
+    LORA_TRY(run_stats(a.dtype, r, st));
+    r.coef = coef;
     LORA_CUDA(launch(tokens_kernel, dim3((unsigned)token_blocks(a.T)), dim3(kPairThreads), 0, st, 1, true, p, a.T, a.V,
-                     a.labels, (const float *)a.logps, r.coef, terms));
-    if (a.dlogits) LORA_TRY(run_grad(a.dtype, r, st));
+                     a.labels, (const float *)a.logps, coef));
+    LORA_TRY(run_grad(a.dtype, r, st));
   }
-  LORA_CUDA(launch(terms_kernel, dim3(1), dim3(kSumThreads), 0, st, 1, true, (const float4 *)terms, a.T, p.metrics));
+  LORA_CUDA(launch(metrics_kernel, dim3(1), dim3(kSumThreads), 0, st, 1, true, p, a.T, a.V, a.labels,
+                   (const float *)a.logps));
   return LORA_OK;
 }
 

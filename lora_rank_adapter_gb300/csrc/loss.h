@@ -41,7 +41,8 @@ struct PolicyArgs {
 int read_clear_error_loss();
 
 size_t preference_ws_bytes(int64_t T, int64_t P);
-size_t policy_ws_bytes(int64_t T);
+// Rows of `row_bytes`; none where a row is held on chip, or without a gradient.
+size_t policy_ws_bytes(int64_t T, int64_t row_bytes, bool grad);
 
 lora_status_t token_logps(const LossArgs &a, float *stats, cudaStream_t st);
 lora_status_t token_logps_backward(const LossArgs &a, const float *stats, const float *dlogps, cudaStream_t st);

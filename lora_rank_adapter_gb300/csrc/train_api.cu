@@ -96,11 +96,11 @@ using namespace lora;
 
 extern "C" {
 
-size_t lora_train_workspace_size(lora_train_op_t op, int64_t n, int64_t pairs) {
-  if (!size_ok(n) || !size_ok(pairs)) return 0;
+size_t lora_train_workspace_size(lora_train_op_t op, int64_t n, int64_t m) {
+  if (!size_ok(n) || m < 0 || m > 4 * kMaxVocab) return 0;
   switch (op) {
-    case LORA_TRAIN_PREFERENCE_LOSS: return preference_ws_bytes(n, pairs);
-    case LORA_TRAIN_POLICY_LOSS: return policy_ws_bytes(n);
+    case LORA_TRAIN_PREFERENCE_LOSS: return size_ok(m) ? preference_ws_bytes(n, m) : 0;
+    case LORA_TRAIN_POLICY_LOSS: return policy_ws_bytes(n, m == 0 ? 4 * kMaxVocab : m, true);
     case LORA_TRAIN_GRAD_NORM: return grad_norm_ws_bytes(n);
   }
   return 0;
@@ -174,7 +174,8 @@ lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const v
   LORA_TRY(check_ptr(advantages, T, 4));
   LORA_TRY(check_ptr(token_logps, T, 4));
   LORA_TRY(check_ptr(metrics, 1, 4));
-  LORA_TRY(check_ws(ws, ws_bytes, policy_ws_bytes(T)));
+  if (T > 0 && (token_logps == old_logps || token_logps == ref_logps)) return LORA_ERR_INVALID_ARG;
+  LORA_TRY(check_ws(ws, ws_bytes, policy_ws_bytes(T, V * (dtype == LORA_BF16 ? 2 : 4), dlogits != nullptr)));
   PolicyArgs p;
   p.old_logps = old_logps; p.ref_logps = ref_logps; p.advantages = advantages; p.weights = weights;
   p.clip_low = clip_low; p.clip_high = clip_high; p.kl_beta = kl_beta; p.metrics = metrics;

@@ -31,6 +31,7 @@ PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PREF_LENGTH_NORMALIZE = 1
 ADAMW_STATE_8BIT, ADAMW_MASTER = 1, 2
 ADAMW_BLOCK, ADAMW_CHUNK = 256, 2048
+POLICY_HELD_BYTES = 768 << 10      # rows up to here need no workspace in lora_policy_loss
 
 
 class AdamWTensor(ctypes.Structure):
@@ -136,10 +137,10 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
-def train_workspace(op, n, pairs=0, device="cuda", stream=None):
+def train_workspace(op, n, m=0, device="cuda", stream=None):
     """A uint8 workspace of lora_train_workspace_size() bytes (None when zero) on
     `device`, kept by the caching allocator until `stream` is done with it."""
-    size = lib().lora_train_workspace_size(op, n, pairs)
+    size = lib().lora_train_workspace_size(op, n, m)
     if size == 0:
         return None
     ws = torch.empty(size, dtype=torch.uint8, device=device)
@@ -148,9 +149,9 @@ def train_workspace(op, n, pairs=0, device="cuda", stream=None):
     return ws
 
 
-def _workspace(ws, op, n, pairs, device, stream):
+def _workspace(ws, op, n, m, device, stream):
     if ws is None:
-        ws = train_workspace(op, n, pairs, device, stream)
+        ws = train_workspace(op, n, m, device, stream)
     return ws, (0 if ws is None else ws.data_ptr()), (0 if ws is None else ws.numel())
 
 
@@ -218,7 +219,10 @@ def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps
     T, V, x, ld, lab, dev = _rows(logits, labels)
     f32 = torch.float32
     d, ldd = _gradient(dlogits, logits)
-    ws, w, wn = _workspace(ws, TRAIN_POLICY_LOSS, T, 0, dev, stream)
+    if d is None or V * logits.element_size() <= POLICY_HELD_BYTES:      # no workspace
+        w = wn = 0
+    else:
+        ws, w, wn = _workspace(ws, TRAIN_POLICY_LOSS, T, V * logits.element_size(), dev, stream)
     st = lib().lora_policy_loss(_dtype(logits), T, V, x, ld, lab, _optional(old_logps, T, f32, "old_logps", dev),
                                 _optional(ref_logps, T, f32, "ref_logps", dev),
                                 _vector(advantages, T, f32, "advantages", dev),

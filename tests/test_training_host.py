@@ -59,7 +59,7 @@ def pref(L, P=2, cu=FAKE, ref=FAKE, kind=0, beta=0.1, eps=0.0, flags=0, tok=FAKE
                                   flags, k["temp"], tok, seq, pair, loss, d, ldd, gs, ws, wsb, NULL)
 
 
-def policy(L, old=FAKE, ref=NULL, adv=FAKE, w=NULL, lo=0.2, hi=0.2, kl=0.0, tok=FAKE, met=FAKE, d=NULL, ldd=0, gs=1.0,
+def policy(L, old=FAKE, ref=NULL, adv=FAKE, w=NULL, lo=0.2, hi=0.2, kl=0.0, tok=ctypes.c_void_p(0x20000), met=FAKE, d=NULL, ldd=0, gs=1.0,
            ws=NULL, wsb=0, **k):
     k = {**ROWS, **k}
     return L.lora_policy_loss(k["dt"], k["T"], k["V"], k["x"], k["ld"], k["lab"], old, ref, adv, w, lo, hi, kl,
@@ -110,13 +110,21 @@ def test_preference_arguments(L):
 def test_policy_arguments(L):
     for change, status in [({"adv": NULL}, INVALID), ({"tok": NULL}, INVALID), ({"met": NULL}, INVALID),
                            ({"old": ODD2}, ALIGNMENT), ({"ref": ODD2}, ALIGNMENT), ({"w": ODD2}, ALIGNMENT),
+                           ({"met": ODD2}, ALIGNMENT),
                            ({"lo": -0.1}, INVALID), ({"lo": 1.1}, INVALID), ({"hi": -1.0}, INVALID),
                            ({"hi": INF}, INVALID), ({"kl": NAN}, INVALID), ({"kl": -1.0}, INVALID),
                            ({"gs": NAN}, INVALID), ({"d": FAKE, "ldd": 3}, INVALID)]:
         assert policy(L, **change) == status, change
-    need = L.lora_train_workspace_size(T.TRAIN_POLICY_LOSS, 6, 0)
-    assert policy(L) == WORKSPACE
-    assert policy(L, ws=FAKE, wsb=need - 1) == WORKSPACE
+    assert policy(L, tok=FAKE, old=FAKE) == INVALID                   # an output that is an input
+    # rows held on chip need no workspace; longer ones do, for a gradient
+    size = L.lora_train_workspace_size
+    assert size(T.TRAIN_POLICY_LOSS, 6, T.POLICY_HELD_BYTES) == 0
+    need = size(T.TRAIN_POLICY_LOSS, 6, T.POLICY_HELD_BYTES + 1)
+    assert need > 0 and size(T.TRAIN_POLICY_LOSS, 6, 0) == need
+    V = T.POLICY_HELD_BYTES // 2 + 1
+    long = dict(V=V, ld=V, d=ctypes.c_void_p(0x30000), ldd=V)
+    assert policy(L, **long) == WORKSPACE
+    assert policy(L, ws=FAKE, wsb=need - 1, **long) == WORKSPACE
 
 
 def test_scale_gradient_arguments(L):
