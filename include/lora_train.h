@@ -44,12 +44,10 @@ extern "C" {
 
 /* Bytes of workspace of the operators below (0: none, or arguments out of range).
  *   LORA_TRAIN_PREFERENCE_LOSS  (T, P)
- *   LORA_TRAIN_POLICY_LOSS      (T, bytes of a row of logits; 0: a bound for any)
- *   LORA_TRAIN_GRAD_NORM        (chunks of the plan, 0) */
+ *   LORA_TRAIN_POLICY_LOSS      (T, bytes of a row of logits; 0: a bound for any) */
 typedef enum {
     LORA_TRAIN_PREFERENCE_LOSS = 0,
-    LORA_TRAIN_POLICY_LOSS = 1,
-    LORA_TRAIN_GRAD_NORM = 2
+    LORA_TRAIN_POLICY_LOSS = 1
 } lora_train_op_t;
 LORA_API size_t lora_train_workspace_size(lora_train_op_t op, int64_t n, int64_t m);
 
@@ -139,8 +137,9 @@ LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_
  * AdamW over many tensors.  lora_adamw_build lays the tensors' addresses out
  * once in a caller's device buffer (the table), in chunks of
  * LORA_ADAMW_CHUNK elements of one tensor; lora_grad_norm and lora_adamw then
- * run over all tensors in one or two launches.  The caller rebuilds the table
- * when an address changes and keeps the tensors alive while it is in use.
+ * run over all tensors in one launch each.  The caller rebuilds the table when an
+ * address changes, keeps the tensors alive while it is in use, and lets calls on
+ * one table run one after the other (the table holds the norm's partial sums).
  *
  * Element i of tensor k, all in 32-bit arithmetic (g is read in its own type):
  *     g' = g * *grad_factor
@@ -190,7 +189,7 @@ typedef struct {
     uint32_t reserved;
 } lora_adamw_plan_t;
 
-/* Bytes of the table of n tensors (0 if an argument is out of range, or for no elements). */
+/* Bytes of the table of n tensors (0 if an argument is out of range). */
 LORA_API size_t lora_adamw_table_size(const lora_adamw_tensor_t *tensors, int32_t n);
 
 /* Writes the table (256-byte aligned device buffer of lora_adamw_table_size() bytes)
@@ -203,9 +202,8 @@ LORA_API lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int3
                            lora_adamw_plan_t *plan, void *stream);
 
 /* out[0] = sqrt(sum of all g^2), out[1] = min(1, max_norm / (out[0] + 1e-6)); out is
- * device float [2], max_norm >= 0.  ws: lora_train_workspace_size(LORA_TRAIN_GRAD_NORM, chunks, 0). */
-LORA_API lora_status_t lora_grad_norm(const lora_adamw_plan_t *plan, float max_norm, float *out, void *ws,
-                           size_t ws_bytes, void *stream);
+ * device float [2], max_norm >= 0. */
+LORA_API lora_status_t lora_grad_norm(const lora_adamw_plan_t *plan, float max_norm, float *out, void *stream);
 
 /* One step.  step >= 1 counts this step; grad_factor: device float [1], or NULL for 1.
  * lr, weight_decay, eps >= 0 and beta1, beta2 in [0, 1), all finite. */

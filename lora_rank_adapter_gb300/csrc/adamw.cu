@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
   if (threadIdx.x == 0) {
     part[blockIdx.x] = sum[0];
     __threadfence();
-    before = atomicAdd(ticket, 1u);
+    before = atomicInc(ticket, gridDim.x - 1);      // back to 0 with the last block
     __threadfence();
   }
   __syncthreads();
@@ -361,11 +361,13 @@ cudaError_t run_step(const lora_adamw_plan_t &plan, const StepArgs &a, cudaStrea
 }  // namespace
 
 // ----------------------------------------------------------------------------- host side
-// Blocks of the norm at most (no tensors: one block that writes the norm 0).
-static int64_t norm_blocks(int64_t chunks) { return std::max<int64_t>(1, std::min<int64_t>(chunks, kNormBlocks)); }
-
-size_t grad_norm_ws_bytes(int64_t chunks) {
-  return ws_round(sizeof(unsigned)) + ws_round(sizeof(Sum2) * (size_t)norm_blocks(chunks));
+size_t table_bytes(int64_t chunks) {
+  return ws_round(sizeof(AdamChunk) * (size_t)chunks) + ws_round(sizeof(unsigned)) + sizeof(Sum2) * kNormBlocks;
+}
+// Behind the chunks: the norm's ticket and partial sums.
+static unsigned *norm_ticket(const void *table, int64_t chunks) {
+  return reinterpret_cast<unsigned *>(static_cast<char *>(const_cast<void *>(table)) +
+                                      ws_round(sizeof(AdamChunk) * (size_t)chunks));
 }
 
 lora_status_t adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, const lora_adamw_plan_t &plan,
@@ -374,6 +376,7 @@ lora_status_t adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, const l
   a.e_p = plan.param_dtype == LORA_BF16 ? 2 : 4;
   a.e_g = plan.grad_dtype == LORA_BF16 ? 2 : 4;
   a.e_s = (plan.flags & LORA_ADAMW_STATE_8BIT) ? 1 : 4;
+  LORA_CUDA(cudaMemsetAsync(norm_ticket(table, plan.chunks), 0, sizeof(unsigned), st));
   for (int32_t i = 0; i < n;) {
     a.n = 0;
     a.first[0] = 0;
@@ -394,14 +397,11 @@ lora_status_t adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, const l
   return LORA_OK;
 }
 
-lora_status_t grad_norm(const lora_adamw_plan_t &plan, float max_norm, float *out, void *ws, size_t ws_bytes,
-                        cudaStream_t st) {
-  WsCarver c(ws, ws_bytes);
-  unsigned *ticket = static_cast<unsigned *>(c.take(sizeof(unsigned)));
-  const int blocks = (int)std::min<int64_t>(norm_blocks(plan.chunks), 8 * (int64_t)num_sms());
-  Sum2 *part = static_cast<Sum2 *>(c.take(sizeof(Sum2) * (size_t)blocks));
-  if (part == nullptr) return LORA_ERR_WORKSPACE;
-  LORA_CUDA(cudaMemsetAsync(ticket, 0, sizeof(unsigned), st));
+lora_status_t grad_norm(const lora_adamw_plan_t &plan, float max_norm, float *out, cudaStream_t st) {
+  // no tensors: one block that writes the norm 0
+  const int blocks = (int)std::max<int64_t>(1, std::min<int64_t>({plan.chunks, kNormBlocks, 8 * (int64_t)num_sms()}));
+  unsigned *ticket = norm_ticket(plan.table, plan.chunks);
+  Sum2 *part = reinterpret_cast<Sum2 *>(reinterpret_cast<char *>(ticket) + ws_round(sizeof(unsigned)));
   const AdamChunk *table = static_cast<const AdamChunk *>(plan.table);
   if (plan.grad_dtype == LORA_BF16)
     LORA_CUDA(launch(norm_kernel<__nv_bfloat16>, dim3(blocks), dim3(kThreads), 0, st, 1, true, table, plan.chunks,

@@ -18,12 +18,12 @@ struct AdamChunk {
 };
 static_assert(sizeof(AdamChunk) == 64, "a chunk is one 64-byte record");
 
-size_t grad_norm_ws_bytes(int64_t chunks);
+// The chunks' records, and room for the gradient norm's partial sums.
+size_t table_bytes(int64_t chunks);
 
 lora_status_t adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, const lora_adamw_plan_t &plan,
                           AdamChunk *table, cudaStream_t st);
-lora_status_t grad_norm(const lora_adamw_plan_t &plan, float max_norm, float *out, void *ws, size_t ws_bytes,
-                        cudaStream_t st);
+lora_status_t grad_norm(const lora_adamw_plan_t &plan, float max_norm, float *out, cudaStream_t st);
 lora_status_t adamw(const lora_adamw_plan_t &plan, const lora_adamw_hyper_t &h, const float *grad_factor,
                     cudaStream_t st);
 

@@ -57,7 +57,7 @@ LossArgs loss_args(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits,
 
 lora_status_t check_plan(const lora_adamw_plan_t *plan) {
   if (plan == nullptr || plan->chunks < 0 || plan->chunks >= kMaxDim) return LORA_ERR_INVALID_ARG;
-  if (plan->chunks > 0 && (plan->table == nullptr || !aligned(plan->table, 256))) return LORA_ERR_INVALID_ARG;
+  if (plan->table == nullptr || !aligned(plan->table, 256)) return LORA_ERR_INVALID_ARG;
   if ((plan->param_dtype != LORA_F32 && plan->param_dtype != LORA_BF16) ||
       (plan->grad_dtype != LORA_F32 && plan->grad_dtype != LORA_BF16))
     return LORA_ERR_UNSUPPORTED;
@@ -101,7 +101,6 @@ size_t lora_train_workspace_size(lora_train_op_t op, int64_t n, int64_t m) {
   switch (op) {
     case LORA_TRAIN_PREFERENCE_LOSS: return size_ok(m) ? preference_ws_bytes(n, m) : 0;
     case LORA_TRAIN_POLICY_LOSS: return policy_ws_bytes(n, m == 0 ? 4 * kMaxVocab : m, true);
-    case LORA_TRAIN_GRAD_NORM: return grad_norm_ws_bytes(n);
   }
   return 0;
 }
@@ -199,11 +198,11 @@ lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void
 
 size_t lora_adamw_table_size(const lora_adamw_tensor_t *tensors, int32_t n) {
   const int64_t chunks = count_chunks(tensors, n);
-  return chunks <= 0 ? 0 : (size_t)chunks * sizeof(AdamChunk);
+  return chunks < 0 ? 0 : table_bytes(chunks);
 }
 
 lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, lora_dtype_t param_dtype,
-                               lora_dtype_t grad_dtype, uint32_t flags, void *table, size_t table_bytes,
+                               lora_dtype_t grad_dtype, uint32_t flags, void *table, size_t bytes,
                                lora_adamw_plan_t *plan, void *stream) {
   if (plan == nullptr) return LORA_ERR_INVALID_ARG;
   const int64_t chunks = count_chunks(tensors, n);
@@ -225,7 +224,7 @@ lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, lo
     }
     if (flags & LORA_ADAMW_MASTER) LORA_TRY(check_ptr(t.master, t.numel, 4));
   }
-  LORA_TRY(check_ws(table, table_bytes, (size_t)chunks * sizeof(AdamChunk)));
+  LORA_TRY(check_ws(table, bytes, table_bytes(chunks)));
   LORA_TRY(guarded([&] {
     return adamw_build(tensors, n, made, static_cast<AdamChunk *>(table), (cudaStream_t)stream);
   }));
@@ -233,13 +232,11 @@ lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, lo
   return LORA_OK;
 }
 
-lora_status_t lora_grad_norm(const lora_adamw_plan_t *plan, float max_norm, float *out, void *ws, size_t ws_bytes,
-                             void *stream) {
+lora_status_t lora_grad_norm(const lora_adamw_plan_t *plan, float max_norm, float *out, void *stream) {
   LORA_TRY(check_plan(plan));
   if (!(max_norm >= 0.f)) return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_ptr(out, 1, 4));
-  LORA_TRY(check_ws(ws, ws_bytes, grad_norm_ws_bytes(plan->chunks)));
-  return guarded([&] { return grad_norm(*plan, max_norm, out, ws, ws_bytes, (cudaStream_t)stream); });
+  return guarded([&] { return grad_norm(*plan, max_norm, out, (cudaStream_t)stream); });
 }
 
 lora_status_t lora_adamw(const lora_adamw_plan_t *plan, const lora_adamw_hyper_t *h, const float *grad_factor,

@@ -17,6 +17,7 @@ tensors of the caller.  All arithmetic runs in the library's CUDA kernels.
 `torch_ops` holds the differentiable forms.
 """
 import ctypes
+import functools
 
 import torch
 
@@ -26,7 +27,7 @@ from .binding import _check, _dtype
 TRAIN_EXPORTS = ["lora_train_workspace_size", "lora_token_logps", "lora_token_logps_backward",
                  "lora_preference_loss", "lora_policy_loss", "lora_scale_gradient", "lora_adamw_table_size",
                  "lora_adamw_build", "lora_grad_norm", "lora_adamw"]
-TRAIN_PREFERENCE_LOSS, TRAIN_POLICY_LOSS, TRAIN_GRAD_NORM = 0, 1, 2
+TRAIN_PREFERENCE_LOSS, TRAIN_POLICY_LOSS = 0, 1
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PREF_LENGTH_NORMALIZE = 1
 ADAMW_STATE_8BIT, ADAMW_MASTER = 1, 2
@@ -76,7 +77,7 @@ def lib():
         "lora_scale_gradient": (i32, [i32, i64, i64, P, i64, P, P]),
         "lora_adamw_table_size": (sz, [TP, i32]),
         "lora_adamw_build": (i32, [TP, i32, i32, i32, u32, P, sz, PP, P]),
-        "lora_grad_norm": (i32, [PP, f32, P, P, sz, P]),
+        "lora_grad_norm": (i32, [PP, f32, P, P]),
         "lora_adamw": (i32, [PP, HP, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -137,10 +138,15 @@ def _raw_stream(stream, device):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
+@functools.lru_cache(maxsize=1024)
+def _workspace_size(op, n, m):
+    return lib().lora_train_workspace_size(op, n, m)
+
+
 def train_workspace(op, n, m=0, device="cuda", stream=None):
     """A uint8 workspace of lora_train_workspace_size() bytes (None when zero) on
     `device`, kept by the caching allocator until `stream` is done with it."""
-    size = lib().lora_train_workspace_size(op, n, m)
+    size = _workspace_size(op, n, m)
     if size == 0:
         return None
     ws = torch.empty(size, dtype=torch.uint8, device=device)
@@ -246,7 +252,8 @@ def lora_scale_gradient(x, factor, stream=None):
 # ----------------------------------------------------------------------------- optimizer
 class AdamWPlan:
     """The addresses of an optimizer's tensors, laid out once on the device.  Holds
-    the tensors; build it again when one of them is replaced."""
+    the tensors; build it again when one of them is replaced.  Its calls belong on one
+    stream, or one after the other."""
 
     def __init__(self, struct, table, tensors):
         self.struct, self.table, self.tensors = struct, table, tensors
@@ -312,7 +319,7 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
                                   addr(exp_avg_sq_scales), addr(masters), p.numel())
     flags = (ADAMW_STATE_8BIT if s8 else 0) | (ADAMW_MASTER if masters is not None else 0)
     size = lib().lora_adamw_table_size(table_in, n)
-    table = torch.empty(max(size, 1), dtype=torch.uint8, device=device)
+    table = torch.empty(size, dtype=torch.uint8, device=device)
     if stream is not None:
         table.record_stream(stream)
     struct = AdamWPlanStruct()
@@ -323,10 +330,9 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
     return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}))
 
 
-def lora_grad_norm(plan, max_norm, out, ws=None, stream=None):
+def lora_grad_norm(plan, max_norm, out, stream=None):
     """out[0] = the 2-norm of all gradients, out[1] = min(1, max_norm / (norm + 1e-6)) (fp32 [2])."""
-    ws, w, wn = _workspace(ws, TRAIN_GRAD_NORM, plan.chunks, 0, plan.device, stream)
-    st = lib().lora_grad_norm(plan.ref, max_norm, _vector(out, 2, torch.float32, "out", plan.device), w, wn,
+    st = lib().lora_grad_norm(plan.ref, max_norm, _vector(out, 2, torch.float32, "out", plan.device),
                               _raw_stream(stream, plan.device))
     _check(st, "lora_grad_norm")
     return out
