@@ -5,6 +5,13 @@
 // the work is laid out once as a table of chunks (adamw_build) and a step is one
 // launch over all of them: a block takes a chunk of 2048 elements, a warp a block
 // of 256 (one scale of an 8-bit state), a lane 8 elements.
+//
+// States in 32 bits are bound by their bytes: 448 tensors, 168 M elements in bf16
+// with fp32 gradients and masters (30 bytes an element): 705 us, 7.1 TB/s; with the
+// norm's reading of the gradients 820 us.  States in 8 bits (10 bytes an element
+// with bf16 gradients): 264 us, 6.4 TB/s, instructions issued in 70 % of the
+// cycles; single-value arithmetic and a division of full precision took 435 us,
+// one block of 256 a warp 281 us without the streaming loads and stores.
 #include <cuda_fp8.h>
 #include <math.h>
 
