@@ -125,7 +125,7 @@ struct Elem<__nv_bfloat16> {
 };
 
 // A row split at 16-byte boundaries: `head` elements before the first, `vecs`
-// whole 16-byte pieces, and the rest.  (V < 2^31: places within a row are ints.)
+// whole 16-byte pieces, and the rest.  (V <= 2^30: places within a row are ints.)
 template <typename E>
 struct RowSpan {
   int head, vecs;
@@ -274,11 +274,12 @@ __device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int r
 }
 
 // The statistics of a row, read once from global memory by the C blocks of a
-// cluster, a slice of `slice` 16-byte pieces each.  bound by the reading: 5462 rows
+// cluster, a slice of `slice` 16-byte pieces each.  Bound by the reading: 5462 rows
 // of 128256 bf16 (1.4 GB) take 213 us, 6.6 TB/s, four loads of a thread in flight.
-// (Plain loads: through TMA copies into shared memory the same took 270 us.)  An ignored row is not read,
-// but its blocks meet all the same: no block leaves before the others have sent
-// to it, whatever each has seen of labels that another stream may be writing.
+// (Plain loads: through TMA copies into shared memory the same took 270 us.)  An
+// ignored row is not read, but its blocks meet all the same: no block leaves before
+// the others have sent to it, whatever each has seen of labels that another stream
+// may be writing.
 template <typename E, int kThreads>
 __global__ void __launch_bounds__(kThreads) stats_kernel(RowArgs a, int C, int slice) {
   __shared__ float2 sh[kThreads / 32];
@@ -478,7 +479,8 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(PreferenceArgs p, i
     float loss, slope;
     if (p.kind == LORA_PREF_SIGMOID) {
       const float h = p.beta * d;
-      loss = -(1.f - p.smoothing) * log_sigmoid(h) - p.smoothing * log_sigmoid(-h);
+      loss = -(1.f - p.smoothing) * log_sigmoid(h);
+      if (p.smoothing > 0.f) loss -= p.smoothing * log_sigmoid(-h);      // no 0 * infinity at an infinite h
       // d loss / d h = sigmoid(h) - (1 - eps), written without cancellation at large |h|
       slope = p.beta * (p.smoothing / (1.f + expf(-h)) - (1.f - p.smoothing) / (1.f + expf(h)));
     } else if (p.kind == LORA_PREF_HINGE) {
@@ -702,7 +704,7 @@ struct HeldArgs {
   PolicyArgs p;
   int cluster;
   int slice;           // 16-byte pieces of a block at most, up to kSlots chunks
-  uint32_t zero;
+  uint32_t zero;       // 0, which the compiler does not know
 };
 
 // A block's slice of a row.

@@ -396,6 +396,90 @@ def test_gradient_against_differences(op):
         assert abs(slope - want) <= 2e-3 * float(d.norm()) + 4e-5, (slope, want)
 
 
+def test_many_short_rows_and_labels_out_of_range():
+    """More rows than any grid holds at once; labels far outside the vocabulary."""
+    T, V = 70001, 5
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(T, V, generator=g).to(DEV)
+    labels = torch.randint(-3, 9, (T,), generator=g)
+    labels[::1000] = 2 ** 40
+    labels[1::1000] = -2 ** 40
+    labels[2::1000] = 2 ** 32 + 1              # its low 32 bits are a valid label
+    labels = labels.to(DEV)
+    logps, stats = torch.empty(T, device=DEV), torch.empty((T, 2), device=DEV)
+    training.lora_token_logps(x, labels, logps, stats=stats)
+    want, p, ok = oracle_logps(x, labels)
+    check_logps(logps, want)
+    assert bool((logps[(~ok).to(DEV)] == 0).all())
+    d = torch.empty_like(x)
+    one = torch.ones(T, device=DEV)
+    training.lora_token_logps_backward(x, labels, stats, one, d)
+    check_dlogits(d, oracle_dlogits(p, labels, ok, torch.ones(T, dtype=torch.float64)), torch.ones(T, dtype=torch.float64), 0.0)
+    for shape in ((T, V), (40, 9001)):         # the same labels where a row takes a block or a cluster
+        lab = torch.full((shape[0],), 2 ** 32 + 1, device=DEV)
+        out = run_policy(torch.randn(shape, device=DEV), lab, None, torch.ones(shape[0]), None)
+        assert bool((out["d"] == 0).all()) and bool((out["metrics"] == 0).all())
+
+
+def test_preference_with_an_impossible_answer():
+    """A label that is masked out has log-probability minus infinity: as the rejected
+    sequence's it leaves loss 0 and no slope, as the chosen one's an infinite loss."""
+    _, x, labels = make(8, 60, F32, seed=2, ignored=0.0)
+    x[6, int(labels[6])] = -math.inf
+    got = run_preference(x, labels, [0, 4, 8], None)
+    assert float(got["loss"]) == 0 and float(got["seq"][1]) == -math.inf
+    assert bool((got["d"] == 0).all())
+    x[2, int(labels[2])], x[6, int(labels[6])] = -math.inf, 0.0
+    got = run_preference(x, labels, [0, 4, 8], None)
+    assert float(got["loss"]) == math.inf and bool(got["d"].isfinite().all())
+
+
+def test_in_a_graph():
+    """Captured once and replayed on new values: no host sync, no state left behind."""
+    _, x, labels = make(40, 3001, BF16, seed=5)
+    old, adv, w, _ = policy_inputs(x, labels, 2)
+    old, adv, w = old.to(DEV), adv.to(DEV), w.to(DEV)
+    cu = torch.tensor([0, 10, 25, 30, 40], dtype=torch.int32, device=DEV)
+    tok, met, d = torch.empty(40, device=DEV), torch.empty(3, device=DEV), torch.empty_like(x)
+    tok2, seq, pair, loss = (torch.empty(n, device=DEV) for n in (40, 4, 2, 1))
+    d2, p = torch.empty_like(x), x.float()
+    m, v, norm = torch.zeros_like(p), torch.zeros_like(p), torch.empty(2, device=DEV)
+    plan = training.lora_adamw_plan([p], [d], [m], [v])
+
+    def step():
+        training.lora_policy_loss(x, labels, old, adv, w, tok, met, dlogits=d)
+        training.lora_preference_loss(x, labels, cu, None, 0.1, tok2, seq, pair, loss, dlogits=d2)
+        training.lora_grad_norm(plan, 0.1, norm)
+        training.lora_adamw(plan, lr=1e-2, step=1, grad_factor=norm[1:])
+
+    outs = (tok, met, d, tok2, seq, pair, loss, d2, p, m, v, norm)
+    start = [t.clone() for t in outs]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+        s.synchronize()
+        for t, b in zip(outs, start):
+            t.copy_(b)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            step()
+        s.synchronize()
+        for change in (1.0, 0.5):
+            for t, b in zip(outs, start):
+                t.copy_(b)
+            x.mul_(change)
+            step()
+            s.synchronize()
+            want = [t.clone() for t in outs]
+            for t, b in zip(outs, start):
+                t.copy_(b)
+            graph.replay()
+            s.synchronize()
+            for t, b in zip(outs, want):
+                assert torch.equal(t, b)
+
+
 def test_offsets_past_32_bits():
     """Rows 2^30 + 8 elements apart: element offsets and byte offsets pass 32 bits."""
     ld, V, T = (1 << 30) + 8, 1000, 4
