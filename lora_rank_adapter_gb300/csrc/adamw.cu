@@ -9,9 +9,8 @@
 // States in 32 bits are bound by their bytes: 448 tensors, 168 M elements in bf16
 // with fp32 gradients and masters (30 bytes an element): 705 us, 7.1 TB/s; with the
 // norm's reading of the gradients 820 us.  States in 8 bits (10 bytes an element
-// with bf16 gradients): 264 us, 6.4 TB/s, instructions issued in 70 % of the
-// cycles; single-value arithmetic and a division of full precision took 435 us,
-// one block of 256 a warp 281 us without the streaming loads and stores.
+// with bf16 gradients): 261 us, 6.5 TB/s, 95 % of the copy rate; single-value
+// arithmetic and a division of full precision took 435 us.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -145,21 +144,36 @@ __device__ __forceinline__ void store4(T *p, const Four<T> &r, int n) {
   }
 }
 
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
 // The factor 448 / a that brings the warp's 256 values to the codes' range, and
-// their scale a / 448.  The largest magnitude is taken on the bit patterns, whose
-// order is that of the magnitudes with NaN above infinity: a NaN makes the
-// block's scale NaN.
+// their scale a / 448.  Across the warp the largest magnitude is taken on the bit
+// patterns, whose order is that of the magnitudes with NaN above infinity: a NaN
+// makes the block's scale NaN.
 __device__ __forceinline__ float code_range(const uint64_t *v, float &scale) {
-  uint32_t top = __float_as_uint(1e-30f);
+  float top = 1e-30f;
 #pragma unroll
   for (int i = 0; i < kLane / 2; ++i) {
     const float2 f = unpk2(v[i]);
-    top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+    top = max_abs(max_abs(top, f.x), f.y);
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  const float a = __uint_as_float(top);
+  const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu));
   scale = __fmul_rn(a, (float)(1.0 / 448.0));
   return __fdiv_rn(448.f, a);
+}
+
+// 1 / x to 2^-22 or so, for x of at least the smallest normal number (the step's
+// divisor is taken up to it).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(1.17549435e-38f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(r));
+  return r;
 }
 
 // ----------------------------------------------------------------------------- the step
@@ -230,12 +244,12 @@ struct Block {
       }
       pm[i] = fma2(mul2(pm[i], both(a.b1)), both(a.one), mul2(gi, both(a.b1c)));
       pv[i] = fma2(mul2(pv[i], both(a.b2)), both(a.one), mul2(mul2(gi, gi), both(a.b2c)));
-      const float2 vv = unpk2(pv[i]), mm = unpk2(pm[i]);
+      const float2 vv = unpk2(pv[i]);
       const uint64_t u = pk2(__fsqrt_rn(vv.x), __fsqrt_rn(vv.y));
       if (k8) pv[i] = u;
-      // the quotient is off by two roundings: far below a parameter's own
+      // the quotient is off by some 2^-22: far below a parameter's own rounding
       const float2 d = unpk2(fma2(u, both(a.root), both(a.eps)));
-      pw[i] = fma2(pk2(__fdividef(mm.x, d.x), __fdividef(mm.y, d.y)), both(a.rate), mul2(pw[i], both(a.decay)));
+      pw[i] = fma2(mul2(pm[i], pk2(reciprocal(d.x), reciprocal(d.y))), both(a.rate), mul2(pw[i], both(a.decay)));
     }
     if (k8) {
       const uint64_t mup = both(code_range(pm, ms)), vup = both(code_range(pv, vs));
@@ -274,10 +288,12 @@ struct Block {
 };
 
 // A block of threads takes a chunk; with states in 8 bits (few bytes a warp) each
-// warp loads two blocks of it before it works on the first.
+// warp loads two blocks of it before it works on the first.  Eight blocks of 128
+// threads an SM (64 registers) take 261 us where 72 registers took 273, nine blocks
+// 273 and ten 297 (spills); four blocks of 256 threads for 32-bit states 820, five 865.
 constexpr int kEach8 = 2, kEach32 = 1;
 template <typename P, typename G, bool k8, bool kMaster>
-__global__ void __launch_bounds__(kThreads / (k8 ? kEach8 : kEach32)) adamw_kernel(StepArgs a) {
+__global__ void __launch_bounds__(kThreads / (k8 ? kEach8 : kEach32), k8 ? 8 : 4) adamw_kernel(StepArgs a) {
   constexpr int kEach = k8 ? kEach8 : kEach32, kWarps = kThreads / 32 / kEach;
   pdl_wait();
   // last to first: the norm before this step has left the last gradients in L2
