@@ -143,16 +143,20 @@ def _workspace_size(op, n, m):
     return lib().lora_train_workspace_size(op, n, m)
 
 
+def _bytes(size, device, stream):
+    """`size` bytes of device memory, in the order of `stream` (None: the current one):
+    what the allocator hands out may be in use until the work before it is done."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def train_workspace(op, n, m=0, device="cuda", stream=None):
     """A uint8 workspace of lora_train_workspace_size() bytes (None when zero) on
-    `device`, kept by the caching allocator until `stream` is done with it."""
+    `device`, for work on `stream`."""
     size = _workspace_size(op, n, m)
-    if size == 0:
-        return None
-    ws = torch.empty(size, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(stream)
-    return ws
+    return _bytes(size, device, stream) if size else None
 
 
 def _workspace(ws, op, n, m, device, stream):
@@ -319,9 +323,7 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
                                   addr(exp_avg_sq_scales), addr(masters), p.numel())
     flags = (ADAMW_STATE_8BIT if s8 else 0) | (ADAMW_MASTER if masters is not None else 0)
     size = lib().lora_adamw_table_size(table_in, n)
-    table = torch.empty(size, dtype=torch.uint8, device=device)
-    if stream is not None:
-        table.record_stream(stream)
+    table = _bytes(size, device, stream)
     struct = AdamWPlanStruct()
     st = lib().lora_adamw_build(table_in, n, _dtype(params[0]) if n else binding.LORA_F32,
                                 _dtype(grads[0]) if n else binding.LORA_F32, flags, table.data_ptr(), table.numel(),

@@ -514,14 +514,23 @@ def test_on_another_stream():
     for a, b in zip(got, got_p):
         assert all(torch.equal(a[k], want[k]) for k in want)
         assert all(torch.equal(b[k], want_p[k]) for k in want_p)
-    # a stream by argument, the workspace coming from the current one
+    # a stream by argument
     logps = torch.empty(200, device=DEV)
     pair, seq, loss = torch.empty(1, device=DEV), torch.empty(2, device=DEV), torch.empty(1, device=DEV)
     cu = torch.tensor([0, 90, 200], dtype=torch.int32, device=DEV)
     torch.cuda.synchronize()
-    training.lora_preference_loss(x, labels, cu, None, 0.2, logps, seq, pair, loss, stream=s)
-    s.synchronize()
-    assert torch.equal(loss, want_p["loss"])
+    for _ in range(5):
+        # the current stream keeps the block that the call's workspace must not be busy
+        busy = torch.empty(1 << 26, device=DEV)
+        for _ in range(20):
+            busy.mul_(1.0001)
+        junk = torch.full((8192,), 7, dtype=torch.uint8, device=DEV)
+        del junk
+        loss.zero_()
+        s.wait_stream(torch.cuda.current_stream())
+        training.lora_preference_loss(x, labels, cu, None, 0.2, logps, seq, pair, loss, stream=s)
+        s.synchronize()
+        assert torch.equal(loss, want_p["loss"])
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
