@@ -366,6 +366,31 @@ class AdamW:
         for p in self.params:
             p.grad = None
 
+    def _states(self):
+        return {k: v for k, v in (("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq),
+                                  ("exp_avg_scale", self.exp_avg_scale),
+                                  ("exp_avg_sq_scale", self.exp_avg_sq_scale), ("masters", self.masters))
+                if v is not None}
+
+    def state_dict(self):
+        """The step count and copies of the states."""
+        return {"step": self.step_count, **{k: [t.clone() for t in v] for k, v in self._states().items()}}
+
+    @torch.no_grad()
+    def load_state_dict(self, state):
+        """Takes over what state_dict() of an optimizer with the same parameters and options gave."""
+        mine = self._states()
+        if set(state) != set(mine) | {"step"} or any(len(state[k]) != len(v) for k, v in mine.items()):
+            raise ValueError("the state is of another optimizer: other options or other parameters")
+        for k, v in mine.items():
+            for t, u in zip(v, state[k]):
+                if t.shape != u.shape or t.dtype != u.dtype:
+                    raise ValueError(f"{k} is of another shape or type")
+        for k, v in mine.items():
+            for t, u in zip(v, state[k]):
+                t.copy_(u)
+        self.step_count = int(state["step"])
+
     @torch.no_grad()
     def step(self):
         """One step from the parameters' .grad; the tensors' addresses are laid out again when a
@@ -373,7 +398,9 @@ class AdamW:
         at = [i for i, p in enumerate(self.params) if p.grad is not None]
         if not at:
             return
-        grads = [self.params[i].grad for i in at]
+        # a gradient laid out otherwise than its parameter is brought to the parameter's layout
+        grads = [g if g.stride() == p.stride() else torch.empty_like(p, dtype=g.dtype).copy_(g)
+                 for p, g in ((self.params[i], self.params[i].grad) for i in at)]
         laid_out = [(i, g.data_ptr(), g.dtype, g.stride(), self.params[i].data_ptr()) for i, g in zip(at, grads)]
         if self._plan is None or laid_out != self._laid_out:
             pick = lambda v: None if v is None else [v[i] for i in at]  # noqa: E731

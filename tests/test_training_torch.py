@@ -154,6 +154,43 @@ def test_optimizer_follows_torch(bits):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bits,masters", [(32, False), (8, True)])
+def test_optimizer_resumes_and_takes_other_layouts(bits, masters):
+    g = torch.Generator().manual_seed(0)
+    start = [torch.randn(40, 30, generator=g).bfloat16(), torch.randn(300, generator=g).bfloat16()]
+    grads = [[torch.randn(p.shape, generator=g) for p in start] for _ in range(4)]
+    make = lambda values: [t.detach().clone().to(DEV).requires_grad_() for t in values]  # noqa: E731
+
+    def run(params, opt, steps, transpose=False):
+        for step in steps:
+            for p, v in zip(params, grads[step]):
+                v = v.bfloat16().to(DEV)
+                p.grad = v.t().contiguous().t() if transpose and v.dim() == 2 else v
+            opt.step()
+
+    options = dict(lr=1e-2, state_bits=bits, masters=masters, max_norm=1.0)
+    a = make(start)
+    opt_a = torch_ops.AdamW(a, **options)
+    run(a, opt_a, range(4))
+    b = make(start)
+    opt_b = torch_ops.AdamW(b, **options)
+    run(b, opt_b, range(2), transpose=True)
+    state = opt_b.state_dict()
+    c = make(b)
+    opt_c = torch_ops.AdamW(c, **options)
+    opt_c.load_state_dict(state)
+    run(c, opt_c, range(2, 4))
+    for p, q in zip(a, c):
+        assert torch.equal(p, q)
+    for k, v in opt_a.state_dict().items():
+        w = opt_c.state_dict()[k]
+        same = lambda t, u: torch.equal(t.view(torch.uint8), u.view(torch.uint8))  # noqa: E731
+        assert v == w if k == "step" else all(same(t, u) for t, u in zip(v, w)), k
+    with pytest.raises(ValueError):
+        torch_ops.AdamW(make(start), lr=1e-2, state_bits=40 - bits).load_state_dict(state)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("args", [["--loss", "preference", "--state-bits", "8"],
                                   ["--loss", "policy", "--state-bits", "32"]])
 def test_example_learns(args):
