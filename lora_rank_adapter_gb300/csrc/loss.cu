@@ -236,14 +236,20 @@ constexpr int kMaxCluster = 8;
 
 // (m, s) of the blocks of a cluster, by warp 0 of each, once.  Each block writes
 // its pair to all the others; `ready` counts one arrival from each.  The caller
-// has let the cluster arrive and wait after `ready` was set up.  False: the wait
-// ran out.
+// has let the cluster arrive and wait after `ready` was set up, and lets no block
+// leave before all have sent.
 struct ClusterSlots {
   uint64_t ready;
   float2 pair[kMaxCluster];
+  int64_t label;       // of the block's row, read once for all its threads
 };
+// Whole warps arrive and wait together ...
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// ... or each thread when it gets here.
+__device__ __forceinline__ void cluster_leave() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 __device__ __forceinline__ void st_dsmem_f2(const void *local_ptr, uint32_t cta, float2 v) {
   uint32_t local = smem_u32(local_ptr), remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(cta));
@@ -259,12 +265,17 @@ __device__ __forceinline__ void st_async_f2(const void *local_ptr, const uint64_
                "f"(v.x), "f"(v.y), "r"(b)
                : "memory");
 }
-__device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int rank, int C, ClusterSlots *slots) {
+__device__ __forceinline__ void cluster_send(float m, float s, int rank, int C, ClusterSlots *slots) {
   const int lane = lane_id();
   if (lane < C) {
     st_dsmem_f2(&slots->pair[rank], lane, make_float2(m, s));
     mbar_arrive_remote(&slots->ready, lane);
   }
+  __syncwarp();
+}
+// False: the wait ran out.
+__device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int C, ClusterSlots *slots) {
+  const int lane = lane_id();
   if (!__all_sync(0xffffffffu, mbar_wait<true>(&slots->ready, 0))) return false;
   const float2 v = lane < C ? slots->pair[lane] : make_float2(kNegInf, 0.f);
   m = v.x;
@@ -277,9 +288,9 @@ __device__ __forceinline__ bool cluster_merge(float &m, float &s, float k, int r
 // cluster, a slice of `slice` 16-byte pieces each.  Bound by the reading: 5462 rows
 // of 128256 bf16 (1.4 GB) take 213 us, 6.6 TB/s, four loads of a thread in flight.
 // (Plain loads: through TMA copies into shared memory the same took 270 us.)  An
-// ignored row is not read, but its blocks meet all the same: no block leaves before
-// the others have sent to it, whatever each has seen of labels that another stream
-// may be writing.
+// ignored row is not read, but its blocks meet all the same, and a block whose wait
+// ran out stays for the others: no block leaves before all have sent to it, whatever
+// each has seen of labels that another stream may be writing.
 template <typename E, int kThreads>
 __global__ void __launch_bounds__(kThreads) stats_kernel(RowArgs a, int C, int slice) {
   __shared__ float2 sh[kThreads / 32];
@@ -288,14 +299,18 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(RowArgs a, int C, int s
   pdl_launch_dependents();      // the next kernel's blocks may take their places and wait there
   const int64_t t = blockIdx.x / C;
   const int rank = (int)(blockIdx.x % C), tid = threadIdx.x;
-  const int64_t label = a.labels[t];
+  int64_t label;
   if (C > 1) {
     if (tid == 0) {
       mbar_init(&slots.ready, C);
       fence_barrier_init();
+      slots.label = a.labels[t];
     }
     __syncthreads();
     cluster_arrive();
+    label = slots.label;
+  } else {
+    label = a.labels[t];
   }
   if (rank == 0 && tid == 0) {
     if (a.coef) a.coef[t] = 0.f;
@@ -319,13 +334,20 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(RowArgs a, int C, int s
     }
     block_merge<kThreads / 32>(m, s, k, sh);
   }
+  bool whole = true;
   if (C > 1) {
     cluster_wait();
-    if (tid < 32 && !cluster_merge(m, s, k, rank, C, &slots)) return;
+    if (tid < 32) cluster_send(m, s, rank, C, &slots);
+    cluster_arrive();
+    if (tid < 32) whole = cluster_merge(m, s, k, C, &slots);
   }
-  if (rank == 0 && tid == 0) {
+  if (rank == 0 && tid == 0 && whole) {
     a.logps[t] = counts ? (picked - m) * a.inv_t - logf(s) : 0.f;
     if (a.stats) a.stats[t] = counts ? make_float2(m, s) : make_float2(0.f, 1.f);
+  }
+  if (C > 1) {
+    __syncwarp();
+    cluster_wait();      // all have sent
   }
 }
 
@@ -735,7 +757,7 @@ struct RingAt {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArgs h) {
+__device__ __forceinline__ void held_rows(const HeldArgs &h) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ uint64_t full[kSlots], empty[kSlots], ready[2];
   __shared__ float2 pairs[2][kMaxCluster * kHeldWarps];  // (m, s) of every warp of the cluster, two exchanges
@@ -786,10 +808,9 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
         again = again || at.parity;
       }
     }
-    // A wait ran out: the copies in flight land before the block ends.
-    if (!ok)
-      for (int i = 0; i < kSlots; ++i)
-        if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
+    // The last copies land before the block ends, whoever else waits for them.
+    for (int i = 0; i < kSlots; ++i)
+      if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
     return;
   }
 
@@ -889,6 +910,16 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
       zero_span<E, kHeldWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N, tid);
     }
   }
+}
+
+// However a thread comes back (the loader ahead of the others, a warp whose wait ran
+// out early), its block stays until all blocks of the cluster have done: their warps
+// store into its shared memory for as long as they go through rows.  All waits within
+// are bounded, so all threads come here.
+template <typename E>
+__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(const __grid_constant__ HeldArgs h) {
+  held_rows<E>(h);
+  if (h.cluster > 1) cluster_leave();
 }
 
 // The three metrics from the log-probabilities, in a fixed order.  (The terms are

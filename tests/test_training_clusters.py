@@ -1,0 +1,97 @@
+"""Blocks of a cluster that store into each other's shared memory: none leaves before the
+others have sent what they send, on any path, and copies in flight land first.  (Shown on
+the source, since the paths in question are those of a wait that ran out; on the GPU, the
+kernels go through many rows a cluster, in place too.)"""
+import os
+import re
+
+import pytest
+import torch
+
+from lora_rank_adapter_gb300 import _build
+from tests.test_training_loss import BF16, DEV, F32, check_policy, make, policy_inputs, run_policy
+
+SOURCE = os.path.join(_build.CSRC, "loss.cu")
+
+
+def _body(name):
+    """The text between the braces of a function of loss.cu, without comments."""
+    with open(SOURCE) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    found = re.search(r"\b%s\([^;{]*\)\s*\{\n(.*?)\n\}\n" % name, text, re.S)
+    assert found, name
+    return found.group(1)
+
+
+def test_no_block_leaves_its_cluster_early():
+    # the statistics: one way out, behind the barrier at which every block has sent
+    stats = _body("stats_kernel")
+    assert not re.search(r"\breturn\b", stats)
+    sends, arrives, receives = (stats.index(k) for k in ("cluster_send(", "cluster_arrive();\n    if (tid < 32) whole",
+                                                         "cluster_merge("))
+    assert sends < arrives < receives < stats.rindex("cluster_wait();")
+    # the blocks that go through rows: whatever way a thread comes back, the cluster meets
+    held = _body("held_kernel")
+    assert not re.search(r"\breturn\b", held)
+    assert re.search(r"if \(h\.cluster > 1\) cluster_leave\(\);\s*$", held)
+    # only these two send
+    with open(SOURCE) as f:
+        text = f.read()
+    assert len(re.findall(r"\bst_async_f2\(&", text)) == 1 and "st_async_f2(&" in _body("held_rows")
+    assert len(re.findall(r"\bcluster_send\(", text)) == 2
+
+
+def test_one_reading_of_the_label_decides_for_a_block():
+    """The statistics' blocks pass barriers of the block inside a branch on the label: all of a
+    block's threads take the same branch, also where another stream is writing the labels."""
+    stats = _body("stats_kernel")
+    assert "slots.label = a.labels[t]" in stats and "label = slots.label" in stats
+
+
+def test_copies_in_flight_land_before_the_block_ends():
+    loader = _body("held_rows").split("if (warp == kHeldWarps) {")[1].split("return;\n  }")[0]
+    assert re.search(r"\}\s*for \(int i = 0; i < kSlots; \+\+i\)\s*if \(again \|\| i < at\.slot\) mbar_wait\(&full", loader)
+    assert "if (!ok)\n      for" not in loader
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,dtype", [(700, 70001, BF16), (2000, 20000, BF16), (900, 40002, F32)])
+def test_many_rows_a_cluster_in_place(T, V, dtype):
+    """Each cluster goes through several rows, some ignored, and the gradient replaces them."""
+    torch.cuda.set_device(0)
+    full, x, labels = make(T, V, dtype, seed=T)
+    old, adv, w, ref = policy_inputs(x, labels, T)
+    adv[::7] = 0.0                                # rows without a gradient among them
+    want = run_policy(x, labels, old, adv, w)
+    for _ in range(3):
+        copy = x.clone()
+        got = run_policy(copy, labels, old, adv, w, d=copy)
+        for k in want:
+            assert torch.equal(got[k], want[k]), k
+    some = torch.arange(0, T, 41)
+    few = run_policy(x[some.to(DEV)], labels[some.to(DEV)], old[some], adv[some], w[some])
+    check_policy(few, x[some.to(DEV)], labels[some.to(DEV)], old[some], adv[some], w[some], None)
+    rows = some.to(DEV)
+    # rows of few and of many: other cuts, so other orders of summation; both coefficients are off by 4e-6 |logp|
+    # (below 20) and by 4e-6 of themselves
+    assert bool(((want["d"][rows].float() - few["d"].float()).abs()
+                 <= 2e-4 * want["d"][rows].float().abs().amax(1, keepdim=True).clamp(min=1e-30)
+                 + 2.0 ** -8 * few["d"].float().abs()).all())
+
+
+@pytest.mark.gpu
+def test_few_rows_over_clusters():
+    """Rows cut over clusters, ignored ones among them, many times over."""
+    from lora_rank_adapter_gb300 import training
+    from tests.test_training_loss import check_logps, oracle_logps
+    torch.cuda.set_device(0)
+    for T in (2, 5, 30, 75):
+        _, x, labels = make(T, 50001, BF16, seed=T, ignored=0.4)
+        want, _, _ = oracle_logps(x, labels)
+        first = None
+        for _ in range(50):
+            logps = torch.full((T,), 5.0, device=DEV)
+            training.lora_token_logps(x, labels, logps)
+            first = logps if first is None else first
+            assert torch.equal(logps, first)
+        check_logps(first, want)
