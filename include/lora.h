@@ -22,7 +22,8 @@
  *     `ws`/`ws_bytes`; lora_workspace_size() gives the bytes an op needs.
  *     The workspace must be 256-byte aligned and must not be shared by calls
  *     that may run concurrently.
- *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Work is
+ *   - `stream` is a cudaStream_t (NULL = the legacy default stream) of the
+ *     current device, on which the operands lie.  Work is
  *     enqueued asynchronously; no entry point synchronises with the device or
  *     reads device data on the host.
  *   - Strides are in ELEMENTS.  "Big" row-major operands (X, Y, dY, dX, x, y)

@@ -3,9 +3,9 @@
 Each function has the name of the C entry point it calls and takes torch
 tensors that already live on the GPU; it reads their pointers, shapes and
 strides, allocates the workspace the C side asks for (torch caching allocator)
-and passes the current CUDA stream.  All arithmetic runs in the library's
-CUDA kernels.  There is no fallback: if liblora.so has not been built, or a
-call fails, an exception is raised.
+and passes the current CUDA stream of the tensors' GPU, whichever GPU is current.
+All arithmetic runs in the library's CUDA kernels.  There is no fallback: if
+liblora.so has not been built, or a call fails, an exception is raised.
 """
 import ctypes
 import os
@@ -107,9 +107,34 @@ def _dtype(t):
     raise TypeError(f"unsupported dtype {t.dtype}")
 
 
-def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+def _raw_stream(stream, device):
+    """The address of the given stream, or of GPU `device`'s current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if getattr(stream, "device_index", device) != device:
+        raise ValueError(f"the stream is one of cuda:{stream.device_index}, the tensors are on cuda:{device}")
+    return stream.cuda_stream
+
+
+def _elsewhere(device, fn, args):
+    """fn(*args) while GPU `device` is the current one: what the library launches and asks of
+    the driver goes by the current GPU (a default stream has the handle 0 on every GPU)."""
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _call(name, t, stream, *args):
+    """The C entry point `name`, whose last argument is the stream, on the GPU of tensor t."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name}: the tensors have to be on a GPU")
+    fn = getattr(lib(), name)
+    args += (_raw_stream(stream, device),)
+    if device == torch._C._cuda_getDevice():
+        st = fn(*args)
+    else:
+        st = _elsewhere(device, fn, args)
+    _check(st, name)
 
 
 def _ptr(t):
@@ -135,10 +160,8 @@ def lora_forward(X, A, B, Y, scale, ws=None, stream=None):
     dt = _dtype(X)
     if ws is None:
         ws = workspace(OP_FORWARD, dt, M, K, L, r, device=X.device)
-    st = lib().lora_forward(dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(A), A.stride(0), A.stride(1),
-                            _ptr(B), B.stride(0), B.stride(1), _ptr(Y), Y.stride(0), float(scale),
-                            *_ws_args(ws), _stream(stream))
-    _check(st, "lora_forward")
+    _call("lora_forward", X, stream, dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(A), A.stride(0), A.stride(1),
+          _ptr(B), B.stride(0), B.stride(1), _ptr(Y), Y.stride(0), float(scale), *_ws_args(ws))
     return Y
 
 
@@ -151,10 +174,9 @@ def lora_forward_h(X, A, B, Y, scale, h, ws=None, stream=None):
     dt = _dtype(X)
     if ws is None:
         ws = workspace(OP_FORWARD, dt, M, K, L, r, device=X.device)
-    st = lib().lora_forward_h(dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(A), A.stride(0), A.stride(1),
-                              _ptr(B), B.stride(0), B.stride(1), _ptr(Y), Y.stride(0), float(scale),
-                              _ptr(h), h.stride(0), *_ws_args(ws), _stream(stream))
-    _check(st, "lora_forward_h")
+    _call("lora_forward_h", X, stream, dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(A), A.stride(0),
+          A.stride(1), _ptr(B), B.stride(0), B.stride(1), _ptr(Y), Y.stride(0), float(scale), _ptr(h),
+          h.stride(0), *_ws_args(ws))
     return Y, h
 
 
@@ -168,12 +190,10 @@ def lora_backward(X, dY, A, B, h, scale, dX, dA, dB, ws=None, stream=None):
     dt = _dtype(X)
     if ws is None:
         ws = workspace(OP_BACKWARD, dt, M, K, L, r, device=X.device)
-    st = lib().lora_backward(dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(dY), dY.stride(0),
-                             _ptr(A), A.stride(0), A.stride(1), _ptr(B), B.stride(0), B.stride(1),
-                             _ptr(h), h.stride(0), float(scale), _ptr(dX), dX.stride(0),
-                             _ptr(dA), dA.stride(0), dA.stride(1), _ptr(dB), dB.stride(0), dB.stride(1),
-                             *_ws_args(ws), _stream(stream))
-    _check(st, "lora_backward")
+    _call("lora_backward", X, stream, dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(dY), dY.stride(0), _ptr(A),
+          A.stride(0), A.stride(1), _ptr(B), B.stride(0), B.stride(1), _ptr(h), h.stride(0), float(scale),
+          _ptr(dX), dX.stride(0), _ptr(dA), dA.stride(0), dA.stride(1), _ptr(dB), dB.stride(0), dB.stride(1),
+          *_ws_args(ws))
     return dX, dA, dB
 
 
@@ -189,12 +209,10 @@ def lora_backward_ex(X, dY, A, B, h, scale, dX, dA, dB, flags=0, ws=None, stream
     dt = _dtype(X)
     if ws is None:
         ws = workspace(OP_BACKWARD, dt, M, K, L, r, device=X.device)
-    st = lib().lora_backward_ex(dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(dY), dY.stride(0),
-                                _ptr(A), A.stride(0), A.stride(1), _ptr(B), B.stride(0), B.stride(1),
-                                _ptr(h), h.stride(0), float(scale), _ptr(dX), dX.stride(0),
-                                _ptr(dA), dA.stride(0), dA.stride(1), _ptr(dB), dB.stride(0), dB.stride(1),
-                                int(flags), *_ws_args(ws), _stream(stream))
-    _check(st, "lora_backward_ex")
+    _call("lora_backward_ex", X, stream, dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(dY), dY.stride(0),
+          _ptr(A), A.stride(0), A.stride(1), _ptr(B), B.stride(0), B.stride(1), _ptr(h), h.stride(0),
+          float(scale), _ptr(dX), dX.stride(0), _ptr(dA), dA.stride(0), dA.stride(1), _ptr(dB), dB.stride(0),
+          dB.stride(1), int(flags), *_ws_args(ws))
     return dX, dA, dB
 
 
@@ -207,11 +225,9 @@ def lora_backward_dx_da(X, dY, A, B, scale, dX, dA, ws=None, stream=None):
     dt = _dtype(X)
     if ws is None:
         ws = workspace(OP_BACKWARD_DX_DA, dt, M, K, L, r, device=X.device)
-    st = lib().lora_backward_dx_da(dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(dY), dY.stride(0),
-                                   _ptr(A), A.stride(0), A.stride(1), _ptr(B), B.stride(0), B.stride(1),
-                                   float(scale), _ptr(dX), dX.stride(0), _ptr(dA), dA.stride(0),
-                                   dA.stride(1), *_ws_args(ws), _stream(stream))
-    _check(st, "lora_backward_dx_da")
+    _call("lora_backward_dx_da", X, stream, dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(dY), dY.stride(0),
+          _ptr(A), A.stride(0), A.stride(1), _ptr(B), B.stride(0), B.stride(1), float(scale), _ptr(dX),
+          dX.stride(0), _ptr(dA), dA.stride(0), dA.stride(1), *_ws_args(ws))
     return dX, dA
 
 
@@ -225,10 +241,9 @@ def lora_backward_db(X, A, dY, scale, dB, ws=None, stream=None):
     dt = _dtype(X)
     if ws is None:
         ws = workspace(OP_BACKWARD_DB, dt, M, K, L, r, device=X.device)
-    st = lib().lora_backward_db(dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(A), A.stride(0), A.stride(1),
-                                _ptr(dY), dY.stride(0), float(scale), _ptr(dB), dB.stride(0), dB.stride(1),
-                                *_ws_args(ws), _stream(stream))
-    _check(st, "lora_backward_db")
+    _call("lora_backward_db", X, stream, dt, M, K, L, r, _ptr(X), X.stride(0), _ptr(A), A.stride(0),
+          A.stride(1), _ptr(dY), dY.stride(0), float(scale), _ptr(dB), dB.stride(0), dB.stride(1),
+          *_ws_args(ws))
     return dB
 
 
@@ -246,8 +261,7 @@ def lora_build_schedule(slots, ranks, R, stream=None):
     n = lib().lora_schedule_size(T, S)
     sched = torch.empty(max(n, 1), dtype=torch.uint8, device=slots.device)
     ad = _addr(slots, S, R)
-    _check(lib().lora_build_schedule(ctypes.byref(ad), _ptr(ranks), _ptr(sched), sched.numel(), _stream(stream)),
-           "lora_build_schedule")
+    _call("lora_build_schedule", slots, stream, ctypes.byref(ad), _ptr(ranks), _ptr(sched), sched.numel())
     return sched
 
 
@@ -257,9 +271,8 @@ def lora_group_by_slot(slots, ranks, R, counts, perm, num_active, ws=None, strea
     if ws is None:
         ws = workspace(OP_GROUP_BY_SLOT, LORA_BF16, T, 0, 0, R, S, device=slots.device)
     ad = _addr(slots, S, R)
-    st = lib().lora_group_by_slot(ctypes.byref(ad), _ptr(ranks), _ptr(counts), _ptr(perm), _ptr(num_active),
-                                  *_ws_args(ws), _stream(stream))
-    _check(st, "lora_group_by_slot")
+    _call("lora_group_by_slot", slots, stream, ctypes.byref(ad), _ptr(ranks), _ptr(counts), _ptr(perm),
+          _ptr(num_active), *_ws_args(ws))
 
 
 def lora_shrink(x, a, slots, ranks, R, h, num_slices=1, ws=None, stream=None, schedule=None):
@@ -271,9 +284,8 @@ def lora_shrink(x, a, slots, ranks, R, h, num_slices=1, ws=None, stream=None, sc
     if ws is None:
         ws = workspace(OP_SHRINK, LORA_BF16, T, IN, num_slices * R, R, S, device=x.device)
     ad = _addr(slots, S, R, schedule)
-    st = lib().lora_shrink(ctypes.byref(ad), _ptr(ranks), IN, num_slices, _ptr(x), x.stride(0), _ptr(a),
-                           a.stride(0), a.stride(1), _ptr(h), h.stride(0), *_ws_args(ws), _stream(stream))
-    _check(st, "lora_shrink")
+    _call("lora_shrink", x, stream, ctypes.byref(ad), _ptr(ranks), IN, num_slices, _ptr(x), x.stride(0),
+          _ptr(a), a.stride(0), a.stride(1), _ptr(h), h.stride(0), *_ws_args(ws))
     return h
 
 
@@ -292,10 +304,8 @@ def lora_expand(h, b, slots, ranks, scalings, y, out_slices, R, ws=None, stream=
     if ws is None:
         ws = workspace(OP_EXPAND, LORA_BF16, T, 0, O, R, S, device=y.device)
     ad = _addr(slots, S, R, schedule)
-    st = lib().lora_expand(ctypes.byref(ad), _ptr(ranks), _ptr(scalings), osl, n, _ptr(h), h.stride(0),
-                           _ptr(b), b.stride(0), b.stride(1), b.stride(2), _ptr(y), y.stride(0),
-                           *_ws_args(ws), _stream(stream))
-    _check(st, "lora_expand")
+    _call("lora_expand", h, stream, ctypes.byref(ad), _ptr(ranks), _ptr(scalings), osl, n, _ptr(h),
+          h.stride(0), _ptr(b), b.stride(0), b.stride(1), b.stride(2), _ptr(y), y.stride(0), *_ws_args(ws))
     return y
 
 
@@ -310,11 +320,9 @@ def lora_apply_linear(x, a, b, slots, ranks, scalings, y, out_slices, R, ws=None
     if ws is None:
         ws = workspace(OP_APPLY_LINEAR, LORA_BF16, T, IN, O, R, S, device=x.device)
     ad = _addr(slots, S, R, schedule)
-    st = lib().lora_apply_linear(ctypes.byref(ad), _ptr(ranks), _ptr(scalings), osl, n, IN, _ptr(x),
-                                 x.stride(0), _ptr(a), a.stride(0), a.stride(1), _ptr(b), b.stride(0),
-                                 b.stride(1), b.stride(2), _ptr(y), y.stride(0), *_ws_args(ws),
-                                 _stream(stream))
-    _check(st, "lora_apply_linear")
+    _call("lora_apply_linear", x, stream, ctypes.byref(ad), _ptr(ranks), _ptr(scalings), osl, n, IN, _ptr(x),
+          x.stride(0), _ptr(a), a.stride(0), a.stride(1), _ptr(b), b.stride(0), b.stride(1), b.stride(2),
+          _ptr(y), y.stride(0), *_ws_args(ws))
     return y
 
 
@@ -323,9 +331,8 @@ def lora_gather_shrink(ids, a, slots, ranks, R, h, stream=None):
     S, RR, V = a.shape
     assert RR == R and ids.dtype == torch.int64
     ad = _addr(slots, S, R)
-    st = lib().lora_gather_shrink(ctypes.byref(ad), _ptr(ranks), V, _ptr(ids), _ptr(a), a.stride(0),
-                                  a.stride(1), a.stride(2), _ptr(h), h.stride(0), _stream(stream))
-    _check(st, "lora_gather_shrink")
+    _call("lora_gather_shrink", ids, stream, ctypes.byref(ad), _ptr(ranks), V, _ptr(ids), _ptr(a),
+          a.stride(0), a.stride(1), a.stride(2), _ptr(h), h.stride(0))
     return h
 
 
