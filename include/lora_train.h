@@ -158,6 +158,22 @@ LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_
  * next step would be huge).  p's update uses m and u before they are rounded.
  * The states follow IEEE single rounding step by step in the order written, so
  * equal inputs give equal codes everywhere.
+ *   Rounding to nearest keeps a state for a few steps, not for thousands: e4m3
+ * values lie 6 to 12 % apart, a step with beta2 = 0.999 lowers u by 0.05 % at most,
+ * so codes stay where they are relative to the block's largest one, and each u
+ * follows that element instead of its own gradients (one outlier in a block leaves
+ * the others' u at 0.3 of their value, steps three times too large, for thousands
+ * of steps).  LORA_ADAMW_STOCHASTIC rounds both states at random instead, up with
+ * the probability of how far up a value is, so that each follows its gradients on
+ * average (u then scatters by some 17 % about its value).  The random bits are a
+ * function of the step, the chunk's number in the table and the element's place in
+ * the chunk, so a step is reproducible all the same:
+ *     mix(x): x ^= x >> 16; x *= A; x ^= x >> 15; x *= B; x ^= x >> 16; x *= A; x ^= x >> 15
+ *     x = (mix(mix(step + mix(step >> 32)) + chunk) + place) * A; x ^= x >> 15; x *= B; x ^= x >> 16
+ * in 32 bits, A = 0x9E3779B9, B = 0xBB67AE85; m takes the low 16 bits of x, u the
+ * high ones, and q = value * (448 / a) goes up when its distance from the value
+ * below, in 2^-20 of the distance between the two (below 2^-6 on q + 2^-6 rounded to
+ * fp32), and 16 * bits + 8 add up to 2^20 or more.
  *   p, g    dtype param_dtype / grad_dtype of the plan, contiguous [numel]
  *   codes   uint8 (e4m3) [numel];  scales  float [ceil(numel / LORA_ADAMW_BLOCK)]
  * Elements need only the alignment of their type; tensors whose pointers are all
@@ -167,6 +183,7 @@ LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_
 #define LORA_ADAMW_CHUNK 2048
 #define LORA_ADAMW_STATE_8BIT 1u
 #define LORA_ADAMW_MASTER 2u
+#define LORA_ADAMW_STOCHASTIC 16u      /* with LORA_ADAMW_STATE_8BIT only */
 
 typedef struct {
     void *param;

@@ -176,6 +176,36 @@ __device__ __forceinline__ float reciprocal(float x) {
   return r;
 }
 
+// Bits for the rounding of 8-bit states, 16 for each of the two states of an element:
+// multiplications by odd numbers and shifted exclusive ors (the golden ratio's and the
+// square root of three's fractions of 2^32), as in multiplicative hashing.
+constexpr uint32_t kMix1 = 0x9E3779B9u, kMix2 = 0xBB67AE85u;
+__host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= kMix1;
+  x ^= x >> 15;
+  x *= kMix2;
+  x ^= x >> 16;
+  x *= kMix1;
+  return x ^ (x >> 15);
+}
+// `x1`: a place times kMix1
+__device__ __forceinline__ uint32_t place_bits(uint32_t x1) {
+  x1 ^= x1 >> 15;
+  x1 *= kMix2;
+  return x1 ^ (x1 >> 16);
+}
+
+// q to one of the two e4m3 values around it, the upper one with the probability of how
+// far up q is.  `bits` (20 of them, the lowest four 0) are added below the three bits
+// of mantissa that stay; below 2^-6, where the values lie 2^-9 apart, after 2^-6 has
+// been added.  Values at a code stay there.
+__device__ __forceinline__ float to_code(float q, uint32_t bits) {
+  const float base = fabsf(q) < 0.015625f ? copysignf(0.015625f, q) : 0.f;
+  const uint32_t t = __float_as_uint(__fadd_rn(q, base)) + bits + 8u;
+  return __fsub_rn(__uint_as_float(t & 0xfff00000u), base);
+}
+
 // ----------------------------------------------------------------------------- the step
 struct StepArgs {
   const AdamChunk *table;
@@ -186,10 +216,12 @@ struct StepArgs {
   float root;                  // 1 / sqrt(1 - beta2^step)
   float eps;
   float one;                   // 1
+  uint32_t noise;              // of the step
 };
 
 // A warp's 256 elements as they lie in memory.
-template <typename P, typename G, bool k8, bool kMaster>
+// kNoise: 8-bit states rounded at random.
+template <typename P, typename G, bool k8, bool kNoise, bool kMaster>
 struct Block {
   using S = std::conditional_t<k8, uint8_t, float>;
   using W = std::conditional_t<kMaster, float, P>;
@@ -222,8 +254,9 @@ struct Block {
   // fma(x, 1, y) with the 1 from memory, because the compiler contracts a packed
   // product and sum to one rounding: equal inputs give equal 8-bit codes,
   // whoever computes them.
+  // `key`: of the chunk and the step.
   template <bool kWhole>
-  __device__ __forceinline__ void step(const StepArgs &a, float factor, const AdamChunk &c, int block) {
+  __device__ __forceinline__ void step(const StepArgs &a, float factor, const AdamChunk &c, int block, uint32_t key) {
     constexpr int kPairs = kLane / 2;
     auto both = [](float x) { return pk2(x, x); };
     uint64_t pw[kPairs], pg[kPairs], pm[kPairs], pv[kPairs];
@@ -260,9 +293,18 @@ struct Block {
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         pm[i] = mul2(pm[i], mup);
-        // the smallest positive code, 2^-9, for a root that would round to zero
         const float2 u = unpk2(pv[i]);
         float2 q = unpk2(mul2(pv[i], vup));
+        if (kNoise) {
+          const uint32_t x1 = (key + block * LORA_ADAMW_BLOCK + 4 * lane_id()) * kMix1;
+          const uint32_t e = 128 * (i / 2) + 2 * (i % 2);
+          const uint32_t r0 = place_bits(x1 + e * kMix1), r1 = place_bits(x1 + (e + 1) * kMix1);
+          const float2 f = unpk2(pm[i]);
+          pm[i] = pk2(to_code(f.x, (r0 << 4) & 0xffff0u), to_code(f.y, (r1 << 4) & 0xffff0u));
+          q.x = to_code(q.x, (r0 >> 12) & 0xffff0u);
+          q.y = to_code(q.y, (r1 >> 12) & 0xffff0u);
+        }
+        // the smallest positive code, 2^-9, for a root that would round to zero
         if (u.x > 0.f) q.x = fmaxf(q.x, 0.001953125f);
         if (u.y > 0.f) q.y = fmaxf(q.y, 0.001953125f);
         pv[i] = pk2(q.x, q.y);
@@ -292,25 +334,27 @@ struct Block {
 // threads an SM (64 registers) take 261 us where 72 registers took 273, nine blocks
 // 273 and ten 297 (spills); four blocks of 256 threads for 32-bit states 820, five 865.
 constexpr int kEach8 = 2, kEach32 = 1;
-template <typename P, typename G, bool k8, bool kMaster>
+template <typename P, typename G, bool k8, bool kNoise, bool kMaster>
 __global__ void __launch_bounds__(kThreads / (k8 ? kEach8 : kEach32), k8 ? 8 : 4) adamw_kernel(StepArgs a) {
   constexpr int kEach = k8 ? kEach8 : kEach32, kWarps = kThreads / 32 / kEach;
   pdl_wait();
   // last to first: the norm before this step has left the last gradients in L2
-  const AdamChunk c = a.table[gridDim.x - 1 - blockIdx.x];
+  const uint32_t chunk = gridDim.x - 1 - blockIdx.x;
+  const AdamChunk c = a.table[chunk];
   const float factor = a.factor ? *a.factor : 1.f;
   const int warp = threadIdx.x >> 5;
-  Block<P, G, k8, kMaster> b[kEach];
+  const uint32_t key = kNoise ? mix(a.noise + chunk) : 0;
+  Block<P, G, k8, kNoise, kMaster> b[kEach];
   if (c.wide && c.count == LORA_ADAMW_CHUNK) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) b[i].template load<true>(c, warp + i * kWarps);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) b[i].template step<true>(a, factor, c, warp + i * kWarps);
+    for (int i = 0; i < kEach; ++i) b[i].template step<true>(a, factor, c, warp + i * kWarps, key);
   } else {
     // whole warps: a block's scale needs all 32 lanes
     for (int i = warp; i * LORA_ADAMW_BLOCK < (int)c.count; i += kWarps) {
       b[0].template load<false>(c, i);
-      b[0].template step<false>(a, factor, c, i);
+      b[0].template step<false>(a, factor, c, i, key);
     }
   }
 }
@@ -370,15 +414,17 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const AdamChunk *table, 
   }
 }
 
-template <typename P, typename G, bool k8>
+template <typename P, typename G, bool k8, bool kNoise>
 cudaError_t run_step(const lora_adamw_plan_t &plan, const StepArgs &a, cudaStream_t st) {
   const dim3 grid((unsigned)plan.chunks), block(kThreads / (k8 ? kEach8 : kEach32));
-  return (plan.flags & LORA_ADAMW_MASTER) ? launch(adamw_kernel<P, G, k8, true>, grid, block, 0, st, 1, true, a)
-                                          : launch(adamw_kernel<P, G, k8, false>, grid, block, 0, st, 1, true, a);
+  return (plan.flags & LORA_ADAMW_MASTER) ? launch(adamw_kernel<P, G, k8, kNoise, true>, grid, block, 0, st, 1, true, a)
+                                          : launch(adamw_kernel<P, G, k8, kNoise, false>, grid, block, 0, st, 1, true, a);
 }
 template <typename P, typename G>
 cudaError_t run_step(const lora_adamw_plan_t &plan, const StepArgs &a, cudaStream_t st) {
-  return (plan.flags & LORA_ADAMW_STATE_8BIT) ? run_step<P, G, true>(plan, a, st) : run_step<P, G, false>(plan, a, st);
+  if (plan.flags & LORA_ADAMW_STOCHASTIC) return run_step<P, G, true, true>(plan, a, st);
+  return (plan.flags & LORA_ADAMW_STATE_8BIT) ? run_step<P, G, true, false>(plan, a, st)
+                                              : run_step<P, G, false, false>(plan, a, st);
 }
 
 }  // namespace
@@ -450,6 +496,7 @@ lora_status_t adamw(const lora_adamw_plan_t &plan, const lora_adamw_hyper_t &h, 
   a.root = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
   a.eps = (float)h.eps;
   a.one = 1.f;
+  a.noise = mix((uint32_t)h.step + mix((uint32_t)(h.step >> 32)));
   const bool p16 = plan.param_dtype == LORA_BF16, g16 = plan.grad_dtype == LORA_BF16;
   cudaError_t e;
   if (p16)

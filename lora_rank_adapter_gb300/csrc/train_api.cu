@@ -55,14 +55,18 @@ LossArgs loss_args(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits,
   return a;
 }
 
+bool flags_ok(uint32_t flags) {
+  if (flags & ~(LORA_ADAMW_STATE_8BIT | LORA_ADAMW_MASTER | LORA_ADAMW_STOCHASTIC)) return false;
+  return !(flags & LORA_ADAMW_STOCHASTIC) || (flags & LORA_ADAMW_STATE_8BIT);
+}
+
 lora_status_t check_plan(const lora_adamw_plan_t *plan) {
   if (plan == nullptr || plan->chunks < 0 || plan->chunks >= kMaxDim) return LORA_ERR_INVALID_ARG;
   if (plan->table == nullptr || !aligned(plan->table, 256)) return LORA_ERR_INVALID_ARG;
   if ((plan->param_dtype != LORA_F32 && plan->param_dtype != LORA_BF16) ||
       (plan->grad_dtype != LORA_F32 && plan->grad_dtype != LORA_BF16))
     return LORA_ERR_UNSUPPORTED;
-  if (plan->flags & ~(LORA_ADAMW_STATE_8BIT | LORA_ADAMW_MASTER)) return LORA_ERR_INVALID_ARG;
-  return LORA_OK;
+  return flags_ok(plan->flags) ? LORA_OK : LORA_ERR_INVALID_ARG;
 }
 
 // Chunks of the tensors, or -1 if a size is out of range.
@@ -210,7 +214,7 @@ lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int32_t n, lo
   lora_adamw_plan_t made = {table, chunks, (int32_t)param_dtype, (int32_t)grad_dtype, flags, 0};
   if ((param_dtype != LORA_F32 && param_dtype != LORA_BF16) || (grad_dtype != LORA_F32 && grad_dtype != LORA_BF16))
     return LORA_ERR_UNSUPPORTED;
-  if (flags & ~(LORA_ADAMW_STATE_8BIT | LORA_ADAMW_MASTER)) return LORA_ERR_INVALID_ARG;
+  if (!flags_ok(flags)) return LORA_ERR_INVALID_ARG;
   const bool s8 = (flags & LORA_ADAMW_STATE_8BIT) != 0;
   for (int32_t i = 0; i < n; ++i) {
     const lora_adamw_tensor_t &t = tensors[i];

@@ -338,7 +338,8 @@ def policy_loss(logits, labels, old_logps, advantages, weights=None, ref_logps=N
 class AdamW:
     """AdamW over an adapter's tensors (all of one dtype), one launch a step.
 
-    state_bits: 32, or 8 for e4m3 states with a scale for each 256 elements.  masters: keep
+    state_bits: 32, or 8 for e4m3 states with a scale for each 256 elements, rounded at
+    random (reproducibly) so that they follow their gradients over any number of steps.  masters: keep
     fp32 copies that the step updates (for bf16 parameters whose updates are smaller than
     their rounding).  max_norm: clip the gradients' global norm to it; `norm` then holds
     (norm, factor) of the last step.  Parameters without a gradient sit a step out."""
@@ -407,7 +408,8 @@ class AdamW:
             self._plan = training.lora_adamw_plan([self.params[i].detach() for i in at], grads, pick(self.exp_avg),
                                                   pick(self.exp_avg_sq), masters=pick(self.masters),
                                                   exp_avg_scales=pick(self.exp_avg_scale),
-                                                  exp_avg_sq_scales=pick(self.exp_avg_sq_scale))
+                                                  exp_avg_sq_scales=pick(self.exp_avg_sq_scale),
+                                                  stochastic=self.exp_avg_scale is not None)
             self._plan.tensors = None        # gradients are not kept alive beyond the step that uses them
             self._laid_out = laid_out
         self.step_count += 1

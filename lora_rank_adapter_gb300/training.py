@@ -31,7 +31,7 @@ TRAIN_EXPORTS = ["lora_train_workspace_size", "lora_token_logps", "lora_token_lo
 TRAIN_PREFERENCE_LOSS, TRAIN_POLICY_LOSS = 0, 1
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PREF_LENGTH_NORMALIZE = 1
-ADAMW_STATE_8BIT, ADAMW_MASTER = 1, 2
+ADAMW_STATE_8BIT, ADAMW_MASTER, ADAMW_STOCHASTIC = 1, 2, 16
 ADAMW_BLOCK, ADAMW_CHUNK = 256, 2048
 POLICY_HELD_BYTES = 768 << 10      # rows up to here need no workspace in lora_policy_loss
 
@@ -281,17 +281,19 @@ def _dense(t):
 
 
 def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_scales=None, exp_avg_sq_scales=None,
-                    stream=None):
+                    stream=None, stochastic=False):
     """Lays out the tensors of lora_grad_norm and lora_adamw.  params and grads: lists of
     bf16 or fp32 tensors (one dtype each).  States in 32 bits: fp32 tensors.  States in 8
     bits: float8_e4m3fn (or uint8) codes of the same shape, with fp32 scales
     [ceil(numel / 256)] in exp_avg_scales / exp_avg_sq_scales (exp_avg_sq then holds the
     square root of the second moment).  masters: fp32 copies that the step updates, the
     parameters being their rounding.  A tensor, its gradient, states and master share one
-    dense layout."""
+    dense layout.  stochastic: 8-bit states are rounded at random (reproducibly, by step
+    and place), without which they stop following their gradients over some thousand steps."""
     n = len(params)
     s8 = exp_avg_scales is not None
     _expect(s8 == (exp_avg_sq_scales is not None), "8-bit states need both lists of scales")
+    _expect(s8 or not stochastic, "stochastic rounding is for 8-bit states")
     lists = {"grads": grads, "exp_avg": exp_avg, "exp_avg_sq": exp_avg_sq, "masters": masters,
              "exp_avg_scales": exp_avg_scales, "exp_avg_sq_scales": exp_avg_sq_scales}
     for name, values in lists.items():
@@ -319,7 +321,8 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
         addr = lambda values: values[i].data_ptr() if values is not None and p.numel() else None  # noqa: E731
         table_in[i] = AdamWTensor(addr(params), addr(grads), addr(exp_avg), addr(exp_avg_sq), addr(exp_avg_scales),
                                   addr(exp_avg_sq_scales), addr(masters), p.numel())
-    flags = (ADAMW_STATE_8BIT if s8 else 0) | (ADAMW_MASTER if masters is not None else 0)
+    flags = (ADAMW_STATE_8BIT if s8 else 0) | (ADAMW_MASTER if masters is not None else 0) | \
+        (ADAMW_STOCHASTIC if stochastic else 0)
     size = lib().lora_adamw_table_size(table_in, n)
     table = _bytes(size, device, stream)
     struct = AdamWPlanStruct()
