@@ -243,13 +243,8 @@ struct ClusterSlots {
   float2 pair[kMaxCluster];
   int64_t label;       // of the block's row, read once for all its threads
 };
-// Whole warps arrive and wait together ...
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// ... or each thread when it gets here.
-__device__ __forceinline__ void cluster_leave() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 __device__ __forceinline__ void st_dsmem_f2(const void *local_ptr, uint32_t cta, float2 v) {
   uint32_t local = smem_u32(local_ptr), remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(cta));
@@ -757,9 +752,9 @@ struct RingAt {
 };
 
 template <typename E>
-__device__ __forceinline__ void held_rows(const HeldArgs &h) {
+__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArgs h) {
   extern __shared__ __align__(128) uint4 ring[];
-  __shared__ uint64_t full[kSlots], empty[kSlots], ready[2];
+  __shared__ uint64_t full[kSlots], empty[kSlots], ready[2], done;
   __shared__ float2 pairs[2][kMaxCluster * kHeldWarps];  // (m, s) of every warp of the cluster, two exchanges
   const RowArgs &a = h.r;
   constexpr int N = Elem<E>::kVec;
@@ -772,6 +767,7 @@ __device__ __forceinline__ void held_rows(const HeldArgs &h) {
       mbar_init(&empty[i], kHeldWarps);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C == 1 ? kHeldWarps : 1);
+    mbar_init(&done, C * kHeldWarps);
     fence_barrier_init();
   }
   __syncthreads();
@@ -811,6 +807,13 @@ __device__ __forceinline__ void held_rows(const HeldArgs &h) {
     // The last copies land before the block ends, whoever else waits for them.
     for (int i = 0; i < kSlots; ++i)
       if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
+    // And the block does not end before every warp of the cluster has sent its last
+    // pair here, also where a wait ran out, or where another stream wrote the labels and
+    // warps took different rows for ignored: for as many limits as a warp's own waits
+    // may take.  (632 us for the rows above; 641 with a barrier of the cluster at the
+    // end, 630 where the block just leaves.)
+    if (C > 1)
+      for (int i = 0; i < kSlots + 2 && !mbar_wait<true>(&done, 0); ++i) {}
     return;
   }
 
@@ -866,7 +869,7 @@ __device__ __forceinline__ void held_rows(const HeldArgs &h) {
                     make_float2(m, s));
     }
     ok = mbar_wait<true>(&ready[set], (count >> 1) & 1) && ok;
-    if (!__all_sync(0xffffffffu, ok)) return;            // a wait ran out: the error word is set
+    if (!__all_sync(0xffffffffu, ok)) break;             // a wait ran out: the error word is set
     ++count;
     m = kNegInf;
     s = 0.f;
@@ -910,16 +913,7 @@ __device__ __forceinline__ void held_rows(const HeldArgs &h) {
       zero_span<E, kHeldWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N, tid);
     }
   }
-}
-
-// However a thread comes back (the loader ahead of the others, a warp whose wait ran
-// out early), its block stays until all blocks of the cluster have done: their warps
-// store into its shared memory for as long as they go through rows.  All waits within
-// are bounded, so all threads come here.
-template <typename E>
-__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(const __grid_constant__ HeldArgs h) {
-  held_rows<E>(h);
-  if (h.cluster > 1) cluster_leave();
+  if (C > 1 && lane < C) mbar_arrive_remote(&done, lane);
 }
 
 // The three metrics from the log-probabilities, in a fixed order.  (The terms are

@@ -23,6 +23,11 @@ def _body(name):
     return found.group(1)
 
 
+def _held():
+    """The loader's part of the policy kernel up to its return, and the other warps' part."""
+    return _body("held_kernel").split("if (warp == kHeldWarps) {")[1].split("    return;\n  }\n", 1)
+
+
 def test_no_block_leaves_its_cluster_early():
     # the statistics: one way out, behind the barrier at which every block has sent
     stats = _body("stats_kernel")
@@ -30,14 +35,17 @@ def test_no_block_leaves_its_cluster_early():
     sends, arrives, receives = (stats.index(k) for k in ("cluster_send(", "cluster_arrive();\n    if (tid < 32) whole",
                                                          "cluster_merge("))
     assert sends < arrives < receives < stats.rindex("cluster_wait();")
-    # the blocks that go through rows: whatever way a thread comes back, the cluster meets
-    held = _body("held_kernel")
-    assert not re.search(r"\breturn\b", held)
-    assert re.search(r"if \(h\.cluster > 1\) cluster_leave\(\);\s*$", held)
+    # the blocks that go through rows: each warp ends by telling all blocks that it has sent its
+    # last, on every path, and the loader keeps its block until all have
+    loader, work = _held()
+    assert loader.index("mbar_wait<true>(&done, 0)") > loader.index("mbar_wait(&full")
+    assert not re.search(r"\breturn\b", work)
+    assert re.search(r"\n  \}\s*if \(C > 1 && lane < C\) mbar_arrive_remote\(&done, lane\);\s*$", work)
+    assert "mbar_init(&done, C * kHeldWarps);" in _body("held_kernel")
     # only these two send
     with open(SOURCE) as f:
         text = f.read()
-    assert len(re.findall(r"\bst_async_f2\(&", text)) == 1 and "st_async_f2(&" in _body("held_rows")
+    assert len(re.findall(r"\bst_async_f2\(&", text)) == 1 and "st_async_f2(&" in work
     assert len(re.findall(r"\bcluster_send\(", text)) == 2
 
 
@@ -49,7 +57,7 @@ def test_one_reading_of_the_label_decides_for_a_block():
 
 
 def test_copies_in_flight_land_before_the_block_ends():
-    loader = _body("held_rows").split("if (warp == kHeldWarps) {")[1].split("return;\n  }")[0]
+    loader, _ = _held()
     assert re.search(r"\}\s*for \(int i = 0; i < kSlots; \+\+i\)\s*if \(again \|\| i < at\.slot\) mbar_wait\(&full", loader)
     assert "if (!ok)\n      for" not in loader
 
