@@ -858,6 +858,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
     // reach memory.  It is sent when `picked` has come (h.zero is 0): past the
     // exchange any warp may write that element.
     if (C == 1) {
+      __syncwarp();                                      // every lane's reads of the row come before the arrival
       if (lane == 0) {
         pairs[set][warp] = make_float2(m, s);
         mbar_arrive(&ready[set]);

@@ -62,6 +62,14 @@ def test_copies_in_flight_land_before_the_block_ends():
     assert "if (!ok)\n      for" not in loader
 
 
+def test_reads_of_a_row_come_before_the_arrival_that_lets_others_write_it():
+    """In place, any warp of the block may write the label's element past the exchange: the arrival
+    for a warp follows the reads of all its lanes, by a barrier of the warp, or carries the value."""
+    _, work = _held()
+    assert re.search(r"if \(C == 1\) \{\s*__syncwarp\(\);\s*if \(lane == 0\)", work)
+    assert "lane + (__float_as_uint(picked) & h.zero)" in work
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,V,dtype", [(700, 70001, BF16), (2000, 20000, BF16), (900, 40002, F32)])
 def test_many_rows_a_cluster_in_place(T, V, dtype):
