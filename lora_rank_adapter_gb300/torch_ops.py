@@ -22,7 +22,8 @@ loss operators of `training`, and `AdamW` an optimizer on lora_grad_norm / lora_
     loss.backward(); optimizer.step()
 The losses form their gradient with the forward pass, while a row is at hand; the
 backward pass multiplies it by the incoming gradient in place (no pass over it when
-that is 1) and hands it on, so it can be taken once.
+that is 1) and hands it on, so it can be taken once and has no gradient of its own:
+second derivatives (create_graph) through a loss raise.
 """
 from typing import List, Optional, Sequence
 
@@ -275,32 +276,55 @@ class TokenLogpsFn(torch.autograd.Function):
         return token_logps_backward_op(logits, labels, stats, dlogps.contiguous(), ctx.temperature), None, None
 
 
+def _anchor(logits):
+    """A tensor of no elements with the logits' history, or None where they have none: it keeps
+    the way back to them open and not their memory."""
+    return logits[:0].clone() if logits.requires_grad and torch.is_grad_enabled() else None
+
+
+class _NoSecondFn(torch.autograd.Function):
+    """The tensor itself as if made from the logits, by a node that refuses to be gone back
+    through.  (A tensor without a history would be a constant to second derivatives.)"""
+
+    @staticmethod
+    def forward(ctx, d, anchor):
+        return d.detach()
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("this loss has no second derivatives: its gradient is made with its forward pass")
+
+
 def _hand_on(ctx, dloss):
     """The gradient that the forward pass made, times the loss's own: once."""
     if ctx.dlogits is None:
         raise RuntimeError("the gradient of this loss is made once, with its forward pass, and has been taken")
     d, ctx.dlogits = ctx.dlogits, None
     training.lora_scale_gradient(d, dloss.float().reshape(1))
+    if torch.is_grad_enabled():              # create_graph
+        d = _NoSecondFn.apply(d, *ctx.saved_tensors)
     return d
 
 
 class PreferenceLossFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, *args):
+    def forward(ctx, logits, anchor, *args):
         loss, pair, seq, tok, d = preference_loss_op(logits, *args, ctx.needs_input_grad[0])
+        ctx.save_for_backward(anchor)
         ctx.dlogits = d if ctx.needs_input_grad[0] else None
         ctx.mark_non_differentiable(pair, seq, tok)
         return loss, pair, seq, tok
 
     @staticmethod
     def backward(ctx, dloss, *_):
-        return (_hand_on(ctx, dloss),) + (None,) * 8
+        return (_hand_on(ctx, dloss),) + (None,) * 9
 
 
 class PolicyLossFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, *args):
+    def forward(ctx, logits, anchor, *args):
         metrics, tok, d = policy_loss_op(logits, *args, ctx.needs_input_grad[0])
+        ctx.save_for_backward(anchor)
         ctx.dlogits = d if ctx.needs_input_grad[0] else None
         loss = metrics[0].clone()
         ctx.mark_non_differentiable(metrics, tok)
@@ -308,7 +332,7 @@ class PolicyLossFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dloss, *_):
-        return (_hand_on(ctx, dloss),) + (None,) * 9
+        return (_hand_on(ctx, dloss),) + (None,) * 10
 
 
 def token_logps(logits: torch.Tensor, labels: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
@@ -321,8 +345,9 @@ def preference_loss(logits, labels, cu_seqlens, ref_logps=None, beta=0.1, kind="
                     length_normalize=False, temperature=1.0):
     """(loss, pair_loss [P], seq_logps [2P]) of P pairs of packed sequences, pair p preferring
     sequence p to sequence P + p; the loss is differentiable in the logits."""
-    loss, pair, seq, _ = PreferenceLossFn.apply(logits, labels, cu_seqlens, ref_logps, float(beta), kind,
-                                                float(label_smoothing), bool(length_normalize), float(temperature))
+    loss, pair, seq, _ = PreferenceLossFn.apply(logits, _anchor(logits), labels, cu_seqlens, ref_logps, float(beta),
+                                                kind, float(label_smoothing), bool(length_normalize),
+                                                float(temperature))
     return loss, pair, seq
 
 
@@ -330,8 +355,8 @@ def policy_loss(logits, labels, old_logps, advantages, weights=None, ref_logps=N
                 kl_beta=0.0, temperature=1.0):
     """(loss, metrics [3], token_logps [T]) of the clipped policy loss with a KL term; the loss
     is differentiable in the logits."""
-    return PolicyLossFn.apply(logits, labels, old_logps, advantages, weights, ref_logps, float(clip_low),
-                              float(clip_high), float(kl_beta), float(temperature))
+    return PolicyLossFn.apply(logits, _anchor(logits), labels, old_logps, advantages, weights, ref_logps,
+                              float(clip_low), float(clip_high), float(kl_beta), float(temperature))
 
 
 # ----------------------------------------------------------------------------- optimizer
