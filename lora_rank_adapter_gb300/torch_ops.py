@@ -367,7 +367,9 @@ class AdamW:
     random (reproducibly) so that they follow their gradients over any number of steps.  masters: keep
     fp32 copies that the step updates (for bf16 parameters whose updates are smaller than
     their rounding).  max_norm: clip the gradients' global norm to it; `norm` then holds
-    (norm, factor) of the last step.  Parameters without a gradient sit a step out."""
+    (norm, factor) of the last step.  Parameters without a gradient sit a step out: each
+    has its own count of steps, which its bias corrections go by (one launch for each
+    count there is)."""
 
     def __init__(self, params, lr=1e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, masters=False,
                  max_norm=None):
@@ -375,7 +377,9 @@ class AdamW:
         if state_bits not in (8, 32):
             raise ValueError("state_bits has to be 8 or 32")
         self.lr, self.betas, self.eps, self.weight_decay, self.max_norm = lr, betas, eps, weight_decay, max_norm
-        self.step_count, self._plan, self._laid_out = 0, None, None
+        self.step_count = 0                  # of the steps taken
+        self._behind = {}                    # by parameter: how many of them it sat out
+        self._plan, self._groups, self._laid_out = None, None, None
         self.norm = torch.zeros(2, device=self.params[0].device) if max_norm is not None and self.params else None
         zeros = lambda p, dt: torch.zeros_like(p, dtype=dt, requires_grad=False)  # noqa: E731
         dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
@@ -398,15 +402,21 @@ class AdamW:
                                   ("exp_avg_sq_scale", self.exp_avg_sq_scale), ("masters", self.masters))
                 if v is not None}
 
+    def _steps(self):
+        """The count of steps; of each parameter, where they differ."""
+        counts = [self.step_count - self._behind.get(i, 0) for i in range(len(self.params))]
+        return self.step_count if not any(self._behind.values()) else counts
+
     def state_dict(self):
-        """The step count and copies of the states."""
-        return {"step": self.step_count, **{k: [t.clone() for t in v] for k, v in self._states().items()}}
+        """The step count (a list of each parameter's, where they differ) and copies of the states."""
+        return {"step": self._steps(), **{k: [t.clone() for t in v] for k, v in self._states().items()}}
 
     @torch.no_grad()
     def load_state_dict(self, state):
         """Takes over what state_dict() of an optimizer with the same parameters and options gave."""
         mine = self._states()
-        if set(state) != set(mine) | {"step"} or any(len(state[k]) != len(v) for k, v in mine.items()):
+        if set(state) != set(mine) | {"step"} or any(len(state[k]) != len(v) for k, v in mine.items()) or \
+                isinstance(state["step"], (list, tuple)) and len(state["step"]) != len(self.params):
             raise ValueError("the state is of another optimizer: other options or other parameters")
         for k, v in mine.items():
             for t, u in zip(v, state[k]):
@@ -415,7 +425,10 @@ class AdamW:
         for k, v in mine.items():
             for t, u in zip(v, state[k]):
                 t.copy_(u)
-        self.step_count = int(state["step"])
+        step = state["step"]
+        counts = [int(c) for c in step] if isinstance(step, (list, tuple)) else [int(step)] * len(self.params)
+        self.step_count = max(counts, default=0)
+        self._behind = {i: self.step_count - c for i, c in enumerate(counts) if c != self.step_count}
 
     @torch.no_grad()
     def step(self):
@@ -428,17 +441,36 @@ class AdamW:
         grads = [g if g.stride() == p.stride() else torch.empty_like(p, dtype=g.dtype).copy_(g)
                  for p, g in ((self.params[i], self.params[i].grad) for i in at)]
         laid_out = [(i, g.data_ptr(), g.dtype, g.stride(), self.params[i].data_ptr()) for i, g in zip(at, grads)]
-        if self._plan is None or laid_out != self._laid_out:
-            pick = lambda v: None if v is None else [v[i] for i in at]  # noqa: E731
-            self._plan = training.lora_adamw_plan([self.params[i].detach() for i in at], grads, pick(self.exp_avg),
-                                                  pick(self.exp_avg_sq), masters=pick(self.masters),
-                                                  exp_avg_scales=pick(self.exp_avg_scale),
-                                                  exp_avg_sq_scales=pick(self.exp_avg_sq_scale),
-                                                  stochastic=self.exp_avg_scale is not None)
-            self._plan.tensors = None        # gradients are not kept alive beyond the step that uses them
-            self._laid_out = laid_out
+        missed = [self._behind.get(i, 0) for i in at] if self._behind else None
+        if self._laid_out != (laid_out, missed):
+            self._laid_out = None
+            self._lay_out(at, grads, missed)
+            self._laid_out = (laid_out, missed)
         self.step_count += 1
+        if len(at) < len(self.params):
+            for i in set(range(len(self.params))).difference(at):
+                self._behind[i] = self._behind.get(i, 0) + 1
         if self.max_norm is not None:
             training.lora_grad_norm(self._plan, self.max_norm, self.norm)
-        training.lora_adamw(self._plan, self.lr, self.step_count, self.betas[0], self.betas[1], self.eps,
-                            self.weight_decay, grad_factor=None if self.max_norm is None else self.norm[1:])
+        for behind, plan in self._groups:
+            training.lora_adamw(plan, self.lr, self.step_count - behind, self.betas[0], self.betas[1], self.eps,
+                                self.weight_decay, grad_factor=None if self.max_norm is None else self.norm[1:])
+
+    def _lay_out(self, at, grads, missed):
+        """The plans of the parameters `at`: of all of them for the norm, and of those with the
+        same count of steps for the step."""
+        def plan(of):
+            pick = lambda v: None if v is None else [v[at[k]] for k in of]  # noqa: E731
+            made = training.lora_adamw_plan([self.params[at[k]].detach() for k in of], [grads[k] for k in of],
+                                            pick(self.exp_avg), pick(self.exp_avg_sq), masters=pick(self.masters),
+                                            exp_avg_scales=pick(self.exp_avg_scale),
+                                            exp_avg_sq_scales=pick(self.exp_avg_sq_scale),
+                                            stochastic=self.exp_avg_scale is not None)
+            made.tensors = None              # gradients are not kept alive beyond the step that uses them
+            return made
+
+        counts = sorted(set(missed)) if missed else [0]
+        everything = range(len(at))
+        self._plan = plan(everything) if len(counts) == 1 or self.max_norm is not None else None
+        self._groups = [(counts[0], self._plan)] if len(counts) == 1 else \
+            [(c, plan([k for k in everything if missed[k] == c])) for c in counts]
