@@ -413,7 +413,9 @@ class AdamW:
 
     @torch.no_grad()
     def load_state_dict(self, state):
-        """Takes over what state_dict() of an optimizer with the same parameters and options gave."""
+        """Takes over what state_dict() of an optimizer with the same parameters and options gave.
+        8-bit codes have to lie in memory as the parameter does: a scale belongs to 256 of them
+        in that order."""
         mine = self._states()
         if set(state) != set(mine) | {"step"} or any(len(state[k]) != len(v) for k, v in mine.items()) or \
                 isinstance(state["step"], (list, tuple)) and len(state["step"]) != len(self.params):
@@ -422,6 +424,9 @@ class AdamW:
             for t, u in zip(v, state[k]):
                 if t.shape != u.shape or t.dtype != u.dtype:
                     raise ValueError(f"{k} is of another shape or type")
+                if t.dtype == torch.float8_e4m3fn and any(a != b for n, a, b in zip(t.shape, t.stride(), u.stride())
+                                                          if n > 1):
+                    raise ValueError(f"{k} holds 8-bit codes of another memory layout")
         for k, v in mine.items():
             for t, u in zip(v, state[k]):
                 t.copy_(u)
