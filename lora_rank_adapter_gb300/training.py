@@ -270,6 +270,8 @@ def _expect(ok, what):
 
 def _dense(t):
     """Whether the elements fill one stretch of memory in some order of the axes."""
+    if t.numel() == 0:
+        return True
     want = 1
     for size, stride in sorted(zip(t.shape, t.stride()), key=lambda x: (x[1], x[0])):
         if size == 1:

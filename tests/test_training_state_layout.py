@@ -1,4 +1,6 @@
 """What the optimizer takes over, by memory layout (on the CPU)."""
+from types import SimpleNamespace
+
 import pytest
 import torch
 
@@ -48,3 +50,25 @@ def test_32_bit_states_and_masters_are_taken_by_element():
     target = _optimizer(torch.zeros(40, 24), masters=True)
     target.load_state_dict(saved)
     assert _same(target.state_dict(), saved)
+
+
+def test_tensors_without_elements_are_dense():
+    for t in (torch.zeros(5, 0), torch.zeros(0, 5), torch.zeros(0, 5).t(), torch.zeros(0), torch.zeros(3, 0, 2),
+              torch.zeros(4, 6)[:, :0], torch.zeros(4, 6)[::2, 3:3]):
+        assert training._dense(t), (t.shape, t.stride())
+    assert not training._dense(torch.zeros(4, 6)[:, :5]) and training._dense(torch.zeros(()))
+
+
+@pytest.mark.gpu
+def test_a_plan_skips_tensors_without_elements():
+    dev = "cuda:0"
+    torch.cuda.set_device(0)
+    shapes = [(5, 0), (7, 3), (0, 4)]
+    make = lambda: [torch.ones(s, device=dev) for s in shapes]  # noqa: E731
+    s = SimpleNamespace(p=make(), g=make(), m=make(), v=make())
+    plan = training.lora_adamw_plan(s.p, s.g, s.m, s.v)
+    norm = torch.empty(2, device=dev)
+    training.lora_grad_norm(plan, 1.0, norm)
+    assert abs(float(norm[0]) - 21 ** 0.5) < 1e-5
+    training.lora_adamw(plan, lr=0.1, step=1)
+    assert bool((s.p[1] != 1).all())
