@@ -168,7 +168,9 @@ def train_workspace(op, n, m=0, device="cuda", stream=None):
 def _workspace(ws, op, n, m, device, stream):
     if ws is None:
         ws = train_workspace(op, n, m, device, stream)
-    return ws, (0 if ws is None else ws.data_ptr()), (0 if ws is None else ws.numel())
+    elif ws.get_device() != device or not ws.is_contiguous():
+        raise ValueError(f"ws has to be one stretch of memory on cuda:{device}, not {ws.device}, strides {ws.stride()}")
+    return ws, (0 if ws is None else ws.data_ptr()), (0 if ws is None else ws.numel() * ws.element_size())
 
 
 # ----------------------------------------------------------------------------- log-probabilities and losses
