@@ -259,10 +259,20 @@ class AdamWPlan:
     the tensors; build it again when one of them is replaced.  Its calls belong on one
     stream, or one after the other."""
 
-    def __init__(self, struct, table, tensors):
+    def __init__(self, struct, table, tensors, stream):
         self.struct, self.table, self.tensors = struct, table, tensors
         self.ref = ctypes.byref(struct)
         self.device, self.chunks = table.get_device(), int(struct.chunks)
+        self.streams = {stream}              # the addresses of those that the table's memory waits for
+
+    def used_on(self, stream):
+        """The address of the stream of a call (None: the current one).  The table's memory is
+        not handed out again before the work on that stream is done, whichever stream it is."""
+        raw = _raw_stream(stream, self.device)
+        if raw not in self.streams:
+            self.table.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+            self.streams.add(raw)
+        return raw
 
 
 def _expect(ok, what):
@@ -330,16 +340,16 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
     size = lib().lora_adamw_table_size(table_in, n)
     table = _bytes(size, device, stream)
     struct = AdamWPlanStruct()
+    raw = _raw_stream(stream, device.index)
     _call("lora_adamw_build", device.index, table_in, n, _dtype(params[0]) if n else binding.LORA_F32,
-          _dtype(grads[0]) if n else binding.LORA_F32, flags, table.data_ptr(), table.numel(), ctypes.byref(struct),
-          _raw_stream(stream, device.index))
-    return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}))
+          _dtype(grads[0]) if n else binding.LORA_F32, flags, table.data_ptr(), table.numel(), ctypes.byref(struct), raw)
+    return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}), raw)
 
 
 def lora_grad_norm(plan, max_norm, out, stream=None):
     """out[0] = the 2-norm of all gradients, out[1] = min(1, max_norm / (norm + 1e-6)) (fp32 [2])."""
     _call("lora_grad_norm", plan.device, plan.ref, max_norm, _vector(out, 2, torch.float32, "out", plan.device),
-          _raw_stream(stream, plan.device))
+          plan.used_on(stream))
     return out
 
 
@@ -348,4 +358,4 @@ def lora_adamw(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     device scalar that the gradients are multiplied by (lora_grad_norm's out[1:])."""
     hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
     _call("lora_adamw", plan.device, plan.ref, ctypes.byref(hyper),
-          _optional(grad_factor, 1, torch.float32, "grad_factor", plan.device), _raw_stream(stream, plan.device))
+          _optional(grad_factor, 1, torch.float32, "grad_factor", plan.device), plan.used_on(stream))

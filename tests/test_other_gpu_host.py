@@ -27,6 +27,9 @@ class Far:
     def data_ptr(self):
         return 0x10000
 
+    def record_stream(self, stream):
+        pass
+
 
 class Stream:
     def __init__(self, device):
@@ -65,6 +68,7 @@ def gpus(monkeypatch):
         monkeypatch.setattr(module, "lib", lambda: Library())
     monkeypatch.setattr(training, "_bytes", lambda size, device, stream: Far(size, dtype=torch.uint8))
     monkeypatch.setattr(training, "_workspace_size", lambda *a: 4096)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(d))
     monkeypatch.setattr(binding, "workspace", lambda *a, **k: Far(4096, dtype=torch.uint8))
     return state, calls
 
