@@ -373,7 +373,7 @@ class AdamW:
 
     def __init__(self, params, lr=1e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, masters=False,
                  max_norm=None):
-        self.params = [p for p in params]
+        self.params = tuple(params)
         if state_bits not in (8, 32):
             raise ValueError("state_bits has to be 8 or 32")
         self.lr, self.betas, self.eps, self.weight_decay, self.max_norm = lr, betas, eps, weight_decay, max_norm
@@ -383,13 +383,14 @@ class AdamW:
         self.norm = torch.zeros(2, device=self.params[0].device) if max_norm is not None and self.params else None
         zeros = lambda p, dt: torch.zeros_like(p, dtype=dt, requires_grad=False)  # noqa: E731
         dt = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
-        self.exp_avg = [zeros(p, dt) for p in self.params]
-        self.exp_avg_sq = [zeros(p, dt) for p in self.params]
-        scales = lambda: [torch.zeros(-(-p.numel() // training.ADAMW_BLOCK), device=p.device)  # noqa: E731
-                          for p in self.params]
+        # the plans hold these tensors' addresses: tuples, since none of them may be replaced
+        self.exp_avg = tuple(zeros(p, dt) for p in self.params)
+        self.exp_avg_sq = tuple(zeros(p, dt) for p in self.params)
+        scales = lambda: tuple(torch.zeros(-(-p.numel() // training.ADAMW_BLOCK), device=p.device)  # noqa: E731
+                               for p in self.params)
         self.exp_avg_scale = scales() if state_bits == 8 else None
         self.exp_avg_sq_scale = scales() if state_bits == 8 else None
-        self.masters = [p.detach().float().clone(memory_format=torch.preserve_format) for p in self.params] \
+        self.masters = tuple(p.detach().float().clone(memory_format=torch.preserve_format) for p in self.params) \
             if masters else None
 
     def zero_grad(self):

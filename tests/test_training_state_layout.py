@@ -52,6 +52,15 @@ def test_32_bit_states_and_masters_are_taken_by_element():
     assert _same(target.state_dict(), saved)
 
 
+def test_states_are_not_replaced_under_the_plan():
+    """A plan holds addresses: a tensor put in a state's place would leave the step writing to the
+    memory of the one that is gone."""
+    opt = _optimizer(torch.zeros(4, 4), state_bits=8, masters=True)
+    for name in ("params", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "masters"):
+        with pytest.raises(TypeError):
+            getattr(opt, name)[0] = torch.zeros(4, 4)
+
+
 def test_tensors_without_elements_are_dense():
     for t in (torch.zeros(5, 0), torch.zeros(0, 5), torch.zeros(0, 5).t(), torch.zeros(0), torch.zeros(3, 0, 2),
               torch.zeros(4, 6)[:, :0], torch.zeros(4, 6)[::2, 3:3]):
