@@ -177,7 +177,9 @@ lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const v
   LORA_TRY(check_ptr(advantages, T, 4));
   LORA_TRY(check_ptr(token_logps, T, 4));
   LORA_TRY(check_ptr(metrics, 1, 4));
-  if (T > 0 && (token_logps == old_logps || token_logps == ref_logps)) return LORA_ERR_INVALID_ARG;
+  // the metrics take these values once more, after the log-probabilities have been written
+  for (const float *in : {old_logps, ref_logps, advantages, weights})
+    if (T > 0 && token_logps == in) return LORA_ERR_INVALID_ARG;
   LORA_TRY(check_ws(ws, ws_bytes, policy_ws_bytes(T, V * (dtype == LORA_BF16 ? 2 : 4), dlogits != nullptr)));
   PolicyArgs p;
   p.old_logps = old_logps; p.ref_logps = ref_logps; p.advantages = advantages; p.weights = weights;
