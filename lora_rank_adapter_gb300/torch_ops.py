@@ -277,8 +277,8 @@ class TokenLogpsFn(torch.autograd.Function):
 
 
 def _anchor(logits):
-    """A tensor of no elements with the logits' history, or None where they have none: it keeps
-    the way back to them open and not their memory."""
+    """A tensor of no elements with the logits' history: it keeps the way back to them open and
+    not their memory.  None where no gradient is wanted."""
     return logits[:0].clone() if logits.requires_grad and torch.is_grad_enabled() else None
 
 
@@ -309,9 +309,9 @@ def _hand_on(ctx, dloss):
 class PreferenceLossFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, anchor, *args):
-        loss, pair, seq, tok, d = preference_loss_op(logits, *args, ctx.needs_input_grad[0])
+        loss, pair, seq, tok, d = preference_loss_op(logits, *args, anchor is not None)
         ctx.save_for_backward(anchor)
-        ctx.dlogits = d if ctx.needs_input_grad[0] else None
+        ctx.dlogits = d if anchor is not None else None
         ctx.mark_non_differentiable(pair, seq, tok)
         return loss, pair, seq, tok
 
@@ -323,9 +323,9 @@ class PreferenceLossFn(torch.autograd.Function):
 class PolicyLossFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, anchor, *args):
-        metrics, tok, d = policy_loss_op(logits, *args, ctx.needs_input_grad[0])
+        metrics, tok, d = policy_loss_op(logits, *args, anchor is not None)
         ctx.save_for_backward(anchor)
-        ctx.dlogits = d if ctx.needs_input_grad[0] else None
+        ctx.dlogits = d if anchor is not None else None
         loss = metrics[0].clone()
         ctx.mark_non_differentiable(metrics, tok)
         return loss, metrics, tok

@@ -51,6 +51,26 @@ def test_second_derivatives_raise(which, monkeypatch):
     _check(_losses("cpu")[which], "cpu")
 
 
+@pytest.mark.parametrize("which", ["preference", "policy"])
+def test_no_gradient_is_made_where_none_is_wanted(which, monkeypatch):
+    """Under no_grad, logits that require a gradient themselves take no second pass and no memory."""
+    wanted = []
+
+    def op(logits, *args):
+        wanted.append(args[-1])
+        empty = torch.zeros(3)
+        return [torch.zeros(()), empty, empty, empty, empty] if which == "preference" else [empty, empty, empty]
+
+    monkeypatch.setattr(torch_ops, which + "_loss_op", op)
+    x = torch.zeros(6, 7, requires_grad=True)
+    loss = _losses("cpu")[which]
+    with torch.no_grad():
+        loss(x)
+    loss(x.detach())
+    loss(x)
+    assert wanted == [False, False, True]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("which", ["preference", "policy", "logps", "linear"])
 def test_second_derivatives_raise_on_the_gpu(which):
