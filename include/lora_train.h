@@ -28,7 +28,8 @@
  * one; a NaN, a plus infinity or a row of nothing but minus infinity gives NaN
  * in that row, as the formula does.
  *
- * `temperature` (finite, > 0) divides the logits: z = logits / temperature.
+ * `temperature` (finite, > 0, log2(e) / temperature finite in fp32) divides the
+ * logits: z = logits / temperature.
  * `dlogits`, where an operator takes it, is written whole (every row, V
  * columns); it is either `logits` itself (same pointer, same stride: the
  * gradient replaces the logits) or shares no element with them.

@@ -35,7 +35,9 @@ lora_status_t check_rows(lora_dtype_t dtype, int64_t T, int64_t V, const void *l
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_UNSUPPORTED;
   if (!size_ok(T) || !size_ok(V)) return LORA_ERR_INVALID_ARG;
   if (V > kMaxVocab) return LORA_ERR_UNSUPPORTED;
-  if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature)) return LORA_ERR_INVALID_ARG;
+  // the kernels scale by log2(e) / temperature
+  if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature * 1.4426950408889634f))
+    return LORA_ERR_INVALID_ARG;
   const int e = dtype == LORA_BF16 ? 2 : 4;
   if (T > 0 && V > 0) {
     if (ldl < V) return LORA_ERR_INVALID_ARG;
