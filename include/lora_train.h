@@ -141,6 +141,7 @@ LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_
  * run over all tensors in one launch each.  The caller rebuilds the table when an
  * address changes, keeps the tensors alive while it is in use, and lets calls on
  * one table run one after the other (the table holds the norm's partial sums).
+ * Tensors share no memory with each other: their chunks are worked on at once.
  *
  * Element i of tensor k, all in 32-bit arithmetic (g is read in its own type):
  *     g' = g * *grad_factor

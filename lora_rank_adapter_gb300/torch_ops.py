@@ -374,6 +374,8 @@ class AdamW:
     def __init__(self, params, lr=1e-4, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, state_bits=32, masters=False,
                  max_norm=None):
         self.params = tuple(params)
+        if len({id(p) for p in self.params}) != len(self.params):
+            raise ValueError("a parameter is given twice: both of its updates would be under way at once")
         if state_bits not in (8, 32):
             raise ValueError("state_bits has to be 8 or 32")
         self.lr, self.betas, self.eps, self.weight_decay, self.max_norm = lr, betas, eps, weight_decay, max_norm

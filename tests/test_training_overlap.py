@@ -4,7 +4,7 @@ import ctypes
 import pytest
 import torch
 
-from lora_rank_adapter_gb300 import _build, training
+from lora_rank_adapter_gb300 import _build, torch_ops, training
 
 INVALID, WORKSPACE = 1, 4
 A, B, C = (ctypes.c_void_p(v) for v in (0x10000, 0x20000, 0x30000))
@@ -25,3 +25,10 @@ def test_token_logps_over_an_input_are_refused(which):
 
     assert call(B) == WORKSPACE
     assert call(B, **{which: B}) == INVALID
+
+
+def test_a_parameter_given_twice_is_refused():
+    a, b = torch.zeros(4, requires_grad=True), torch.zeros(4, requires_grad=True)
+    with pytest.raises(ValueError, match="twice"):
+        torch_ops.AdamW([a, b, a])
+    assert len(torch_ops.AdamW(p for p in (a, b)).params) == 2
