@@ -548,7 +548,7 @@ struct PolicyTerm {
 __device__ __forceinline__ PolicyTerm policy_term(const PolicyArgs &p, const PolicyRow &in, float logp) {
   const float A = in.A, w = in.w;
   // on the policy itself r is 1, also for a label that is masked out (a NaN stays one)
-  const float r = p.old_logps ? expf(logp - in.old) : logp == kNegInf ? 1.f : expf(logp - logp);
+  const float r = expf(p.old_logps ? logp - in.old : logp == kNegInf ? 0.f : logp - logp);
   const float hi = 1.f + p.clip_high, lo = 1.f - p.clip_low;
   const bool clipped = (A > 0.f && r > hi) || (A < 0.f && r < lo);
   float pg = -A * r, coef = -A * r;
