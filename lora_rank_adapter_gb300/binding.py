@@ -8,6 +8,7 @@ All arithmetic runs in the library's CUDA kernels.  There is no fallback: if
 liblora.so has not been built, or a call fails, an exception is raised.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -116,11 +117,16 @@ def _raw_stream(stream, device):
     return stream.cuda_stream
 
 
-def _elsewhere(device, fn, args):
-    """fn(*args) while GPU `device` is the current one: what the library launches and asks of
-    the driver goes by the current GPU (a default stream has the handle 0 on every GPU)."""
+def _elsewhere(device, fn, *args):
     with torch.cuda.device(device):
         return fn(*args)
+
+
+def _entry(fn, device):
+    """The entry point fn, to be called while GPU `device` is the current one: what the library
+    launches and asks of the driver goes by the current GPU (a default stream has the handle 0
+    on every GPU)."""
+    return fn if device == torch._C._cuda_getDevice() else functools.partial(_elsewhere, device, fn)
 
 
 def _call(name, t, stream, *args):
@@ -128,13 +134,7 @@ def _call(name, t, stream, *args):
     device = t.get_device()
     if device < 0:
         raise ValueError(f"{name}: the tensors have to be on a GPU")
-    fn = getattr(lib(), name)
-    args += (_raw_stream(stream, device),)
-    if device == torch._C._cuda_getDevice():
-        st = fn(*args)
-    else:
-        st = _elsewhere(device, fn, args)
-    _check(st, name)
+    _check(_entry(getattr(lib(), name), device)(*args, _raw_stream(stream, device)), name)
 
 
 def _ptr(t):

@@ -23,7 +23,7 @@ import functools
 import torch
 
 from . import binding
-from .binding import _check, _dtype, _elsewhere, _raw_stream
+from .binding import _check, _dtype, _entry, _raw_stream
 
 TRAIN_EXPORTS = ["lora_train_workspace_size", "lora_token_logps", "lora_token_logps_backward",
                  "lora_preference_loss", "lora_policy_loss", "lora_scale_gradient", "lora_adamw_table_size",
@@ -134,16 +134,6 @@ def _gradient(dlogits, logits):
     return _matrix(dlogits, "dlogits")[2:]
 
 
-def _call(name, device, *args):
-    """The C entry point `name` on GPU `device` (its number), whichever GPU is current."""
-    fn = getattr(lib(), name)
-    if device == torch._C._cuda_getDevice():
-        st = fn(*args)
-    else:
-        st = _elsewhere(device, fn, args)
-    _check(st, name)
-
-
 @functools.lru_cache(maxsize=1024)
 def _workspace_size(op, n, m):
     return lib().lora_train_workspace_size(op, n, m)
@@ -179,8 +169,10 @@ def lora_token_logps(logits, labels, logps, temperature=1.0, stats=None, stream=
     label is outside [0, V)).  stats: fp32 [T, 2] for lora_token_logps_backward."""
     T, V, x, ld, lab, dev = _rows(logits, labels)
     f32 = torch.float32
-    _call("lora_token_logps", dev, _dtype(logits), T, V, x, ld, lab, temperature,
-          _vector(logps, T, f32, "logps", dev), _optional(stats, 2 * T, f32, "stats", dev), _raw_stream(stream, dev))
+    entry = _entry(lib().lora_token_logps, dev)
+    st = entry(_dtype(logits), T, V, x, ld, lab, temperature, _vector(logps, T, f32, "logps", dev),
+               _optional(stats, 2 * T, f32, "stats", dev), _raw_stream(stream, dev))
+    _check(st, "lora_token_logps")
     return logps
 
 
@@ -192,9 +184,10 @@ def lora_token_logps_backward(logits, labels, stats, dlogps, dlogits, temperatur
     if dlogits is None:
         raise ValueError("dlogits are missing")
     d, ldd = _gradient(dlogits, logits)
-    _call("lora_token_logps_backward", dev, _dtype(logits), T, V, x, ld, lab, temperature,
-          _vector(stats, 2 * T, f32, "stats", dev), _vector(dlogps, T, f32, "dlogps", dev), d, ldd,
-          _raw_stream(stream, dev))
+    entry = _entry(lib().lora_token_logps_backward, dev)
+    st = entry(_dtype(logits), T, V, x, ld, lab, temperature, _vector(stats, 2 * T, f32, "stats", dev),
+               _vector(dlogps, T, f32, "dlogps", dev), d, ldd, _raw_stream(stream, dev))
+    _check(st, "lora_token_logps_backward")
     return dlogits
 
 
@@ -214,12 +207,14 @@ def lora_preference_loss(logits, labels, cu_seqlens, ref_logps, beta, token_logp
     P = n // 2
     d, ldd = _gradient(dlogits, logits)
     ws, w, wn = _workspace(ws, TRAIN_PREFERENCE_LOSS, T, P, dev, stream)
-    _call("lora_preference_loss", dev, _dtype(logits), T, V, P, x, ld, lab,
-          _vector(cu_seqlens, n, torch.int32, "cu_seqlens", dev), _optional(ref_logps, 2 * P, f32, "ref_logps", dev),
-          PREFERENCE_KINDS[kind], beta, label_smoothing, PREF_LENGTH_NORMALIZE if length_normalize else 0,
-          temperature, _vector(token_logps, T, f32, "token_logps", dev),
-          _vector(seq_logps, 2 * P, f32, "seq_logps", dev), _vector(pair_loss, P, f32, "pair_loss", dev),
-          _vector(loss, 1, f32, "loss", dev), d, ldd, grad_scale, w, wn, _raw_stream(stream, dev))
+    entry = _entry(lib().lora_preference_loss, dev)
+    st = entry(_dtype(logits), T, V, P, x, ld, lab, _vector(cu_seqlens, n, torch.int32, "cu_seqlens", dev),
+               _optional(ref_logps, 2 * P, f32, "ref_logps", dev), PREFERENCE_KINDS[kind], beta, label_smoothing,
+               PREF_LENGTH_NORMALIZE if length_normalize else 0, temperature,
+               _vector(token_logps, T, f32, "token_logps", dev), _vector(seq_logps, 2 * P, f32, "seq_logps", dev),
+               _vector(pair_loss, P, f32, "pair_loss", dev), _vector(loss, 1, f32, "loss", dev), d, ldd, grad_scale,
+               w, wn, _raw_stream(stream, dev))
+    _check(st, "lora_preference_loss")
     return loss
 
 
@@ -236,11 +231,13 @@ def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps
         w = wn = 0
     else:
         ws, w, wn = _workspace(ws, TRAIN_POLICY_LOSS, T, V * logits.element_size(), dev, stream)
-    _call("lora_policy_loss", dev, _dtype(logits), T, V, x, ld, lab, _optional(old_logps, T, f32, "old_logps", dev),
-          _optional(ref_logps, T, f32, "ref_logps", dev), _vector(advantages, T, f32, "advantages", dev),
-          _optional(weights, T, f32, "weights", dev), clip_low, clip_high, kl_beta, temperature,
-          _vector(token_logps, T, f32, "token_logps", dev), _vector(metrics, 3, f32, "metrics", dev), d, ldd,
-          grad_scale, w, wn, _raw_stream(stream, dev))
+    entry = _entry(lib().lora_policy_loss, dev)
+    st = entry(_dtype(logits), T, V, x, ld, lab, _optional(old_logps, T, f32, "old_logps", dev),
+               _optional(ref_logps, T, f32, "ref_logps", dev), _vector(advantages, T, f32, "advantages", dev),
+               _optional(weights, T, f32, "weights", dev), clip_low, clip_high, kl_beta, temperature,
+               _vector(token_logps, T, f32, "token_logps", dev), _vector(metrics, 3, f32, "metrics", dev), d, ldd,
+               grad_scale, w, wn, _raw_stream(stream, dev))
+    _check(st, "lora_policy_loss")
     return metrics
 
 
@@ -248,8 +245,9 @@ def lora_scale_gradient(x, factor, stream=None):
     """x *= factor (fp32 device scalar) in place for a [T, V] gradient; no pass over x when it is 1."""
     T, V, p, ld = _matrix(x, "gradients")
     dev = x.get_device()
-    _call("lora_scale_gradient", dev, _dtype(x), T, V, p, ld, _vector(factor, 1, torch.float32, "factor", dev),
-          _raw_stream(stream, dev))
+    entry = _entry(lib().lora_scale_gradient, dev)
+    st = entry(_dtype(x), T, V, p, ld, _vector(factor, 1, torch.float32, "factor", dev), _raw_stream(stream, dev))
+    _check(st, "lora_scale_gradient")
     return x
 
 
@@ -268,7 +266,7 @@ class AdamWPlan:
     def used_on(self, stream):
         """The address of the stream of a call (None: the current one).  The table's memory is
         not handed out again before the work on that stream is done, whichever stream it is."""
-        raw = _raw_stream(stream, self.device)
+        raw = torch._C._cuda_getCurrentRawStream(self.device) if stream is None else _raw_stream(stream, self.device)
         if raw not in self.streams:
             self.table.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
             self.streams.add(raw)
@@ -341,15 +339,18 @@ def lora_adamw_plan(params, grads, exp_avg, exp_avg_sq, masters=None, exp_avg_sc
     table = _bytes(size, device, stream)
     struct = AdamWPlanStruct()
     raw = _raw_stream(stream, device.index)
-    _call("lora_adamw_build", device.index, table_in, n, _dtype(params[0]) if n else binding.LORA_F32,
-          _dtype(grads[0]) if n else binding.LORA_F32, flags, table.data_ptr(), table.numel(), ctypes.byref(struct), raw)
+    entry = _entry(lib().lora_adamw_build, device.index)
+    st = entry(table_in, n, _dtype(params[0]) if n else binding.LORA_F32, _dtype(grads[0]) if n else binding.LORA_F32,
+               flags, table.data_ptr(), table.numel(), ctypes.byref(struct), raw)
+    _check(st, "lora_adamw_build")
     return AdamWPlan(struct, table, (list(params), {k: list(v) for k, v in lists.items() if v is not None}), raw)
 
 
 def lora_grad_norm(plan, max_norm, out, stream=None):
     """out[0] = the 2-norm of all gradients, out[1] = min(1, max_norm / (norm + 1e-6)) (fp32 [2])."""
-    _call("lora_grad_norm", plan.device, plan.ref, max_norm, _vector(out, 2, torch.float32, "out", plan.device),
-          plan.used_on(stream))
+    entry = _entry(lib().lora_grad_norm, plan.device)
+    st = entry(plan.ref, max_norm, _vector(out, 2, torch.float32, "out", plan.device), plan.used_on(stream))
+    _check(st, "lora_grad_norm")
     return out
 
 
@@ -357,5 +358,7 @@ def lora_adamw(plan, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     """One AdamW step over the plan's tensors; step counts from 1.  grad_factor: fp32
     device scalar that the gradients are multiplied by (lora_grad_norm's out[1:])."""
     hyper = AdamWHyper(lr, beta1, beta2, eps, weight_decay, step)
-    _call("lora_adamw", plan.device, plan.ref, ctypes.byref(hyper),
-          _optional(grad_factor, 1, torch.float32, "grad_factor", plan.device), plan.used_on(stream))
+    entry = _entry(lib().lora_adamw, plan.device)
+    st = entry(plan.ref, ctypes.byref(hyper), _optional(grad_factor, 1, torch.float32, "grad_factor", plan.device),
+               plan.used_on(stream))
+    _check(st, "lora_adamw")

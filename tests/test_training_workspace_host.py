@@ -35,6 +35,12 @@ def test_a_workspace_off_the_gpu_or_with_gaps_is_refused(gpus, call):  # noqa: F
 
 def test_a_workspace_counts_in_bytes(gpus, monkeypatch):  # noqa: F811
     sizes = []
-    monkeypatch.setattr(training, "_call", lambda name, device, *args: sizes.append(args[-2]))
+
+    class Library:
+        def lora_preference_loss(self, *args):
+            sizes.append(args[-2])
+            return 0
+
+    monkeypatch.setattr(training, "lib", lambda: Library())
     _preference(Far(1000))
     assert sizes == [4000]
