@@ -11,9 +11,10 @@
  *
  * The conventions of lora.h hold: device pointers owned by the caller, scratch
  * passed in as ws (256-byte aligned), strides in elements, work enqueued on
- * `stream` without a host sync, host-checkable errors returned before anything
- * is launched, results independent of the run (no float atomics).  Logits rows
- * need only the alignment of their element type: any row stride, any V.
+ * `stream` (of the current device) without a host sync, host-checkable errors
+ * returned before anything is launched, results independent of the run (no float
+ * atomics).  Logits rows need only the alignment of their element type: any row
+ * stride, any V.
  *
  * The loss operators work on T rows of logits, element (t, v) at
  * logits[t*ldl + v], LORA_BF16 or LORA_F32, 0 <= T < 2^31, 0 <= V <= 2^30
@@ -23,7 +24,7 @@
  * IGNORED row: it contributes nothing, its log-probability and its gradient are
  * zero, and its logits are not read (they may hold anything, NaN included).
  * Softmax statistics and sums are held in 32 bits or more; a gradient stored in
- * bf16 is rounded once, to nearest even.  Logits of minus infinity or of the
+ * bf16 is rounded once, to nearest even (lora_scale_gradient rounds it again).  Logits of minus infinity or of the
  * type's lowest value have probability zero as long as the row has a larger
  * one; a NaN, a plus infinity or a row of nothing but minus infinity gives NaN
  * in that row, as the formula does.
@@ -113,7 +114,7 @@ LORA_API lora_status_t lora_preference_loss(lora_dtype_t dtype, int64_t T, int64
  *   old_logps, ref_logps  device float [T] or NULL;  advantages  device float [T]
  *   weights     device float [T] or NULL for 1: the caller's mean (1 / number of
  *               rows that count, 1 / (sequences * rows of the sequence), ...)
- *   token_logps float [T], not one of the inputs;  metrics float [3]: the loss,
+ *   token_logps float [T], none of the inputs;  metrics float [3]: the loss,
  *               sum weights * kl, and sum of weights over the clipped rows
  *   dlogits     NULL, or grad_scale * d loss / d logits
  *   clip_low in [0, 1], clip_high >= 0, kl_beta >= 0, all finite
@@ -129,7 +130,9 @@ LORA_API lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V
 /* --------------------------------------------------------------------------------
  * lora_scale_gradient:  x[t][v] *= *factor (device float), rounded once.  Returns
  * to the stream at once when *factor is 1: the gradient that a loss operator
- * wrote ahead of time then needs no second pass.
+ * wrote ahead of time then needs no second pass.  Otherwise a bf16 gradient has
+ * been rounded twice (exactly, once, where the factor is a power of two); grad_scale
+ * of the loss operators scales before the one rounding.
  * -------------------------------------------------------------------------------- */
 LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void *x, int64_t ldx,
                            const float *factor, void *stream);
@@ -149,6 +152,8 @@ LORA_API lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_
  *     v  = beta2 v + (1 - beta2) g'^2
  *     p  = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
  * With `master` the update is taken on master[i] (float) and p is its rounding.
+ * The quotient is off by some 2^-22; a divisor below the smallest normal number
+ * (eps = 0 and v = 0) counts as that number, so that 0 / 0 gives 0.
  *
  * States in 32 bits: exp_avg (m) and exp_avg_sq (v) are float [numel].
  * States in 8 bits (LORA_ADAMW_STATE_8BIT): blocks of LORA_ADAMW_BLOCK
@@ -225,7 +230,8 @@ LORA_API lora_status_t lora_adamw_build(const lora_adamw_tensor_t *tensors, int3
 LORA_API lora_status_t lora_grad_norm(const lora_adamw_plan_t *plan, float max_norm, float *out, void *stream);
 
 /* One step.  step >= 1 counts this step; grad_factor: device float [1], or NULL for 1.
- * lr, weight_decay, eps >= 0 and beta1, beta2 in [0, 1), all finite. */
+ * lr, weight_decay, eps >= 0 and beta1, beta2 in [0, 1), all finite.  These are host
+ * values: a step captured in a graph replays the same count, rate and random bits. */
 typedef struct {
     double lr, beta1, beta2, eps, weight_decay;
     int64_t step;

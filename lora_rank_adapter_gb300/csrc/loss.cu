@@ -700,8 +700,8 @@ __global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Ro
 // sends its (m, s) to every block of the cluster, waits for all of them, and
 // works out the row's coefficient by itself.
 //
-// 8699 rows of 128256 bf16, 20 % ignored (1.8 GB read, 2.2 GB written): 630 us,
-// 6.4 TB/s, 94 % of the copy rate; two passes over the row took 860 us.  What it
+// 8699 rows of 128256 bf16, 20 % ignored (1.8 GB read, 2.2 GB written): 632 us,
+// 6.35 TB/s, 93 % of the copy rate; two passes over the row took 860 us.  What it
 // came from: 1026 us with one row for a cluster at a time, 759 us with the ring,
 // and 630 us when the warps' sums went by asynchronous stores instead of arrivals
 // with release semantics, which waited for the last row's gradient to reach
@@ -811,8 +811,8 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
     // And the block does not end before every warp of the cluster has sent its last
     // pair here, also where a wait ran out, or where another stream wrote the labels and
     // warps took different rows for ignored: for as many limits as a warp's own waits
-    // may take.  (632 us for the rows above; 641 with a barrier of the cluster at the
-    // end, 630 where the block just leaves.)
+    // may take.  (At most 1 % of the rows above: 632 us, 641 with a barrier of the
+    // cluster at the end, 630 where the block just leaves.)
     if (C > 1)
       for (int i = 0; i < kSlots + 2 && !mbar_wait<true>(&done, 0); ++i) {}
     return;

@@ -22,8 +22,11 @@ loss operators of `training`, and `AdamW` an optimizer on lora_grad_norm / lora_
     loss.backward(); optimizer.step()
 The losses form their gradient with the forward pass, while a row is at hand; the
 backward pass multiplies it by the incoming gradient in place (no pass over it when
-that is 1) and hands it on, so it can be taken once and has no gradient of its own:
-second derivatives (create_graph) through a loss raise.
+that is 1; a bf16 gradient is rounded once more unless that is a power of two) and
+hands it on, so it can be taken once and has no gradient of its own: second
+derivatives (create_graph) through a loss raise.  That pass is Python, so
+torch.compile runs the two losses outside its graph (fullgraph=True refuses them);
+token_logps is two opaque nodes.
 """
 from typing import List, Optional, Sequence
 
@@ -364,9 +367,9 @@ class AdamW:
     """AdamW over an adapter's tensors (all of one dtype), one launch a step.
 
     state_bits: 32, or 8 for e4m3 states with a scale for each 256 elements, rounded at
-    random (reproducibly) so that they follow their gradients over any number of steps.  masters: keep
-    fp32 copies that the step updates (for bf16 parameters whose updates are smaller than
-    their rounding).  max_norm: clip the gradients' global norm to it; `norm` then holds
+    random (reproducibly) so that they follow their gradients over any number of steps.
+    masters: keep fp32 copies that the step updates (for bf16 parameters whose updates are
+    smaller than their rounding).  max_norm: clip the gradients' global norm to it; `norm` then holds
     (norm, factor) of the last step.  Parameters without a gradient sit a step out: each
     has its own count of steps, which its bias corrections go by (one launch for each
     count there is)."""
