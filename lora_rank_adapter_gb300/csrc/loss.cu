@@ -810,11 +810,12 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldArg
       if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
     // And the block does not end before every warp of the cluster has sent its last
     // pair here, also where a wait ran out, or where another stream wrote the labels and
-    // warps took different rows for ignored: for as many limits as a warp's own waits
-    // may take.  (At most 1 % of the rows above: 632 us, 641 with a barrier of the
+    // warps took different rows for ignored: for as many limits as may lie ahead of a
+    // warp, whose rows in the ring are kSlots at most, of kSlots chunks and an exchange
+    // each.  (At most 1 % of the rows above: 632 us, 641 with a barrier of the
     // cluster at the end, 630 where the block just leaves.)
     if (C > 1)
-      for (int i = 0; i < kSlots + 2 && !mbar_wait<true>(&done, 0); ++i) {}
+      for (int i = 0; i < kSlots * (kSlots + 1) && !mbar_wait<true>(&done, 0); ++i) {}
     return;
   }
 

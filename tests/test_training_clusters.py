@@ -39,6 +39,7 @@ def test_no_block_leaves_its_cluster_early():
     # last, on every path, and the loader keeps its block until all have
     loader, work = _held()
     assert loader.index("mbar_wait<true>(&done, 0)") > loader.index("mbar_wait(&full")
+    assert "i < kSlots * (kSlots + 1) && !mbar_wait<true>(&done, 0)" in loader      # every wait that may lie ahead
     assert not re.search(r"\breturn\b", work)
     assert re.search(r"\n  \}\s*if \(C > 1 && lane < C\) mbar_arrive_remote\(&done, lane\);\s*$", work)
     assert "mbar_init(&done, C * kHeldWarps);" in _body("held_kernel")
