@@ -645,6 +645,8 @@ __global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Ro
     s = both.x + both.y;
     if (edge != kNegInf) absorb_one(m, s, edge, k);
     warp_merge(m, s, k);
+    // past this point the gradient may replace the row: all reads of it come before
+    if (kTeam == 1) __syncwarp();
     if (kTeam > 1) {
       if (lane_id() == 0) sh[tid >> 5] = make_float2(m, s);
       __syncthreads();

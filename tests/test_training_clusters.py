@@ -69,10 +69,14 @@ def test_reads_of_a_row_come_before_the_arrival_that_lets_others_write_it():
     _, work = _held()
     assert re.search(r"if \(C == 1\) \{\s*__syncwarp\(\);\s*if \(lane == 0\)", work)
     assert "lane + (__float_as_uint(picked) & h.zero)" in work
+    short = _body("short_kernel")
+    reads, merge, writes = (short.index(k) for k in ("const float picked", "if (kTeam == 1) __syncwarp();", "g.piece<E>"))
+    assert reads < merge < writes and merge < short.index("__syncthreads();") < writes
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,V,dtype", [(700, 70001, BF16), (2000, 20000, BF16), (900, 40002, F32)])
+@pytest.mark.parametrize("T,V,dtype", [(700, 70001, BF16), (2000, 20000, BF16), (900, 40002, F32),
+                                       (5000, 300, F32), (3000, 4000, BF16), (3000, 15001, BF16)])
 def test_many_rows_a_cluster_in_place(T, V, dtype):
     """Each cluster goes through several rows, some ignored, and the gradient replaces them."""
     torch.cuda.set_device(0)
