@@ -6,6 +6,8 @@
  *   lora_token_logps, lora_token_logps_backward   log-probabilities of the labels, and their gradient
  *   lora_preference_loss                          paired log-ratio loss, and its gradient
  *   lora_policy_loss                              clipped policy loss with a KL term, and its gradient
+ *   lora_top_logps, lora_top_logps_backward       log-probabilities with entropy and the most probable tokens, and their gradient
+ *   lora_distill_loss                             divergence from a teacher's most probable tokens, and its gradient
  *   lora_scale_gradient                           a gradient times a device scalar, in place
  *   lora_adamw_build, lora_grad_norm, lora_adamw  an AdamW step over many tensors at once
  *
@@ -126,6 +128,73 @@ LORA_API lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V
                            const float *advantages, const float *weights, float clip_low, float clip_high,
                            float kl_beta, float temperature, float *token_logps, float *metrics, void *dlogits,
                            int64_t lddl, float grad_scale, void *ws, size_t ws_bytes, void *stream);
+
+/* --------------------------------------------------------------------------------
+ * lora_top_logps: with p = softmax(z), z = logits / temperature, for each row
+ *     logps      ln p_label
+ *     entropy    -sum_v p_v ln p_v
+ *     top_ids    the K most probable tokens, the most probable one first, equally
+ *                probable ones by lowest id;  top_logps  their ln p
+ *     rest_logps ln of the sum of p over all other tokens (summed by itself, so that
+ *                it holds for a sure model too; minus infinity where there is none)
+ * Tokens of logit minus infinity are no alternatives: where fewer than K others are
+ * there, the last entries are -1, of log-probability minus infinity.  A row of NaN
+ * (see above) has -1 and NaN throughout.
+ *   0 <= K <= LORA_TOP_MAX (above: LORA_ERR_UNSUPPORTED)
+ *   labels     int64 [T], or NULL where no label is scored (logps NULL too): every row
+ *              then counts.  An ignored row has logps, entropy and rest_logps 0, top_ids
+ *              -1 and top_logps minus infinity.
+ *   logps      float [T], or NULL;  entropy, rest_logps  float [T], or NULL
+ *   top_ids    int64 [T][K];  top_logps  float [T][K]
+ *   stats      NULL, or float [T][2] for the gradient (as lora_token_logps writes it;
+ *              8-byte aligned)
+ * -------------------------------------------------------------------------------- */
+#define LORA_TOP_MAX 128
+LORA_API lora_status_t lora_top_logps(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits,
+                           int64_t ldl, const int64_t *labels, float temperature, float *logps, float *entropy,
+                           int64_t *top_ids, float *top_logps, float *rest_logps, float *stats, void *stream);
+
+/* --------------------------------------------------------------------------------
+ * lora_top_logps_backward: the gradient through logps, entropy and top_logps,
+ *     dlogits[t][v] = ( (v == label) dlogps + sum over j with top_ids[j] == v of dtop_logps[j]
+ *                       - p_v (dlogps + sum_j dtop_logps[j] + dentropy (ln p_v + entropy)) ) / temperature
+ *   stats      float [T][2], entropy float [T]: as lora_top_logps wrote them for the same
+ *              logits, labels and temperature (entropy NULL if dentropy is)
+ *   dlogps, dentropy  float [T] or NULL for zero (dlogps NULL if labels are);
+ *   dtop_logps float [T][K] or NULL for zero; then top_ids may be NULL.  An entry
+ *              outside [0, V) has no gradient; any distinct or repeated ids will do.
+ * An ignored row, and one whose incoming gradients are all zero, gets zeros and is not read.
+ * -------------------------------------------------------------------------------- */
+LORA_API lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K,
+                           const void *logits, int64_t ldl, const int64_t *labels, const int64_t *top_ids,
+                           float temperature, const float *stats, const float *entropy, const float *dlogps,
+                           const float *dentropy, const float *dtop_logps, void *dlogits, int64_t lddl,
+                           void *stream);
+
+/* --------------------------------------------------------------------------------
+ * lora_distill_loss: how far the rows are from a teacher's record of its most probable
+ * tokens (what lora_top_logps writes for the teacher's logits: another model, or
+ * this one with its adapters off).  With q_j = exp(top_logps[t][j]) and p_j the
+ * softmax of logits / temperature at top_ids[t][j], over the row's listed tokens,
+ *     LORA_DISTILL_FORWARD   row_loss = sum_j q_j (ln q_j - ln p_j)   [+ q_r (ln q_r - ln p_r)]
+ *     LORA_DISTILL_REVERSE   row_loss = sum_j p_j (ln p_j - ln q_j)   [+ p_r (ln p_r - ln q_r)]
+ *     loss = sum_t weights[t] * row_loss[t]
+ * where the terms in brackets, the rest, are taken if rest_logps is given:
+ * q_r = exp(rest_logps[t]), p_r the sum of p over all tokens that are not listed.  Terms of
+ * a zero q (forward) or a zero p (reverse) are zero.
+ *   top_ids    int64 [T][K], 1 <= K <= LORA_TOP_MAX.  An id outside [0, V) is no token (a
+ *              shorter list); one that its row lists again counts where it comes first.
+ *   top_logps  float [T][K];  rest_logps  float [T] or NULL: at the temperature of this call
+ *   weights    float [T] or NULL for 1.  A row of weight 0 or without a listed token is
+ *              IGNORED: its row_loss and its gradient are zero and its logits are not read.
+ *   row_loss   float [T], none of the inputs;  loss  float [1]
+ *   dlogits    NULL, or grad_scale * d loss / d logits
+ * -------------------------------------------------------------------------------- */
+typedef enum { LORA_DISTILL_FORWARD = 0, LORA_DISTILL_REVERSE = 1 } lora_distill_kind_t;
+LORA_API lora_status_t lora_distill_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits,
+                           int64_t ldl, const int64_t *top_ids, const float *top_logps, const float *rest_logps,
+                           const float *weights, lora_distill_kind_t kind, float temperature, float *row_loss,
+                           float *loss, void *dlogits, int64_t lddl, float grad_scale, void *stream);
 
 /* --------------------------------------------------------------------------------
  * lora_scale_gradient:  x[t][v] *= *factor (device float), rounded once.  Returns

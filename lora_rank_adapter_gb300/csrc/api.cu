@@ -12,6 +12,7 @@
 
 #include "host_common.h"
 #include "loss.h"
+#include "top.h"
 #include "multi.h"
 #include "single_common.h"
 #include "single_tc.h"
@@ -460,8 +461,8 @@ lora_status_t lora_gather_shrink(const lora_addressing_t *addr, const int32_t *r
 lora_status_t lora_device_error(int32_t *code) {
   if (code == nullptr) return LORA_ERR_INVALID_ARG;
   int v = 0;
-  int parts[6] = {read_clear_error_single_common(), read_clear_error_single_f32(), read_clear_error_multi(),
-                  read_clear_error_single_tc(), read_clear_error_decode(), read_clear_error_loss()};
+  int parts[7] = {read_clear_error_single_common(), read_clear_error_single_f32(), read_clear_error_multi(),
+                  read_clear_error_single_tc(), read_clear_error_decode(), read_clear_error_loss(), read_clear_error_distill()};
   for (int p : parts) {
     if (p < 0) return LORA_ERR_CUDA;
     v |= p;

@@ -1,0 +1,279 @@
+// rows.cuh -- what the kernels over rows of logits share: 16-byte pieces of bf16 or
+// fp32 elements, running softmax statistics, a row's gradient, zeros, and the
+// cluster's barrier and stores.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+#include "f32x2.cuh"
+
+namespace lora {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -INFINITY;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t ex2_2(uint64_t v) {
+  const float2 f = unpk2(v);
+  return pk2(ex2(f.x), ex2(f.y));
+}
+
+template <typename E>
+struct Elem;
+template <>
+struct Elem<float> {
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ float load(const float *p) { return *p; }
+  static __device__ __forceinline__ void store(float *p, float v) { *p = v; }
+  // a 16-byte piece as kVec / 2 pairs, and its largest value
+  static __device__ __forceinline__ void pairs(const uint4 &q, uint64_t *v) {
+    v[0] = pk2(__uint_as_float(q.x), __uint_as_float(q.y));
+    v[1] = pk2(__uint_as_float(q.z), __uint_as_float(q.w));
+  }
+  static __device__ __forceinline__ uint4 pack_pairs(const uint64_t *v) {
+    const float2 a = unpk2(v[0]), b = unpk2(v[1]);
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+  }
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 (&q)[U]) {
+    float b = kNegInf;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      b = fmaxf(b, fmaxf(fmaxf(__uint_as_float(q[u].x), __uint_as_float(q[u].y)),
+                         fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w))));
+    return b;
+  }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
+  // minus infinity in place i of a piece
+  static __device__ __forceinline__ void strike(uint4 &q, int i) {
+    if (i == 0) q.x = 0xff800000u;
+    if (i == 1) q.y = 0xff800000u;
+    if (i == 2) q.z = 0xff800000u;
+    if (i == 3) q.w = 0xff800000u;
+  }
+  static __device__ __forceinline__ void unpack(const uint4 &q, float *v) {
+    v[0] = __uint_as_float(q.x);
+    v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z);
+    v[3] = __uint_as_float(q.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float *v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void pairs(const uint4 &q, uint64_t *v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = pk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 pack_pairs(const uint64_t *v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpk2(v[i]);
+      w[i] = pack_bf16(f.x, f.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  template <int U>
+  static __device__ __forceinline__ float largest(const uint4 (&q)[U]) {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+    __nv_bfloat162 b = two(0xff80ff80u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      b = __hmax2(b, __hmax2(__hmax2(two(q[u].x), two(q[u].y)), __hmax2(two(q[u].z), two(q[u].w))));
+    const float2 f = __bfloat1622float2(b);
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
+  static __device__ __forceinline__ void strike(uint4 &q, int i) {
+    const uint32_t keep = i & 1 ? 0x0000ffffu : 0xffff0000u, put = 0xff80ff80u & ~keep;
+    if (i >> 1 == 0) q.x = (q.x & keep) | put;
+    if (i >> 1 == 1) q.y = (q.y & keep) | put;
+    if (i >> 1 == 2) q.z = (q.z & keep) | put;
+    if (i >> 1 == 3) q.w = (q.w & keep) | put;
+  }
+  static __device__ __forceinline__ void unpack(const uint4 &q, float *v) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float *v) {
+    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+};
+
+// A row split at 16-byte boundaries: `head` elements before the first, `vecs`
+// whole 16-byte pieces, and the rest.  (V <= 2^30: places within a row are ints.)
+template <typename E>
+struct RowSpan {
+  int head, vecs;
+  __device__ __forceinline__ RowSpan(const E *row, int V) {
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+    head = (int)(((16u - off) & 15u) / sizeof(E));
+    if (head > V) head = V;
+    vecs = (V - head) / Elem<E>::kVec;
+  }
+  __device__ __forceinline__ int tail() const { return head + vecs * Elem<E>::kVec; }
+};
+
+// Running (m, s): the largest value seen and s = sum exp((x - m) * inv_t), with
+// k = inv_t * log2(e).  While m is minus infinity nothing but minus infinity has
+// been seen and s is zero; the reference is then 0 instead of m, so that
+// exp(-inf - ref) is 0 and not NaN.
+__device__ __forceinline__ float ref_of(float m) { return m == kNegInf ? 0.f : m; }
+
+// One element into the running pair.
+__device__ __forceinline__ void absorb_one(float &m, float &s, float v, float k) {
+  const float mm = fmaxf(m, v), r = ref_of(mm);
+  s = s * ex2((m - r) * k) + ex2((v - r) * k);
+  m = mm;
+}
+
+// U 16-byte pieces into a running maximum and a pair of partial sums.  The
+// reference moves once for all of them.
+template <typename E, int U>
+__device__ __forceinline__ void absorb(float &m, uint64_t &s, const uint4 (&q)[U], float k) {
+  const float mm = fmaxf(m, Elem<E>::largest(q)), r = ref_of(mm), f = ex2((m - r) * k);
+  const uint64_t r2 = pk2(-r, -r), k2 = pk2(k, k);
+  m = mm;
+  s = mul2(s, pk2(f, f));
+  uint64_t t = 0;      // a second chain of sums: (0, 0)
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint64_t v[Elem<E>::kVec / 2];
+    Elem<E>::pairs(q[u], v);
+#pragma unroll
+    for (int j = 0; j < Elem<E>::kVec / 2; ++j) {
+      const uint64_t e = ex2_2(mul2(add2(v[j], r2), k2));
+      if (j & 1) t = add2(t, e); else s = add2(s, e);
+    }
+  }
+  s = add2(s, t);
+}
+
+// Pieces [from, to) of a row, kThreads threads, U loads of each in flight.
+template <typename E, int kThreads, int U>
+__device__ __forceinline__ void absorb_span(float &m, uint64_t &s, const uint4 *p, int from, int to, float k) {
+  int i = from + (int)threadIdx.x;
+  for (; to - i > (U - 1) * kThreads; i += U * kThreads) {
+    uint4 q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) q[u] = p[i + u * kThreads];
+    absorb<E, U>(m, s, q, k);
+  }
+  if (U > 1 && i < to) {
+    uint4 q[U > 1 ? U - 1 : 1];
+#pragma unroll
+    for (int u = 0; u < U - 1; ++u) q[u] = to - i > u * kThreads ? p[i + u * kThreads] : Elem<E>::lowest();
+    absorb<E, U - 1>(m, s, q, k);
+  }
+}
+
+// (m, s) of the warp's lanes: the largest m, then one rescaling of each s.
+__device__ __forceinline__ void warp_merge(float &m, float &s, float k) {
+  float mm;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mm) : "f"(m));
+  s *= ex2((m - ref_of(mm)) * k);
+  m = mm;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+}
+
+// (m, s) of the whole block, known to the threads of warp 0.
+template <int kWarps>
+__device__ __forceinline__ void block_merge(float &m, float &s, float k, float2 *sh) {
+  warp_merge(m, s, k);
+  if (lane_id() == 0) sh[threadIdx.x >> 5] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  const float2 v = threadIdx.x < kWarps ? sh[threadIdx.x] : make_float2(kNegInf, 0.f);
+  m = v.x;
+  s = v.y;
+  warp_merge(m, s, k);
+}
+
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_dsmem_f2(const void *local_ptr, uint32_t cta, float2 v) {
+  uint32_t local = smem_u32(local_ptr), remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(cta));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote), "f"(v.x), "f"(v.y) : "memory");
+}
+// A pair stored to another block of the cluster, its bytes completing `bar` there
+// (only in a kernel that was launched as clusters).
+__device__ __forceinline__ void st_async_f2(const void *local_ptr, const uint64_t *local_bar, uint32_t cta, float2 v) {
+  uint32_t p, b;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(smem_u32(local_ptr)), "r"(cta));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(local_bar)), "r"(cta));
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(p),
+               "f"(v.x), "f"(v.y), "r"(b)
+               : "memory");
+}
+
+// Zeros over elements [from, to) of an output row.
+template <typename E, int kThreads>
+__device__ __forceinline__ void zero_span(E *out, int from, int to, int tid) {
+  E *o = out + from;
+  const RowSpan<E> so(o, to - from);
+  if (tid < so.head) Elem<E>::store(o + tid, 0.f);
+  uint4 *body = reinterpret_cast<uint4 *>(o + so.head);
+  for (int i = tid; i < so.vecs; i += kThreads) __stcs(body + i, make_uint4(0, 0, 0, 0));
+  if (tid < to - from - so.tail()) Elem<E>::store(o + so.tail() + tid, 0.f);
+}
+
+// A row's gradient d_v = c [v == label] + f exp(z_v - m), f = -c / S.
+struct RowGrad {
+  float m, k, c, f;
+  __device__ __forceinline__ float operator()(float v) const { return f * ex2((v - m) * k); }
+  // a 16-byte piece, as if it did not hold the label
+  template <typename E>
+  __device__ __forceinline__ uint4 piece(const uint4 &q) const {
+    constexpr int N = Elem<E>::kVec;
+    uint64_t v[N / 2];
+    Elem<E>::pairs(q, v);
+    const uint64_t m2 = pk2(-m, -m), k2 = pk2(k, k), f2 = pk2(f, f);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) v[j] = mul2(ex2_2(mul2(add2(v[j], m2), k2)), f2);
+    return Elem<E>::pack_pairs(v);
+  }
+};
+
+// Elements [e0, e1) of the output row where it sits at another offset to a
+// 16-byte boundary than the logits: 4-byte words of the output, their elements
+// read one by one (src: element i of the row at src[i]).
+template <typename E, int kThreads, typename G>
+__device__ __forceinline__ void grad_words(E *out, const E *src, int e0, int e1, int label, const G &g) {
+  auto one = [&](int i) { return g(Elem<E>::load(src + i)) + (i == label ? g.c : 0.f); };
+  const int tid = threadIdx.x;
+  if (sizeof(E) == 4) {
+#pragma unroll 4
+    for (int i = e0 + tid; i < e1; i += kThreads) Elem<E>::store(out + i, one(i));
+  } else {
+    const int w0 = e0 + (int)((reinterpret_cast<uintptr_t>(out + e0) >> 1) & 1);      // the first whole word
+    const int words = e1 > w0 ? (e1 - w0) / 2 : 0;
+#pragma unroll 4
+    for (int i = tid; i < words; i += kThreads)
+      __stcs(reinterpret_cast<unsigned *>(out + w0) + i, pack_bf16(one(w0 + 2 * i), one(w0 + 2 * i + 1)));
+    if (tid == 0 && w0 > e0 && e0 < e1) Elem<E>::store(out + e0, one(e0));
+    if (tid == 1 && w0 + 2 * words < e1) Elem<E>::store(out + e1 - 1, one(e1 - 1));
+  }
+}
+
+}  // namespace lora

@@ -1,0 +1,683 @@
+// top.cu -- log-probabilities of given tokens with the row's entropy, its most
+// probable tokens and the mass that they leave, and the gradient through them
+// (include/lora_train.h).
+//
+// Mathematics.  With u = (x - m) / temperature, m the row's largest logit, e = exp(u)
+// and S = sum e: ln p = u - ln S, the entropy H = -sum p ln p = ln S - (sum e u) / S,
+// and with incoming gradients g (of the label and of the listed tokens, their sum
+// G) and h (of H)
+//     d_v = (1 / temperature) (sum of the g of token v - p_v (G + h (ln p_v + H))).
+// Sums run over u in units of log 2, as the exponential does.
+//
+// Bytes decide: one exponential and some ten operations an element.  A row is read
+// once, its K largest found on the way (top_kernel); the gradient reads it once more.
+#include <math.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "f32x2.cuh"
+#include "host_common.h"
+#include "rows.cuh"
+#include "top.h"
+
+namespace lora {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+// exp2 of it is zero; it stands in for minus infinity where that would meet a zero.
+constexpr float kLeast = -200.f;
+constexpr int kMaxTop = LORA_TOP_MAX;
+
+// ----------------------------------------------------------------------------- order
+// Values in an order of unsigned integers (both zeros alike), and back.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o ^ (o & 0x80000000u ? 0x80000000u : 0xffffffffu));
+}
+// A token's place in the order of the alternatives: by value, then by lowest id.  No
+// token has the key 0.
+__device__ __forceinline__ uint64_t key_of(float v, int id) {
+  return (uint64_t)order_of(v) << 32 | (0xffffffffu - (uint32_t)id);
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return value_of((uint32_t)(key >> 32)); }
+__device__ __forceinline__ int key_id(uint64_t key) { return (int)(0xffffffffu - (uint32_t)key); }
+constexpr float kLowest = -3.402823466e38f;      // what is below is minus infinity: no alternative
+
+// ----------------------------------------------------------------------------- statistics
+// Running largest value m, s = sum e and w = sum e u over what was seen, e = 2^u,
+// u = (x - m) k.
+struct Sums {
+  float m, s, w;
+  __device__ __forceinline__ void move(float mm, float k) {
+    const float d = (m - ref_of(mm)) * k, f = ex2(d);
+    w = (w + fmaxf(d, kLeast) * s) * f;
+    s *= f;
+    m = mm;
+  }
+  __device__ __forceinline__ void add(float v, float k) {
+    const float mm = fmaxf(m, v);
+    move(mm, k);
+    const float u = (v - ref_of(mm)) * k, e = ex2(u);      // a NaN goes into s
+    s += e;
+    w += e * fmaxf(u, kLeast);
+  }
+  __device__ __forceinline__ void add(Sums o, float k) {
+    const float mm = fmaxf(m, o.m);
+    move(mm, k);
+    o.move(mm, k);
+    s += o.s;
+    w += o.w;
+  }
+};
+
+__device__ __forceinline__ Sums no_sums() { return {kNegInf, 0.f, 0.f}; }
+
+// The same with pairs of partial sums, U 16-byte pieces at once; `top`: the largest of them.
+template <typename E>
+struct PairSums {
+  float m = kNegInf;
+  uint64_t s = 0, w = 0;
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 (&q)[U], float top, float k) {
+    const float mm = fmaxf(m, top), r = ref_of(mm), d = (m - r) * k, f = ex2(d), dd = fmaxf(d, kLeast);
+    const uint64_t r2 = pk2(-r, -r), k2 = pk2(k, k), f2 = pk2(f, f);
+    m = mm;
+    w = mul2(fma2(s, pk2(dd, dd), w), f2);
+    s = mul2(s, f2);
+    uint64_t t = 0, y = 0;      // second chains
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint64_t v[Elem<E>::kVec / 2];
+      Elem<E>::pairs(q[u], v);
+#pragma unroll
+      for (int j = 0; j < Elem<E>::kVec / 2; ++j) {
+        const uint64_t x = mul2(add2(v[j], r2), k2), e = ex2_2(x);
+        const float2 xf = unpk2(x);
+        const uint64_t c = pk2(fmaxf(xf.x, kLeast), fmaxf(xf.y, kLeast));
+        if (j & 1) {
+          t = add2(t, e);
+          y = fma2(e, c, y);
+        } else {
+          s = add2(s, e);
+          w = fma2(e, c, w);
+        }
+      }
+    }
+    s = add2(s, t);
+    w = add2(w, y);
+  }
+  __device__ __forceinline__ Sums sums() const {
+    const float2 a = unpk2(s), b = unpk2(w);
+    Sums r;
+    r.m = m;
+    r.s = a.x + a.y;
+    r.w = b.x + b.y;
+    return r;
+  }
+};
+
+__device__ __forceinline__ void warp_merge(Sums &x, float k) {
+  float mm;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mm) : "f"(x.m));
+  x.move(mm, k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x.s += __shfl_xor_sync(0xffffffffu, x.s, o);
+    x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+  }
+}
+
+// ----------------------------------------------------------------------------- the K largest
+constexpr int kHits = 1024;      // pieces set aside, over all warps of a block
+constexpr int kList = 1024;      // tokens among which the K largest are found; kMaxCluster lists of kMaxTop
+
+template <int kThreads>
+struct TopShared {
+  static constexpr int kWarps = kThreads / 32, kWarpHits = kHits / kWarps;
+  uint4 piece[kWarps][kWarpHits];
+  int at[kWarps][kWarpHits];
+  float tops[kThreads];
+  uint64_t list[kList];
+  uint64_t best[kMaxTop];
+  Sums part[kWarps > kMaxCluster ? kWarps : kMaxCluster];
+  int hits[kWarps];
+  unsigned count[256];           // of the digit's values, where all tokens are gone through
+  int listed, overflow;
+  uint32_t digit, left;
+  float bar;
+  int64_t label;
+};
+
+// A value that K of the threads' largest values reach, or the lowest one: no more than 2^-7 of itself
+// below the K-th largest of them.  By warp 0.
+template <int kThreads>
+__device__ __forceinline__ float bar_of(const float *tops, int K) {
+  constexpr int kEach = kThreads / 32;
+  uint32_t o[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) o[i] = order_of(tops[lane_id() + 32 * i]) >> 16;
+  uint32_t t = 0;
+  for (int b = 15; b >= 0; --b) {
+    const uint32_t c = t | 1u << b;
+    unsigned n = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) n += o[i] >= c;
+    if (__reduce_add_sync(0xffffffffu, n) >= (unsigned)K) t = c;
+  }
+  return value_of((t < 0x80u ? 0x80u : t) << 16);      // 0x80 << 16: the lowest finite value
+}
+
+// The K largest of n keys (the rest of them 0) into best, in order.  Returns the least
+// key that belongs to them.
+template <int kThreads>
+__device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int K, uint64_t *best) {
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = list[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += list[j] > key;
+    if (rank < K) best[rank] = key;
+  }
+  for (int i = n + (int)threadIdx.x; i < K; i += kThreads) best[i] = 0;
+  __syncthreads();
+  return K > 0 && n >= K ? best[K - 1] : 0;
+}
+
+// The K largest of elements [e0, e1) whatever they are: digits of eight bits from the
+// highest on, the elements read again for each, then those above the K-th, and the
+// first ones that equal it.  Into list; returns how many.
+template <typename E, int kThreads>
+__device__ __noinline__ int select_all(TopShared<kThreads> &sh, const E *row, int e0, int e1, int K) {
+  const int tid = threadIdx.x;
+  uint32_t prefix = 0, left = K;      // the K-th largest's digits so far, its rank among those that share them
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += kThreads) sh.count[i] = 0;
+    __syncthreads();
+    for (int i = e0 + tid; i < e1; i += kThreads) {
+      const float v = Elem<E>::load(row + i);
+      const uint32_t o = order_of(v);
+      if (v >= kLowest && (shift == 24 || o >> (shift + 8) == prefix >> (shift + 8)))
+        atomicAdd(&sh.count[o >> shift & 255u], 1u);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t n = 0;
+      int d = 255;
+      for (; d > 0 && n + sh.count[d] < left; --d) n += sh.count[d];
+      sh.digit = d;
+      sh.left = left - n;            // fewer than K tokens in all: the digits come to 0, everything is above
+    }
+    __syncthreads();
+    prefix |= sh.digit << shift;
+    left = sh.left;
+    __syncthreads();
+  }
+  if (tid == 0) sh.listed = 0;
+  __syncthreads();
+  for (int i = e0 + tid; i < e1; i += kThreads) {
+    const float v = Elem<E>::load(row + i);
+    if (v >= kLowest && order_of(v) > prefix) {
+      const int n = atomicAdd(&sh.listed, 1);
+      if (n < K) sh.list[n] = key_of(v, i);
+    }
+  }
+  __syncthreads();
+  int have = min(sh.listed, K);
+  __syncthreads();
+  for (int from = e0; from < e1 && have < K; from += kThreads) {
+    const int i = from + tid;
+    float v = kNegInf;
+    if (i < e1) v = Elem<E>::load(row + i);
+    const bool same = v >= kLowest && order_of(v) == prefix;
+    const unsigned mask = __ballot_sync(0xffffffffu, same);
+    if (lane_id() == 0) sh.hits[tid >> 5] = __popc(mask);
+    __syncthreads();
+    int before = have, all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < tid >> 5) before += sh.hits[w];
+      all += sh.hits[w];
+    }
+    const int place = before + __popc(mask & ((1u << lane_id()) - 1u));
+    if (same && place < K) sh.list[place] = key_of(v, i);
+    have = min(have + all, K);
+    __syncthreads();
+  }
+  return have;
+}
+
+struct TopRow {
+  const void *logits;
+  int64_t ldl;
+  const int64_t *labels;
+  int64_t T, V;
+  int K;
+  float inv_t;
+  float *logps, *entropy;
+  int64_t *ids;
+  float *top, *rest;
+  float2 *stats;
+};
+
+template <typename E, int kThreads>
+__global__ void __launch_bounds__(kThreads) top_kernel(TopRow a, int C, int slice) {
+  constexpr int kWarps = kThreads / 32, N = Elem<E>::kVec, U = 4;
+  using Shared = TopShared<kThreads>;
+  __shared__ Shared sh;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t t = blockIdx.x / C;
+  const int rank = (int)(blockIdx.x % C), tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, K = a.K, V = (int)a.V;
+  if (tid == 0) {
+    sh.label = a.labels ? a.labels[t] : 0;      // read once for the block
+    sh.listed = sh.overflow = 0;
+  }
+  __syncthreads();
+  const int64_t label = sh.label;
+  const bool counts = !a.labels || (label >= 0 && label < V);
+  const float k = a.inv_t * kLog2e;
+  float picked = 0.f;
+  Sums rest = no_sums();                         // of all but the block's K largest
+  if (counts) {
+    const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
+    const RowSpan<E> sp(row, V);
+    const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
+    const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
+    if (rank == 0 && tid == 0 && a.labels) picked = Elem<E>::load(row + label);
+    PairSums<E> sums;
+    float top = kNegInf, bar = INFINITY;         // a thread's largest value so far; what a token has to reach
+    int hits = 0;                                // the warp's
+    int next = 1;                                // the round before which the bar is raised again
+    const int rounds = (v1 - v0 + U * kThreads - 1) / (U * kThreads);
+    for (int n = 0; n < rounds; ++n) {
+      const int i = v0 + n * U * kThreads + tid;
+      uint4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) q[u] = i + u * kThreads < v1 ? src[i + u * kThreads] : Elem<E>::lowest();
+      float g = Elem<E>::largest(q);
+      if (K > 0) {
+        top = fmaxf(top, g);
+        if (n + 1 == next) {
+          sh.tops[tid] = top;
+          __syncthreads();
+          if (warp == 0) {
+            const float b = bar_of<kThreads>(sh.tops, K);
+            if (lane == 0) sh.bar = b;
+          }
+          __syncthreads();
+          bar = sh.bar;
+          next *= 2;
+        }
+        if (__any_sync(0xffffffffu, g >= bar)) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint4 one[1] = {q[u]};
+            const bool hit = Elem<E>::largest(one) >= bar;
+            const unsigned mask = __ballot_sync(0xffffffffu, hit);
+            const int place = hits + __popc(mask & ((1u << lane) - 1u));
+            if (hit && place < Shared::kWarpHits) {
+              sh.piece[warp][place] = q[u];
+              sh.at[warp][place] = i + u * kThreads;
+            }
+            if (hit) q[u] = Elem<E>::lowest();
+            hits += __popc(mask);
+          }
+          g = Elem<E>::largest(q);
+        }
+      }
+      sums.add(q, g, k);
+    }
+    rest = sums.sums();
+    // the ragged ends, at most seven elements each: the first block's and the last one's
+    const bool at_head = rank == 0 && tid < sp.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
+    const int edge_at = at_head ? tid : tail + tid - 16;
+    float edge = kNegInf;
+    if (at_head || at_tail) edge = Elem<E>::load(row + edge_at);
+    if (K == 0) {
+      if (at_head || at_tail) rest.add(edge, k);
+    } else {
+      if (lane == 0) sh.hits[warp] = min(hits, Shared::kWarpHits);
+      if (hits > Shared::kWarpHits) sh.overflow = 1;
+      sh.tops[tid] = top;
+      __syncthreads();
+      if (warp == 0) {
+        const float b = bar_of<kThreads>(sh.tops, K);
+        if (lane == 0) sh.bar = b;
+      }
+      __syncthreads();
+      bar = sh.bar;
+      auto offer = [&](float v, int id) {
+        if (!(v >= bar)) return;
+        const int n = atomicAdd(&sh.listed, 1);
+        if (n < kList) sh.list[n] = key_of(v, id);
+      };
+      if (!sh.overflow) {
+        for (int j = lane; j < min(hits, Shared::kWarpHits); j += 32) {
+          float v[N];
+          Elem<E>::unpack(sh.piece[warp][j], v);
+          const int id = sp.head + sh.at[warp][j] * N;
+#pragma unroll
+          for (int e = 0; e < N; ++e) offer(v[e], id + e);
+        }
+        if (at_head || at_tail) offer(edge, edge_at);
+      }
+      __syncthreads();
+      const bool all = sh.overflow || sh.listed > kList;      // too many tokens for what was set aside
+      int n = sh.listed;
+      if (all) {
+        __syncthreads();
+        n = select_all<E, kThreads>(sh, row, rank == 0 ? 0 : sp.head + v0 * N, rank == C - 1 ? V : sp.head + v1 * N, K);
+      }
+      const uint64_t least = rank_list<kThreads>(sh.list, n, K, sh.best);
+      auto left = [&](float v, int id) {
+        if (!(v >= kLowest && key_of(v, id) >= least)) rest.add(v, k);
+      };
+      if (all) {
+        rest = no_sums();
+        for (int i = v0 + tid; i < v1; i += kThreads) {
+          float v[N];
+          Elem<E>::unpack(src[i], v);
+          for (int e = 0; e < N; ++e) left(v[e], sp.head + i * N + e);
+        }
+      } else {
+        for (int j = lane; j < min(hits, Shared::kWarpHits); j += 32) {
+          float v[N];
+          Elem<E>::unpack(sh.piece[warp][j], v);
+          const int id = sp.head + sh.at[warp][j] * N;
+#pragma unroll
+          for (int e = 0; e < N; ++e) left(v[e], id + e);
+        }
+      }
+      if (at_head || at_tail) left(edge, edge_at);
+    }
+  }
+  if (C > 1) {
+    // every block's K largest and sums to the first block, which finds the K largest of all
+    warp_merge(rest, k);
+    if (lane == 0) sh.part[warp] = rest;
+    __syncthreads();
+    rest = no_sums();
+    if (warp == 0) {
+      if (lane < kWarps) rest = sh.part[lane];
+      warp_merge(rest, k);
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();                              // the first block has done with its list and parts
+    if (counts) {
+      uint32_t list, part;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(list) : "r"(smem_u32(sh.list + rank * K)));
+      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(part) : "r"(smem_u32(sh.part + rank)));
+      for (int i = tid; i < K; i += kThreads)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list + 8 * i), "l"(sh.best[i]) : "memory");
+      if (tid == 0) {
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part), "f"(rest.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 4), "f"(rest.s) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 8), "f"(rest.w) : "memory");
+      }
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;                       // nothing is sent from here on
+    rest = no_sums();
+    if (counts) {
+      for (int i = tid; i < K; i += kThreads) sh.best[i] = 0;
+      __syncthreads();
+      // a token's rank: its place in its own list, and those above it in each of the others
+      for (int i = tid; i < C * K; i += kThreads) {
+        const uint64_t key = sh.list[i];
+        if (key == 0) continue;
+        const int own = i / K;
+        int above = i - own * K;
+        for (int c = 0; c < C; ++c) {
+          if (c == own) continue;
+          int lo = 0, hi = K;                    // those before lo are above, those from hi on are not
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (sh.list[c * K + mid] > key) lo = mid + 1; else hi = mid;
+          }
+          above += lo;
+        }
+        if (above < K) sh.best[above] = key; else rest.add(key_value(key), k);
+      }
+      if (tid < C) rest.add(sh.part[tid], k);
+    }
+    __syncthreads();
+  }
+  warp_merge(rest, k);
+  if (lane == 0) sh.part[warp] = rest;
+  __syncthreads();
+  if (warp != 0) return;
+  rest = no_sums();
+  if (lane < kWarps) rest = sh.part[lane];
+  warp_merge(rest, k);
+  if (!counts) {
+    for (int i = lane; i < K; i += 32) {
+      a.ids[t * K + i] = -1;
+      a.top[t * K + i] = kNegInf;
+    }
+    if (lane == 0) {
+      if (a.logps) a.logps[t] = 0.f;
+      if (a.entropy) a.entropy[t] = 0.f;
+      if (a.rest) a.rest[t] = 0.f;
+      if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
+    }
+    return;
+  }
+  Sums total = no_sums();                        // of the K largest
+  for (int i = lane; i < K; i += 32)
+    if (sh.best[i]) total.add(key_value(sh.best[i]), k);
+  warp_merge(total, k);
+  total.add(rest, k);
+  const bool fine = total.s > 0.f && total.s < INFINITY;
+  const float log_s = fine ? logf(total.s) : NAN, m = total.m;
+  for (int i = lane; i < K; i += 32) {
+    const uint64_t key = sh.best[i];
+    a.ids[t * K + i] = key && fine ? key_id(key) : -1;
+    a.top[t * K + i] = !fine ? NAN : key ? (key_value(key) - m) * a.inv_t - log_s : kNegInf;
+  }
+  if (lane == 0) {
+    if (a.logps) a.logps[t] = (picked - m) * a.inv_t - log_s;
+    if (a.entropy) a.entropy[t] = log_s - total.w * kLn2 / total.s;
+    if (a.rest) a.rest[t] = !fine ? NAN : rest.s > 0.f ? (rest.m - m) * a.inv_t + logf(rest.s) - log_s : kNegInf;
+    if (a.stats) a.stats[t] = make_float2(m, total.s);
+  }
+}
+
+// ----------------------------------------------------------------------------- gradient
+// d = e (a + b u) for a token that no gradient comes from by itself.
+struct TopGrad {
+  float m, k, a, b;
+  static constexpr float c = 0.f;
+  __device__ __forceinline__ float operator()(float v) const {
+    const float u = fmaxf((v - m) * k, kLeast);
+    return ex2(u) * fmaf(b, u, a);
+  }
+  template <typename E>
+  __device__ __forceinline__ uint4 piece(const uint4 &q) const {
+    constexpr int N = Elem<E>::kVec;
+    uint64_t v[N / 2];
+    Elem<E>::pairs(q, v);
+    const uint64_t m2 = pk2(-m, -m), k2 = pk2(k, k), a2 = pk2(a, a), b2 = pk2(b, b);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      const float2 x = unpk2(mul2(add2(v[j], m2), k2));
+      const uint64_t u = pk2(fmaxf(x.x, kLeast), fmaxf(x.y, kLeast));
+      v[j] = mul2(ex2_2(u), fma2(b2, u, a2));
+    }
+    return Elem<E>::pack_pairs(v);
+  }
+};
+
+struct TopGradRow {
+  TopRow r;
+  const float *dlogps, *dentropy, *dtop;
+  void *dlogits;
+  int64_t lddl;
+};
+
+constexpr int kGradThreads = 256;
+
+template <typename E>
+__global__ void __launch_bounds__(kGradThreads) top_grad_kernel(TopGradRow h, int parts, int slice) {
+  __shared__ int ids[kMaxTop + 1];               // -1: none; the label after the listed tokens
+  __shared__ float add[kMaxTop + 1];
+  __shared__ int64_t label_of;
+  pdl_wait();
+  const TopRow &a = h.r;
+  const int64_t t = a.T - 1 - blockIdx.x / parts;      // the rows that were read last come first
+  const int rank = (int)(blockIdx.x % parts), tid = threadIdx.x, V = (int)a.V, K = h.dtop ? a.K : 0;
+  constexpr int N = Elem<E>::kVec;
+  if (tid == 0) label_of = a.labels ? a.labels[t] : 0;      // read once for the block
+  __syncthreads();
+  const int64_t label = label_of;
+  const bool counts = !a.labels || (label >= 0 && label < V);
+  E *out = static_cast<E *>(h.dlogits) + t * h.lddl;
+  const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
+  const RowSpan<E> sp(row, V);
+  const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
+  const int e0 = rank == 0 ? 0 : sp.head + v0 * N, e1 = rank == parts - 1 ? V : sp.head + v1 * N;
+  if (tid <= K) {
+    int64_t id = -1;
+    float g = 0.f;
+    if (tid < K) {
+      id = a.ids[t * K + tid];
+      g = h.dtop[t * K + tid];
+    } else if (a.labels && h.dlogps) {
+      id = label;
+      g = h.dlogps[t];
+    }
+    const bool there = counts && id >= 0 && id < V;
+    ids[tid] = there ? (int)id : -1;
+    add[tid] = there ? g : 0.f;
+  }
+  __syncthreads();
+  float G = 0.f;
+  bool any = false;
+  for (int j = lane_id(); j <= K; j += 32) {
+    G += add[j];
+    any = any || add[j] != 0.f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
+  const float dh = counts && h.dentropy ? h.dentropy[t] : 0.f;
+  if (!counts || (dh == 0.f && !__any_sync(0xffffffffu, any))) {      // the same for all warps
+    zero_span<E, kGradThreads>(out, e0, e1, tid);
+    return;
+  }
+  const float2 st = a.stats[t];
+  const float log_s = logf(st.y), f = a.inv_t / st.y;
+  TopGrad g;
+  g.m = st.x;
+  g.k = a.inv_t * kLog2e;
+  g.a = -f * (dh != 0.f ? G + dh * (a.entropy[t] - log_s) : G);
+  g.b = -f * dh * kLn2;
+  // a listed token's own gradient, once for each time that it is listed; its logit
+  // before the gradient may replace it
+  const int mark = tid <= K ? ids[tid] : -1;
+  const bool mine = mark >= e0 && mark < e1;
+  float value = 0.f;
+  if (mine) {
+    float sum = 0.f;
+    for (int j = 0; j <= K; ++j)
+      if (ids[j] == mark) sum += add[j];
+    value = g(Elem<E>::load(row + mark)) + sum * a.inv_t;
+  }
+  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
+  __syncthreads();
+  if (!same) {
+    grad_words<E, kGradThreads>(out, row, e0, e1, -1, g);
+  } else {
+    const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
+    uint4 *dst = reinterpret_cast<uint4 *>(out + sp.head);
+    int i = v0 + tid;
+    for (; v1 - i > 3 * kGradThreads; i += 4 * kGradThreads) {
+      uint4 q[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) q[u] = src[i + u * kGradThreads];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) __stcs(dst + i + u * kGradThreads, g.piece<E>(q[u]));
+    }
+    for (; i < v1; i += kGradThreads) __stcs(dst + i, g.piece<E>(src[i]));
+    auto one = [&](int j) { Elem<E>::store(out + j, g(Elem<E>::load(row + j))); };
+    if (rank == 0 && tid < sp.head) one(tid);
+    if (rank == parts - 1 && tid < V - tail) one(tail + tid);
+  }
+  __syncthreads();                               // the listed tokens' places come after the pieces
+  if (mine) Elem<E>::store(out + mark, value);
+}
+
+// 16-byte pieces of one of `parts` slices of a row.
+int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_up(ceil_div(bytes / 16, parts), 8)); }
+
+TopRow row_of(const TopArgs &a) {
+  TopRow r{};
+  r.logits = a.logits;
+  r.ldl = a.ldl;
+  r.labels = a.labels;
+  r.T = a.T;
+  r.V = a.V;
+  r.K = a.K;
+  r.inv_t = 1.f / a.temperature;
+  r.logps = a.logps;
+  r.entropy = a.entropy;
+  r.ids = a.top_ids;
+  r.top = a.top_logps;
+  r.rest = a.rest_logps;
+  r.stats = reinterpret_cast<float2 *>(a.stats);
+  return r;
+}
+
+template <typename E>
+cudaError_t launch_top(const TopRow &r, int64_t bytes, cudaStream_t st) {
+  const int64_t sms = num_sms();
+  if (2 * r.T < sms) {
+    const int c = (int)std::min<int64_t>({std::max<int64_t>(1, 4 * sms / r.T), std::max<int64_t>(1, bytes / (4 << 10)),
+                                          kMaxCluster});
+    return launch(top_kernel<E, 256>, dim3((unsigned)(r.T * c)), dim3(256), 0, st, c, true, r, c, slice_of(bytes, c));
+  }
+  return launch(top_kernel<E, 256>, dim3((unsigned)r.T), dim3(256), 0, st, 1, true, r, 1, slice_of(bytes, 1));
+}
+
+// Blocks for each row of the gradient pass, as for the gradient of label log-probabilities.
+int parts_of(int64_t T, int64_t bytes) {
+  const int64_t once = 8 * (int64_t)num_sms();
+  int64_t c = std::min(ceil_div(8 * once, T), bytes / (16 << 10));
+  c = std::max(c, std::min(ceil_div(once, T), bytes / (4 << 10)));
+  return (int)std::min<int64_t>(std::max<int64_t>(c, 1), 64);
+}
+
+}  // namespace
+
+// ----------------------------------------------------------------------------- host side
+lora_status_t top_logps(const TopArgs &a, cudaStream_t st) {
+  if (a.T == 0) return LORA_OK;
+  const TopRow r = row_of(a);
+  LORA_CUDA(a.dtype == LORA_BF16 ? launch_top<__nv_bfloat16>(r, a.V * 2, st) : launch_top<float>(r, a.V * 4, st));
+  return LORA_OK;
+}
+
+lora_status_t top_logps_backward(const TopArgs &a, const TopGradArgs &g, cudaStream_t st) {
+  if (a.T == 0 || a.V == 0) return LORA_OK;
+  TopGradRow h{};
+  h.r = row_of(a);
+  h.r.ids = const_cast<int64_t *>(g.top_ids);
+  h.r.stats = reinterpret_cast<float2 *>(const_cast<float *>(g.stats));
+  h.r.entropy = const_cast<float *>(g.entropy);
+  h.dlogps = g.dlogps;
+  h.dentropy = g.dentropy;
+  h.dtop = g.dtop_logps;
+  h.dlogits = g.dlogits;
+  h.lddl = g.lddl;
+  const int64_t bytes = a.V * (a.dtype == LORA_BF16 ? 2 : 4);
+  const int c = parts_of(a.T, bytes), slice = slice_of(bytes, c);
+  const dim3 grid((unsigned)(a.T * c)), block(kGradThreads);
+  LORA_CUDA(a.dtype == LORA_BF16 ? launch(top_grad_kernel<__nv_bfloat16>, grid, block, 0, st, 1, true, h, c, slice)
+                                 : launch(top_grad_kernel<float>, grid, block, 0, st, 1, true, h, c, slice));
+  return LORA_OK;
+}
+
+}  // namespace lora

@@ -6,6 +6,7 @@
 #include "adamw.h"
 #include "host_common.h"
 #include "loss.h"
+#include "top.h"
 
 namespace lora {
 namespace {
@@ -30,8 +31,9 @@ lora_status_t check_ws(const void *ws, size_t ws_bytes, size_t need) {
   return LORA_OK;
 }
 
-lora_status_t check_rows(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
-                         const int64_t *labels, float temperature, const void *dlogits, int64_t lddl) {
+// Rows of logits alone.
+lora_status_t check_logits(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
+                           float temperature, const void *dlogits, int64_t lddl) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_UNSUPPORTED;
   if (!size_ok(T) || !size_ok(V)) return LORA_ERR_INVALID_ARG;
   if (V > kMaxVocab) return LORA_ERR_UNSUPPORTED;
@@ -46,6 +48,12 @@ lora_status_t check_rows(lora_dtype_t dtype, int64_t T, int64_t V, const void *l
     LORA_TRY(check_opt(dlogits, e));
     if (dlogits == logits && lddl != ldl) return LORA_ERR_INVALID_ARG;
   }
+  return LORA_OK;
+}
+
+lora_status_t check_rows(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
+                         const int64_t *labels, float temperature, const void *dlogits, int64_t lddl) {
+  LORA_TRY(check_logits(dtype, T, V, logits, ldl, temperature, dlogits, lddl));
   return check_ptr(labels, T, 8);
 }
 
@@ -190,6 +198,78 @@ lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const v
     return policy_loss(loss_args(dtype, T, V, logits, ldl, labels, temperature, token_logps, dlogits, lddl,
                                  grad_scale), p, ws, ws_bytes, (cudaStream_t)stream);
   });
+}
+
+lora_status_t lora_top_logps(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits, int64_t ldl,
+                             const int64_t *labels, float temperature, float *logps, float *entropy,
+                             int64_t *top_ids, float *top_logps_out, float *rest_logps, float *stats, void *stream) {
+  LORA_TRY(check_logits(dtype, T, V, logits, ldl, temperature, nullptr, 0));
+  if (K < 0) return LORA_ERR_INVALID_ARG;
+  if (K > LORA_TOP_MAX) return LORA_ERR_UNSUPPORTED;
+  if (T > 0 && (labels == nullptr) != (logps == nullptr)) return LORA_ERR_INVALID_ARG;
+  LORA_TRY(check_opt(labels, 8));
+  LORA_TRY(check_opt(logps, 4));
+  LORA_TRY(check_opt(entropy, 4));
+  LORA_TRY(check_opt(rest_logps, 4));
+  LORA_TRY(check_opt(stats, 8));
+  LORA_TRY(check_ptr(top_ids, T * K, 8));
+  LORA_TRY(check_ptr(top_logps_out, T * K, 4));
+  TopArgs a{};
+  a.dtype = dtype; a.T = T; a.V = V; a.K = K; a.logits = logits; a.ldl = ldl; a.labels = labels;
+  a.temperature = temperature; a.logps = logps; a.entropy = entropy; a.top_ids = top_ids; a.top_logps = top_logps_out;
+  a.rest_logps = rest_logps; a.stats = stats;
+  return guarded([&] { return top_logps(a, (cudaStream_t)stream); });
+}
+
+lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits,
+                                      int64_t ldl, const int64_t *labels, const int64_t *top_ids, float temperature,
+                                      const float *stats, const float *entropy, const float *dlogps,
+                                      const float *dentropy, const float *dtop_logps, void *dlogits, int64_t lddl,
+                                      void *stream) {
+  LORA_TRY(check_logits(dtype, T, V, logits, ldl, temperature, dlogits, lddl));
+  if (K < 0) return LORA_ERR_INVALID_ARG;
+  if (K > LORA_TOP_MAX) return LORA_ERR_UNSUPPORTED;
+  if (T > 0 && labels == nullptr && dlogps != nullptr) return LORA_ERR_INVALID_ARG;
+  if (T > 0 && entropy == nullptr && dentropy != nullptr) return LORA_ERR_INVALID_ARG;
+  LORA_TRY(check_ptr(dlogits, T * V, 1));
+  LORA_TRY(check_opt(labels, 8));
+  LORA_TRY(check_ptr(stats, T, 8));
+  LORA_TRY(check_opt(entropy, 4));
+  LORA_TRY(check_opt(dlogps, 4));
+  LORA_TRY(check_opt(dentropy, 4));
+  LORA_TRY(check_opt(dtop_logps, 4));
+  if (dtop_logps != nullptr) LORA_TRY(check_ptr(top_ids, T * K, 8));
+  TopArgs a{};
+  a.dtype = dtype; a.T = T; a.V = V; a.K = K; a.logits = logits; a.ldl = ldl; a.labels = labels;
+  a.temperature = temperature;
+  const TopGradArgs g = {top_ids, stats, entropy, dlogps, dentropy, dtop_logps, dlogits, lddl};
+  return guarded([&] { return top_logps_backward(a, g, (cudaStream_t)stream); });
+}
+
+lora_status_t lora_distill_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits, int64_t ldl,
+                                const int64_t *top_ids, const float *teacher_logps, const float *rest_logps,
+                                const float *weights, lora_distill_kind_t kind, float temperature, float *row_loss,
+                                float *loss, void *dlogits, int64_t lddl, float grad_scale, void *stream) {
+  LORA_TRY(check_logits(dtype, T, V, logits, ldl, temperature, dlogits, lddl));
+  if (K < 1) return LORA_ERR_INVALID_ARG;
+  if (K > LORA_TOP_MAX) return LORA_ERR_UNSUPPORTED;
+  if (kind != LORA_DISTILL_FORWARD && kind != LORA_DISTILL_REVERSE) return LORA_ERR_UNSUPPORTED;
+  if (!isfinite(grad_scale)) return LORA_ERR_INVALID_ARG;
+  LORA_TRY(check_ptr(top_ids, T * K, 8));
+  LORA_TRY(check_ptr(teacher_logps, T * K, 4));
+  LORA_TRY(check_opt(rest_logps, 4));
+  LORA_TRY(check_opt(weights, 4));
+  LORA_TRY(check_ptr(row_loss, T, 4));
+  LORA_TRY(check_ptr(loss, 1, 4));
+  // the sum takes the weights once more, after the rows' losses have been written
+  for (const float *in : {teacher_logps, rest_logps, weights})
+    if (T > 0 && row_loss == in) return LORA_ERR_INVALID_ARG;
+  DistillArgs a{};
+  a.dtype = dtype; a.T = T; a.V = V; a.K = K; a.logits = logits; a.ldl = ldl; a.ids = top_ids;
+  a.teacher = teacher_logps; a.rest = rest_logps; a.weights = weights; a.reverse = kind == LORA_DISTILL_REVERSE;
+  a.temperature = temperature; a.row_loss = row_loss; a.loss = loss; a.dlogits = dlogits; a.lddl = lddl;
+  a.grad_scale = grad_scale;
+  return guarded([&] { return distill_loss(a, (cudaStream_t)stream); });
 }
 
 lora_status_t lora_scale_gradient(lora_dtype_t dtype, int64_t T, int64_t V, void *x, int64_t ldx,

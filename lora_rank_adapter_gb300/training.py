@@ -1,6 +1,8 @@
 """Thin Python binding of the training operators (include/lora_train.h): the
 log-probabilities of labels, the preference loss and the clipped policy loss with
-their gradients, and the AdamW step over an adapter's many tensors.
+their gradients, log-probabilities with entropy and the most probable tokens, the
+distillation loss from a teacher's record of those, and the AdamW step over an
+adapter's many tensors.
 
 Like `binding`, each function has the name of the C entry point it calls, takes
 torch tensors that already live on the GPU, checks and marshals them, allocates
@@ -26,11 +28,14 @@ from . import binding
 from .binding import _check, _dtype, _entry, _raw_stream
 
 TRAIN_EXPORTS = ["lora_train_workspace_size", "lora_token_logps", "lora_token_logps_backward",
-                 "lora_preference_loss", "lora_policy_loss", "lora_scale_gradient", "lora_adamw_table_size",
-                 "lora_adamw_build", "lora_grad_norm", "lora_adamw"]
+                 "lora_preference_loss", "lora_policy_loss", "lora_top_logps", "lora_top_logps_backward",
+                 "lora_distill_loss", "lora_scale_gradient", "lora_adamw_table_size", "lora_adamw_build",
+                 "lora_grad_norm", "lora_adamw"]
 TRAIN_PREFERENCE_LOSS, TRAIN_POLICY_LOSS = 0, 1
 PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 PREF_LENGTH_NORMALIZE = 1
+TOP_MAX = 128                      # alternatives of a row at most
+DISTILL_KINDS = {"forward": 0, "reverse": 1}
 ADAMW_STATE_8BIT, ADAMW_MASTER, ADAMW_STOCHASTIC = 1, 2, 16
 ADAMW_BLOCK, ADAMW_CHUNK = 256, 2048
 POLICY_HELD_BYTES = 768 << 10      # rows up to here need no workspace in lora_policy_loss
@@ -75,6 +80,9 @@ def lib():
                                        P, i64, f32, P, sz, P]),
         "lora_policy_loss": (i32, [i32, i64, i64, P, i64, P, P, P, P, P, f32, f32, f32, f32, P, P, P, i64, f32,
                                    P, sz, P]),
+        "lora_top_logps": (i32, [i32, i64, i64, i32, P, i64, P, f32, P, P, P, P, P, P, P]),
+        "lora_top_logps_backward": (i32, [i32, i64, i64, i32, P, i64, P, P, f32, P, P, P, P, P, P, i64, P]),
+        "lora_distill_loss": (i32, [i32, i64, i64, i32, P, i64, P, P, P, P, i32, f32, P, P, P, i64, f32, P]),
         "lora_scale_gradient": (i32, [i32, i64, i64, P, i64, P, P]),
         "lora_adamw_table_size": (sz, [TP, i32]),
         "lora_adamw_build": (i32, [TP, i32, i32, i32, u32, P, sz, PP, P]),
@@ -239,6 +247,94 @@ def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps
                grad_scale, w, wn, _raw_stream(stream, dev))
     _check(st, "lora_policy_loss")
     return metrics
+
+
+def _entries(t, T, K, dtype, name, device):
+    """The address of a contiguous [T, K] tensor."""
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != K:
+        raise ValueError(f"{name} have to be [{T}, {K}], not {tuple(t.shape)}")
+    return _vector(t, T * K, dtype, name, device)
+
+
+def lora_top_logps(logits, top_ids, top_logps, labels=None, logps=None, entropy=None, rest_logps=None, stats=None,
+                   temperature=1.0, stream=None):
+    """The most probable tokens of each row with their log-probabilities (int64 and fp32
+    [T, K], K up to TOP_MAX, are written; most probable first, ties by lowest id; -1 and
+    minus infinity where there are fewer), and what else is asked for, fp32 [T]: the
+    labels' log-probabilities, the entropy, and the log of the mass of all other tokens.
+    labels: int64 [T], with logps, or both None; a row whose label is outside [0, V) is
+    ignored.  stats: fp32 [T, 2] for lora_top_logps_backward."""
+    T, V, x, ld = _matrix(logits, "logits")
+    dev, f32 = logits.get_device(), torch.float32
+    if (labels is None) != (logps is None):
+        raise ValueError("labels and logps go together")
+    if top_ids.dim() != 2:
+        raise ValueError("top_ids have to be [T, K]")
+    K = top_ids.shape[1]
+    entry = _entry(lib().lora_top_logps, dev)
+    st = entry(_dtype(logits), T, V, K, x, ld, _optional(labels, T, torch.int64, "labels", dev), temperature,
+               _optional(logps, T, f32, "logps", dev), _optional(entropy, T, f32, "entropy", dev),
+               _entries(top_ids, T, K, torch.int64, "top_ids", dev), _entries(top_logps, T, K, f32, "top_logps", dev),
+               _optional(rest_logps, T, f32, "rest_logps", dev), _optional(stats, 2 * T, f32, "stats", dev),
+               _raw_stream(stream, dev))
+    _check(st, "lora_top_logps")
+    return top_logps
+
+
+def lora_top_logps_backward(logits, stats, dlogits, labels=None, top_ids=None, entropy=None, dlogps=None,
+                            dentropy=None, dtop_logps=None, temperature=1.0, stream=None):
+    """dlogits of lora_top_logps from its stats and the gradients of its results (fp32 [T],
+    [T] and [T, K]; None for zero): dlogps needs the labels, dentropy the entropy, dtop_logps
+    the top_ids that lora_top_logps wrote.  dlogits may be the logits themselves."""
+    T, V, x, ld = _matrix(logits, "logits")
+    dev, f32 = logits.get_device(), torch.float32
+    if dlogits is None:
+        raise ValueError("dlogits are missing")
+    for given, needs, what in ((dlogps, labels, "dlogps need the labels"), (dentropy, entropy, "dentropy needs the entropy"),
+                               (dtop_logps, top_ids, "dtop_logps need the top_ids")):
+        if given is not None and needs is None:
+            raise ValueError(what)
+    d, ldd = _gradient(dlogits, logits)
+    K, ids, dtop = 0, None, None
+    if dtop_logps is not None:
+        if top_ids.dim() != 2:
+            raise ValueError("top_ids have to be [T, K]")
+        K = top_ids.shape[1]
+        ids = _entries(top_ids, T, K, torch.int64, "top_ids", dev)
+        dtop = _entries(dtop_logps, T, K, f32, "dtop_logps", dev)
+    entry = _entry(lib().lora_top_logps_backward, dev)
+    st = entry(_dtype(logits), T, V, K, x, ld, _optional(labels, T, torch.int64, "labels", dev), ids, temperature,
+               _vector(stats, 2 * T, f32, "stats", dev), _optional(entropy, T, f32, "entropy", dev),
+               _optional(dlogps, T, f32, "dlogps", dev), _optional(dentropy, T, f32, "dentropy", dev), dtop, d, ldd,
+               _raw_stream(stream, dev))
+    _check(st, "lora_top_logps_backward")
+    return dlogits
+
+
+def lora_distill_loss(logits, top_ids, top_logps, row_loss, loss, rest_logps=None, weights=None, dlogits=None,
+                      kind="forward", temperature=1.0, grad_scale=1.0, stream=None):
+    """The divergence of each row from a teacher's record, the top_ids [T, K], top_logps [T, K]
+    and rest_logps [T] that lora_top_logps wrote for the teacher's logits at this temperature,
+    summed with the rows' weights (fp32 [T], None: 1); with dlogits also its gradient.  kind:
+    "forward", KL(teacher || student), or "reverse", KL(student || teacher).  Without rest_logps
+    only the listed tokens' terms are taken, with it also that of all others together.  row_loss
+    [T] and loss [1] are written; a row of weight 0, or without a token in [0, V), is ignored."""
+    T, V, x, ld = _matrix(logits, "logits")
+    dev, f32 = logits.get_device(), torch.float32
+    if kind not in DISTILL_KINDS:
+        raise ValueError(f"kind has to be one of {sorted(DISTILL_KINDS)}")
+    if top_ids.dim() != 2:
+        raise ValueError("top_ids have to be [T, K]")
+    K = top_ids.shape[1]
+    d, ldd = _gradient(dlogits, logits)
+    entry = _entry(lib().lora_distill_loss, dev)
+    st = entry(_dtype(logits), T, V, K, x, ld, _entries(top_ids, T, K, torch.int64, "top_ids", dev),
+               _entries(top_logps, T, K, f32, "top_logps", dev), _optional(rest_logps, T, f32, "rest_logps", dev),
+               _optional(weights, T, f32, "weights", dev), DISTILL_KINDS[kind], temperature,
+               _vector(row_loss, T, f32, "row_loss", dev), _vector(loss, 1, f32, "loss", dev), d, ldd, grad_scale,
+               _raw_stream(stream, dev))
+    _check(st, "lora_distill_loss")
+    return loss
 
 
 def lora_scale_gradient(x, factor, stream=None):
