@@ -35,7 +35,7 @@ struct Distill {
   int64_t T, V;
   int K;
   bool reverse;
-  float inv_t;
+  Scale scale;
   float *row_loss;
   void *dlogits;
   int64_t lddl;
@@ -63,7 +63,7 @@ struct RowTerms {
   float dz[kEach];
 };
 __device__ __forceinline__ RowTerms row_terms(const Distill &a, const Record &r, float ln_qr, float m, float s, float c) {
-  const float k = a.inv_t * kLog2e;
+  const float k = a.scale.k;
   float top = kNegInf;
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
@@ -78,14 +78,14 @@ __device__ __forceinline__ RowTerms row_terms(const Distill &a, const Record &r,
     sum += e[i];
   }
   const float rest = s * ex2((m - ref) * k), S = warp_sum_f(sum) + rest, ln_S = logf(S);
-  const float p_r = rest / S, ln_pr = (m - ref) * a.inv_t + logf(s) - ln_S;
+  const float p_r = rest / S, ln_pr = a.scale.gap(m, ref) + logf(s) - ln_S;
   float L = 0.f, Q = 0.f, P = 0.f, p[kEach], q[kEach], gap[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const bool there = r.id[i] >= 0;
     p[i] = e[i] / S;
     q[i] = there ? expf(r.lnq[i]) : 0.f;
-    gap[i] = (r.z[i] - ref) * a.inv_t - ln_S - r.lnq[i];
+    gap[i] = a.scale.gap(r.z[i], ref) - ln_S - r.lnq[i];
     if (!there) {
       p[i] = gap[i] = 0.f;
     } else if (a.reverse) {
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Distill a, int C, int
   const RowSpan<E> sp(row, V);
   const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
   const int e0 = rank == 0 ? 0 : sp.head + v0 * N, e1 = rank == C - 1 ? V : sp.head + v1 * N;
-  const float k = a.inv_t * kLog2e;
+  const float k = a.scale.k;
   if (tid < kMaxTop) {
     const int64_t id = tid < K ? a.ids[t * K + tid] : -1;
     ids[tid] = id >= 0 && id < V ? (int)id : -1;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Distill a, int C, int
       r.z[i] = logit[j];
       r.lnq[i] = r.id[i] >= 0 ? a.teacher[t * K + j] : 0.f;
     }
-    const RowTerms x = row_terms(a, r, a.rest ? a.rest[t] : 0.f, m, s, w * a.grad_scale * a.inv_t);
+    const RowTerms x = row_terms(a, r, a.rest ? a.rest[t] : 0.f, m, s, w * a.grad_scale * a.scale.hi);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) dz[i * 32 + lane] = x.dz[i];
     if (lane == 0) {
@@ -304,7 +304,7 @@ lora_status_t distill_loss(const DistillArgs &a, cudaStream_t st) {
   }
   Distill r{};
   r.logits = a.logits; r.ldl = a.ldl; r.ids = a.ids; r.teacher = a.teacher; r.rest = a.rest; r.weights = a.weights;
-  r.T = a.T; r.V = a.V; r.K = a.K; r.reverse = a.reverse; r.inv_t = 1.f / a.temperature; r.row_loss = a.row_loss;
+  r.T = a.T; r.V = a.V; r.K = a.K; r.reverse = a.reverse; r.scale = Scale::of(a.temperature); r.row_loss = a.row_loss;
   r.dlogits = a.dlogits; r.lddl = a.lddl; r.grad_scale = a.grad_scale;
   LORA_CUDA(a.dtype == LORA_BF16 ? launch_distill<__nv_bfloat16>(r, a.V * 2, st) : launch_distill<float>(r, a.V * 4, st));
   LORA_CUDA(launch(loss_kernel, dim3(1), dim3(kSumThreads), 0, st, 1, true, (const float *)a.row_loss, a.weights, a.T,

@@ -207,6 +207,23 @@ __device__ __forceinline__ void block_merge(float &m, float &s, float k, float2 
   warp_merge(m, s, k);
 }
 
+// 1 / temperature: for the exponential (times log2(e), rounded once), and in two parts for
+// the few values whose own last bits count.
+struct Scale {
+  float k, hi, lo;
+  static Scale of(float temperature) {
+    const double inv = 1.0 / (double)temperature;
+    const float hi = (float)inv;
+    return {(float)(inv * 1.4426950408889634074), hi, (float)(inv - (double)hi)};
+  }
+  // (x - y) / temperature; the difference's rounding error, exact in fp32, counts too
+  __device__ __forceinline__ float gap(float x, float y) const {
+    const float d = __fsub_rn(x, y), b = __fsub_rn(d, x);
+    const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(y, b));
+    return fabsf(d) < INFINITY ? fmaf(d, hi, fmaf(e, hi, d * lo)) : d * hi;
+  }
+};
+
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

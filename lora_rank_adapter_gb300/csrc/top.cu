@@ -254,7 +254,7 @@ struct TopRow {
   const int64_t *labels;
   int64_t T, V;
   int K;
-  float inv_t;
+  Scale scale;
   float *logps, *entropy;
   int64_t *ids;
   float *top, *rest;
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) top_kernel(TopRow a, int C, int slic
   __syncthreads();
   const int64_t label = sh.label;
   const bool counts = !a.labels || (label >= 0 && label < V);
-  const float k = a.inv_t * kLog2e;
+  const float k = a.scale.k;
   float picked = 0.f;
   Sums rest = no_sums();                         // of all but the block's K largest
   if (counts) {
@@ -471,18 +471,24 @@ __global__ void __launch_bounds__(kThreads) top_kernel(TopRow a, int C, int slic
   for (int i = lane; i < K; i += 32)
     if (sh.best[i]) total.add(key_value(sh.best[i]), k);
   warp_merge(total, k);
+  const float listed = total.s, listed_m = total.m;
   total.add(rest, k);
   const bool fine = total.s > 0.f && total.s < INFINITY;
   const float log_s = fine ? logf(total.s) : NAN, m = total.m;
   for (int i = lane; i < K; i += 32) {
     const uint64_t key = sh.best[i];
     a.ids[t * K + i] = key && fine ? key_id(key) : -1;
-    a.top[t * K + i] = !fine ? NAN : key ? (key_value(key) - m) * a.inv_t - log_s : kNegInf;
+    a.top[t * K + i] = !fine ? NAN : key ? a.scale.gap(key_value(key), m) - log_s : kNegInf;
   }
   if (lane == 0) {
-    if (a.logps) a.logps[t] = (picked - m) * a.inv_t - log_s;
+    if (a.logps) a.logps[t] = a.scale.gap(picked, m) - log_s;
     if (a.entropy) a.entropy[t] = log_s - total.w * kLn2 / total.s;
-    if (a.rest) a.rest[t] = !fine ? NAN : rest.s > 0.f ? (rest.m - m) * a.inv_t + logf(rest.s) - log_s : kNegInf;
+    if (a.rest) {
+      // ln of rest / (rest + listed), without the two large logarithms where that is more than nothing
+      const float ratio = listed * ex2((listed_m - ref_of(rest.m)) * k) / rest.s;
+      a.rest[t] = !fine ? NAN : !(rest.s > 0.f) ? kNegInf
+                  : ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(rest.m, m) + logf(rest.s) - log_s;
+    }
     if (a.stats) a.stats[t] = make_float2(m, total.s);
   }
 }
@@ -569,10 +575,10 @@ __global__ void __launch_bounds__(kGradThreads) top_grad_kernel(TopGradRow h, in
     return;
   }
   const float2 st = a.stats[t];
-  const float log_s = logf(st.y), f = a.inv_t / st.y;
+  const float log_s = logf(st.y), f = a.scale.hi / st.y;
   TopGrad g;
   g.m = st.x;
-  g.k = a.inv_t * kLog2e;
+  g.k = a.scale.k;
   g.a = -f * (dh != 0.f ? G + dh * (a.entropy[t] - log_s) : G);
   g.b = -f * dh * kLn2;
   // a listed token's own gradient, once for each time that it is listed; its logit
@@ -584,7 +590,7 @@ __global__ void __launch_bounds__(kGradThreads) top_grad_kernel(TopGradRow h, in
     float sum = 0.f;
     for (int j = 0; j <= K; ++j)
       if (ids[j] == mark) sum += add[j];
-    value = g(Elem<E>::load(row + mark)) + sum * a.inv_t;
+    value = g(Elem<E>::load(row + mark)) + sum * a.scale.hi;
   }
   const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
   __syncthreads();
@@ -621,7 +627,7 @@ TopRow row_of(const TopArgs &a) {
   r.T = a.T;
   r.V = a.V;
   r.K = a.K;
-  r.inv_t = 1.f / a.temperature;
+  r.scale = Scale::of(a.temperature);
   r.logps = a.logps;
   r.entropy = a.entropy;
   r.ids = a.top_ids;
