@@ -49,6 +49,14 @@ struct Elem<float> {
                          fmaxf(__uint_as_float(q[u].z), __uint_as_float(q[u].w))));
     return b;
   }
+  // a piece's largest value, as much of it as comparing pieces takes
+  using Peak = float;
+  static __device__ __forceinline__ Peak peak(const uint4 &q) {
+    return fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)), fmaxf(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+  static __device__ __forceinline__ Peak higher(Peak a, Peak b) { return fmaxf(a, b); }
+  static __device__ __forceinline__ float value(Peak p) { return p; }
+  static __device__ __forceinline__ Peak no_peak() { return kNegInf; }
   static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u); }
   // minus infinity in place i of a piece
   static __device__ __forceinline__ void strike(uint4 &q, int i) {
@@ -95,6 +103,20 @@ struct Elem<__nv_bfloat16> {
       b = __hmax2(b, __hmax2(__hmax2(two(q[u].x), two(q[u].y)), __hmax2(two(q[u].z), two(q[u].w))));
     const float2 f = __bfloat1622float2(b);
     return fmaxf(f.x, f.y);
+  }
+  using Peak = __nv_bfloat162;
+  static __device__ __forceinline__ Peak peak(const uint4 &q) {
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); };
+    return __hmax2(__hmax2(two(q.x), two(q.y)), __hmax2(two(q.z), two(q.w)));
+  }
+  static __device__ __forceinline__ Peak higher(Peak a, Peak b) { return __hmax2(a, b); }
+  static __device__ __forceinline__ float value(Peak p) {
+    const float2 f = __bfloat1622float2(p);
+    return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ Peak no_peak() {
+    const uint32_t w = 0xff80ff80u;
+    return *reinterpret_cast<const __nv_bfloat162 *>(&w);
   }
   static __device__ __forceinline__ uint4 lowest() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
   static __device__ __forceinline__ void strike(uint4 &q, int i) {

@@ -132,56 +132,89 @@ __device__ __forceinline__ void warp_merge(Sums &x, float k) {
 }
 
 // ----------------------------------------------------------------------------- the K largest
-constexpr int kHits = 1024;      // pieces set aside, over all warps of a block
-constexpr int kList = 1024;      // tokens among which the K largest are found; kMaxCluster lists of kMaxTop
+constexpr int kTopThreads = 256;
+constexpr int kTopWarps = kTopThreads / 32;
+constexpr int kPer = 4;                                  // 16-byte pieces of a round for each thread
+#ifndef TOPB
+#define TOPB 4
+#endif
+constexpr int kTopBlocks = TOPB;                         // on an SM
+constexpr int kWarpHits = 128;                           // pieces that a warp sets aside
+constexpr int kList = 1344;                              // tokens among which the K largest are found
 
-template <int kThreads>
 struct TopShared {
-  static constexpr int kWarps = kThreads / 32, kWarpHits = kHits / kWarps;
-  uint4 piece[kWarps][kWarpHits];
-  int at[kWarps][kWarpHits];
-  float tops[kThreads];
+  uint4 piece[kTopWarps][kWarpHits];
+  int at[kTopWarps][kWarpHits];
+  float tops[kTopThreads];
   uint64_t list[kList];
   uint64_t best[kMaxTop];
-  Sums part[kWarps > kMaxCluster ? kWarps : kMaxCluster];
-  int hits[kWarps];
+  Sums part[2][kTopWarps];
   unsigned count[256];           // of the digit's values, where all tokens are gone through
+  int hits[kTopWarps];
+  float bar;
   int listed, overflow;
   uint32_t digit, left;
-  float bar;
   int64_t label;
 };
+// What the first block of a cluster gets from all.
+struct TopGathered {
+  uint64_t best[kMaxCluster * kMaxTop];
+  int rank[kMaxCluster * kMaxTop];
+  Sums part[kMaxCluster];
+};
 
-// A value that K of the threads' largest values reach, or the lowest one: no more than 2^-7 of itself
-// below the K-th largest of them.  By warp 0.
-template <int kThreads>
-__device__ __forceinline__ float bar_of(const float *tops, int K) {
-  constexpr int kEach = kThreads / 32;
-  uint32_t o[kEach];
+// What a token has to reach to be one of the K largest: a value that K of the threads' largest
+// values reach, and few more.  By a warp; at least the lowest finite value.  Each of kEach values
+// of a lane stands for kTopWarps / kEach threads, the largest of theirs: the fewer, the shorter the
+// search, and the more threads reach what it finds (n ln(n / (n - K)) of n values, not K).
+template <int kEach>
+__device__ __forceinline__ float bar_among(const float *tops, int K) {
+  uint32_t o[kEach], hi = 0, lo = 0xffffu;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) o[i] = order_of(tops[lane_id() + 32 * i]) >> 16;
-  uint32_t t = 0;
-  for (int b = 15; b >= 0; --b) {
-    const uint32_t c = t | 1u << b;
-    unsigned n = 0;
+  for (int i = 0; i < kEach; ++i) {
+    float v = tops[lane_id() + 32 * i];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) n += o[i] >= c;
-    if (__reduce_add_sync(0xffffffffu, n) >= (unsigned)K) t = c;
+    for (int j = i + kEach; j < kTopWarps; j += kEach) v = fmaxf(v, tops[lane_id() + 32 * j]);
+    o[i] = order_of(v) >> 16;
+    hi = max(hi, o[i]);
+    lo = min(lo, o[i]);
   }
-  return value_of((t < 0x80u ? 0x80u : t) << 16);      // 0x80 << 16: the lowest finite value
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  const int bits = 32 - __clz(hi ^ lo);                  // all agree on the bits above these
+  uint32_t t = lo >> bits << bits;
+  for (int b = bits - 1; b >= 0; --b) {
+    const uint32_t c = t | 1u << b;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) n += __popc(__ballot_sync(0xffffffffu, o[i] >= c));
+    if (n >= K) t = c;
+    if (n >= K && n <= K + K / 8) break;
+  }
+  return value_of((t < 0x80u ? 0x80u : t) << 16);        // 0x80 << 16: the lowest finite value
+}
+__device__ __forceinline__ float bar_of(const float *tops, int K) {
+  if (K <= 16) return bar_among<1>(tops, K);
+  if (K <= 32) return bar_among<2>(tops, K);
+  if (K <= 64) return bar_among<4>(tops, K);
+  return bar_among<8>(tops, K);
 }
 
-// The K largest of n keys (the rest of them 0) into best, in order.  Returns the least
-// key that belongs to them.
-template <int kThreads>
+// The K largest of n keys into best, in order, the rest of it 0.  Returns the least key
+// that belongs to them.  Each key is compared with all by as many lanes as there are.
 __device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int K, uint64_t *best) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t key = list[i];
+  int g = 1;
+  while (g < 32 && 2 * g * n <= kTopThreads) g *= 2;
+  const int sub = threadIdx.x & (g - 1);
+  for (int from = 0; from < n; from += kTopThreads / g) {
+    const int i = from + (int)threadIdx.x / g;
+    const uint64_t key = i < n ? list[i] : 0;
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += list[j] > key;
-    if (rank < K) best[rank] = key;
+    for (int j = sub; j < n; j += g) rank += list[j] > key;
+    for (int o = g >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (sub == 0 && i < n && rank < K) best[rank] = key;
   }
-  for (int i = n + (int)threadIdx.x; i < K; i += kThreads) best[i] = 0;
+  for (int i = n + (int)threadIdx.x; i < K; i += kTopThreads) best[i] = 0;
   __syncthreads();
   return K > 0 && n >= K ? best[K - 1] : 0;
 }
@@ -189,14 +222,14 @@ __device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int K
 // The K largest of elements [e0, e1) whatever they are: digits of eight bits from the
 // highest on, the elements read again for each, then those above the K-th, and the
 // first ones that equal it.  Into list; returns how many.
-template <typename E, int kThreads>
-__device__ __noinline__ int select_all(TopShared<kThreads> &sh, const E *row, int e0, int e1, int K) {
+template <typename E>
+__device__ __noinline__ int select_all(TopShared &sh, const E *row, int e0, int e1, int K) {
   const int tid = threadIdx.x;
   uint32_t prefix = 0, left = K;      // the K-th largest's digits so far, its rank among those that share them
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kThreads) sh.count[i] = 0;
+    for (int i = tid; i < 256; i += kTopThreads) sh.count[i] = 0;
     __syncthreads();
-    for (int i = e0 + tid; i < e1; i += kThreads) {
+    for (int i = e0 + tid; i < e1; i += kTopThreads) {
       const float v = Elem<E>::load(row + i);
       const uint32_t o = order_of(v);
       if (v >= kLowest && (shift == 24 || o >> (shift + 8) == prefix >> (shift + 8)))
@@ -217,7 +250,7 @@ __device__ __noinline__ int select_all(TopShared<kThreads> &sh, const E *row, in
   }
   if (tid == 0) sh.listed = 0;
   __syncthreads();
-  for (int i = e0 + tid; i < e1; i += kThreads) {
+  for (int i = e0 + tid; i < e1; i += kTopThreads) {
     const float v = Elem<E>::load(row + i);
     if (v >= kLowest && order_of(v) > prefix) {
       const int n = atomicAdd(&sh.listed, 1);
@@ -227,7 +260,7 @@ __device__ __noinline__ int select_all(TopShared<kThreads> &sh, const E *row, in
   __syncthreads();
   int have = min(sh.listed, K);
   __syncthreads();
-  for (int from = e0; from < e1 && have < K; from += kThreads) {
+  for (int from = e0; from < e1 && have < K; from += kTopThreads) {
     const int i = from + tid;
     float v = kNegInf;
     if (i < e1) v = Elem<E>::load(row + i);
@@ -236,7 +269,7 @@ __device__ __noinline__ int select_all(TopShared<kThreads> &sh, const E *row, in
     if (lane_id() == 0) sh.hits[tid >> 5] = __popc(mask);
     __syncthreads();
     int before = have, all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kTopThreads / 32; ++w) {
       if (w < tid >> 5) before += sh.hits[w];
       all += sh.hits[w];
     }
@@ -261,235 +294,264 @@ struct TopRow {
   float2 *stats;
 };
 
-template <typename E, int kThreads>
-__global__ void __launch_bounds__(kThreads) top_kernel(TopRow a, int C, int slice) {
-  constexpr int kWarps = kThreads / 32, N = Elem<E>::kVec, U = 4;
-  using Shared = TopShared<kThreads>;
-  __shared__ Shared sh;
+// A block's slice of a row.
+template <typename E>
+struct TopSlice {
+  const E *row;
+  int head, vecs, v0, v1, rounds;
+  __device__ __forceinline__ TopSlice(const TopRow &a, int64_t t, int rank, int slice) {
+    row = static_cast<const E *>(a.logits) + t * a.ldl;
+    const RowSpan<E> sp(row, (int)a.V);
+    head = sp.head;
+    vecs = sp.vecs;
+    v0 = min(rank * slice, vecs);
+    v1 = min(v0 + slice, vecs);
+    rounds = max(1, (v1 - v0 + kPer * kTopThreads - 1) / (kPer * kTopThreads));
+  }
+  __device__ __forceinline__ const uint4 *pieces() const { return reinterpret_cast<const uint4 *>(row + head); }
+};
+
+// The results of an ignored row.
+__device__ __forceinline__ void top_nothing(const TopRow &a, int64_t t, int lane) {
+  for (int i = lane; i < a.K; i += 32) {
+    a.ids[t * a.K + i] = -1;
+    a.top[t * a.K + i] = kNegInf;
+  }
+  if (lane != 0) return;
+  if (a.logps) a.logps[t] = 0.f;
+  if (a.entropy) a.entropy[t] = 0.f;
+  if (a.rest) a.rest[t] = 0.f;
+  if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
+}
+
+template <typename E, bool kSplit>
+__global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, int clusters, int slice) {
+  constexpr int N = Elem<E>::kVec, kThreads = kTopThreads;
+  using Peak = typename Elem<E>::Peak;
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  TopShared &sh = *reinterpret_cast<TopShared *>(dynamic);
+  const int C = kSplit ? clusters : 1;
+  const int rank = (int)(blockIdx.x % C), tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, K = a.K, V = (int)a.V;
+  const float k = a.scale.k;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t = blockIdx.x / C;
-  const int rank = (int)(blockIdx.x % C), tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, K = a.K, V = (int)a.V;
   if (tid == 0) {
-    sh.label = a.labels ? a.labels[t] : 0;      // read once for the block
+    sh.label = a.labels ? a.labels[t] : 0;               // read once for the block
     sh.listed = sh.overflow = 0;
   }
   __syncthreads();
   const int64_t label = sh.label;
-  const bool counts = !a.labels || (label >= 0 && label < V);
-  const float k = a.scale.k;
-  float picked = 0.f;
-  Sums rest = no_sums();                         // of all but the block's K largest
-  if (counts) {
-    const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
-    const RowSpan<E> sp(row, V);
-    const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
-    const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
-    if (rank == 0 && tid == 0 && a.labels) picked = Elem<E>::load(row + label);
-    PairSums<E> sums;
-    float top = kNegInf, bar = INFINITY;         // a thread's largest value so far; what a token has to reach
-    int hits = 0;                                // the warp's
-    int next = 1;                                // the round before which the bar is raised again
-    const int rounds = (v1 - v0 + U * kThreads - 1) / (U * kThreads);
-    for (int n = 0; n < rounds; ++n) {
-      const int i = v0 + n * U * kThreads + tid;
-      uint4 q[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) q[u] = i + u * kThreads < v1 ? src[i + u * kThreads] : Elem<E>::lowest();
-      float g = Elem<E>::largest(q);
-      if (K > 0) {
-        top = fmaxf(top, g);
-        if (n + 1 == next) {
-          sh.tops[tid] = top;
-          __syncthreads();
-          if (warp == 0) {
-            const float b = bar_of<kThreads>(sh.tops, K);
-            if (lane == 0) sh.bar = b;
-          }
-          __syncthreads();
-          bar = sh.bar;
-          next *= 2;
-        }
-        if (__any_sync(0xffffffffu, g >= bar)) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const uint4 one[1] = {q[u]};
-            const bool hit = Elem<E>::largest(one) >= bar;
-            const unsigned mask = __ballot_sync(0xffffffffu, hit);
-            const int place = hits + __popc(mask & ((1u << lane) - 1u));
-            if (hit && place < Shared::kWarpHits) {
-              sh.piece[warp][place] = q[u];
-              sh.at[warp][place] = i + u * kThreads;
-            }
-            if (hit) q[u] = Elem<E>::lowest();
-            hits += __popc(mask);
-          }
-          g = Elem<E>::largest(q);
-        }
-      }
-      sums.add(q, g, k);
-    }
-    rest = sums.sums();
-    // the ragged ends, at most seven elements each: the first block's and the last one's
-    const bool at_head = rank == 0 && tid < sp.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
-    const int edge_at = at_head ? tid : tail + tid - 16;
-    float edge = kNegInf;
-    if (at_head || at_tail) edge = Elem<E>::load(row + edge_at);
-    if (K == 0) {
-      if (at_head || at_tail) rest.add(edge, k);
-    } else {
-      if (lane == 0) sh.hits[warp] = min(hits, Shared::kWarpHits);
-      if (hits > Shared::kWarpHits) sh.overflow = 1;
-      sh.tops[tid] = top;
-      __syncthreads();
-      if (warp == 0) {
-        const float b = bar_of<kThreads>(sh.tops, K);
-        if (lane == 0) sh.bar = b;
-      }
-      __syncthreads();
-      bar = sh.bar;
-      auto offer = [&](float v, int id) {
-        if (!(v >= bar)) return;
-        const int n = atomicAdd(&sh.listed, 1);
-        if (n < kList) sh.list[n] = key_of(v, id);
-      };
-      if (!sh.overflow) {
-        for (int j = lane; j < min(hits, Shared::kWarpHits); j += 32) {
-          float v[N];
-          Elem<E>::unpack(sh.piece[warp][j], v);
-          const int id = sp.head + sh.at[warp][j] * N;
-#pragma unroll
-          for (int e = 0; e < N; ++e) offer(v[e], id + e);
-        }
-        if (at_head || at_tail) offer(edge, edge_at);
-      }
-      __syncthreads();
-      const bool all = sh.overflow || sh.listed > kList;      // too many tokens for what was set aside
-      int n = sh.listed;
-      if (all) {
-        __syncthreads();
-        n = select_all<E, kThreads>(sh, row, rank == 0 ? 0 : sp.head + v0 * N, rank == C - 1 ? V : sp.head + v1 * N, K);
-      }
-      const uint64_t least = rank_list<kThreads>(sh.list, n, K, sh.best);
-      auto left = [&](float v, int id) {
-        if (!(v >= kLowest && key_of(v, id) >= least)) rest.add(v, k);
-      };
-      if (all) {
-        rest = no_sums();
-        for (int i = v0 + tid; i < v1; i += kThreads) {
-          float v[N];
-          Elem<E>::unpack(src[i], v);
-          for (int e = 0; e < N; ++e) left(v[e], sp.head + i * N + e);
-        }
-      } else {
-        for (int j = lane; j < min(hits, Shared::kWarpHits); j += 32) {
-          float v[N];
-          Elem<E>::unpack(sh.piece[warp][j], v);
-          const int id = sp.head + sh.at[warp][j] * N;
-#pragma unroll
-          for (int e = 0; e < N; ++e) left(v[e], id + e);
-        }
-      }
-      if (at_head || at_tail) left(edge, edge_at);
-    }
+  // A block of a cluster takes part in all that its row asks for, whatever it has seen of its label.
+  const bool live = !a.labels || (label >= 0 && label < V);
+  if (kSplit) {
+    cluster_arrive();                                    // no block is written to before it runs
+  } else if (!live) {
+    if (warp == 0) top_nothing(a, t, lane);
+    return;
   }
-  if (C > 1) {
-    // every block's K largest and sums to the first block, which finds the K largest of all
-    warp_merge(rest, k);
-    if (lane == 0) sh.part[warp] = rest;
-    __syncthreads();
-    rest = no_sums();
-    if (warp == 0) {
-      if (lane < kWarps) rest = sh.part[lane];
-      warp_merge(rest, k);
+  TopSlice<E> sl(a, t, rank, slice);
+  if (!live) sl.v1 = sl.v0;
+  const int tail = sl.head + sl.vecs * N;
+  float picked = 0.f;
+  if (live && rank == 0 && warp == 0 && a.labels) picked = Elem<E>::load(sl.row + label);
+  // the ragged ends, at most seven elements each: the first block's and the last one's
+  const bool at_head = live && rank == 0 && tid < sl.head;
+  const bool at_tail = live && rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
+  const int edge_at = at_head ? tid : tail + tid - 16;
+  float edge = kNegInf;
+  if (at_head || at_tail) edge = Elem<E>::load(sl.row + edge_at);
+  PairSums<E> sums;
+  float top = kNegInf, bar = INFINITY;                 // a thread's largest value so far; what a token has to reach
+  int hits = 0;                                        // the warp's
+  int next = 1;                                        // the round that raises the bar next
+  for (int n = 0; n < sl.rounds; ++n) {
+    const int i = sl.v0 + n * kPer * kThreads + tid;
+    uint4 q[kPer];
+    Peak peak[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      q[u] = i + u * kThreads < sl.v1 ? sl.pieces()[i + u * kThreads] : Elem<E>::lowest();
     }
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();                              // the first block has done with its list and parts
-    if (counts) {
-      uint32_t list, part;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(list) : "r"(smem_u32(sh.list + rank * K)));
-      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(part) : "r"(smem_u32(sh.part + rank)));
-      for (int i = tid; i < K; i += kThreads)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(list + 8 * i), "l"(sh.best[i]) : "memory");
-      if (tid == 0) {
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part), "f"(rest.m) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 4), "f"(rest.s) : "memory");
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 8), "f"(rest.w) : "memory");
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) peak[u] = Elem<E>::peak(q[u]);
+    auto largest = [&] {
+      return Elem<E>::value(Elem<E>::higher(Elem<E>::higher(peak[0], peak[1]), Elem<E>::higher(peak[2], peak[3])));
+    };
+    float g = largest();
+    if (K > 0) {
+      top = fmaxf(top, g);
+      if (n + 1 == next || n + 1 == sl.rounds) {
+        sh.tops[tid] = top;
+        __syncthreads();
+        if (warp == 0) {
+          const float b = bar_of(sh.tops, K);
+          if (lane == 0) sh.bar = b;
+        }
+        __syncthreads();
+        bar = sh.bar;
+        next *= K > 32 ? 2 : 4;
+      }
+      if (__any_sync(0xffffffffu, g >= bar)) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const bool hit = Elem<E>::value(peak[u]) >= bar;
+          const unsigned mask = __ballot_sync(0xffffffffu, hit);
+          if (mask == 0) continue;
+          const int place = hits + __popc(mask & ((1u << lane) - 1u));
+          hits += __popc(mask);
+          if (!hit) continue;
+          if (place < kWarpHits) {
+            sh.piece[warp][place] = q[u];
+            sh.at[warp][place] = i + u * kThreads;
+          }
+          q[u] = Elem<E>::lowest();
+          peak[u] = Elem<E>::no_peak();
+        }
+        g = largest();
       }
     }
+    sums.add(q, g, k);
+  }
+  Sums rest = sums.sums();                             // of all but the block's K largest
+  if (K == 0) {
+    if (at_head || at_tail) rest.add(edge, k);
+  } else {
+    if (lane == 0 && hits > kWarpHits) sh.overflow = 1;
+    hits = min(hits, kWarpHits);
+    // the last round has left the bar at the K-th largest value, or little below it
+    auto offer = [&](float v, int id) {
+      if (!(v >= bar)) return;
+      const int n = atomicAdd(&sh.listed, 1);
+      if (n < kList) sh.list[n] = key_of(v, id);
+    };
+    __syncwarp();
+    for (int j = lane; j < hits; j += 32) {
+      float v[N];
+      Elem<E>::unpack(sh.piece[warp][j], v);
+      const int id = sl.head + sh.at[warp][j] * N;
+#pragma unroll
+      for (int e = 0; e < N; ++e) offer(v[e], id + e);
+    }
+    if (at_head || at_tail) offer(edge, edge_at);
+    __syncthreads();
+    int n = sh.listed;
+    const bool all = sh.overflow || n > kList;         // more tokens than can be set aside
+    if (all) {
+      __syncthreads();
+      n = select_all<E>(sh, sl.row, rank == 0 ? 0 : sl.head + sl.v0 * N, rank == C - 1 ? V : sl.head + sl.v1 * N, K);
+    }
+    const uint64_t least = rank_list(sh.list, n, K, sh.best);
+    if (tid == 0) sh.listed = sh.overflow = 0;
+    auto left = [&](float v, int id) {
+      if (!(v >= kLowest && key_of(v, id) >= least)) rest.add(v, k);
+    };
+    if (all) {
+      rest = no_sums();
+      for (int i = sl.v0 + tid; i < sl.v1; i += kThreads) {
+        float v[N];
+        Elem<E>::unpack(sl.pieces()[i], v);
+        for (int e = 0; e < N; ++e) left(v[e], sl.head + i * N + e);
+      }
+    } else {
+      for (int j = lane; j < hits; j += 32) {
+        float v[N];
+        Elem<E>::unpack(sh.piece[warp][j], v);
+        const int id = sl.head + sh.at[warp][j] * N;
+#pragma unroll
+        for (int e = 0; e < N; ++e) left(v[e], id + e);
+      }
+    }
+    if (at_head || at_tail) left(edge, edge_at);
+  }
+  warp_merge(rest, k);
+  if (lane == 0) sh.part[0][warp] = rest;
+  __syncthreads();
+  rest = no_sums();
+  if (warp == 0) {
+    if (lane < kTopWarps) rest = sh.part[0][lane];
+    warp_merge(rest, k);
+  }
+  if (kSplit) {
+    // every block's K largest and sums to the first block, which finds the K largest of all
+    TopGathered &all = *reinterpret_cast<TopGathered *>(dynamic + sizeof(TopShared));
+    __syncwarp();
+    cluster_wait();
+    uint32_t to, part;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(all.best + rank * K)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(part) : "r"(smem_u32(all.part + rank)));
+    for (int i = tid; i < K; i += kThreads)
+      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8 * i), "l"(sh.best[i]) : "memory");
+    if (tid == 0) {
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part), "f"(rest.m) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 4), "f"(rest.s) : "memory");
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 8), "f"(rest.w) : "memory");
+    }
+    if (rank == 0)
+      for (int i = tid; i < C * K; i += kThreads) all.rank[i] = i % K;
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    if (rank != 0) return;                       // nothing is sent from here on
-    rest = no_sums();
-    if (counts) {
+    if (rank != 0) return;                               // nothing is sent from here on
+    {
+      rest = no_sums();
+      // a token's rank: its place in its own list, and those above it in each of the others
+      for (int i = tid; i < C * C * K; i += kThreads) {
+        const int c = i / (C * K), own = i - c * (C * K);
+        const uint64_t key = all.best[own];
+        if (key == 0 || own / K == c) continue;
+        const uint64_t *list = all.best + c * K;
+        int lo = 0, hi = K;                            // those before lo are above, those from hi on are not
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (list[mid] > key) lo = mid + 1; else hi = mid;
+        }
+        if (lo > 0) atomicAdd(&all.rank[own], lo);
+      }
       for (int i = tid; i < K; i += kThreads) sh.best[i] = 0;
       __syncthreads();
-      // a token's rank: its place in its own list, and those above it in each of the others
       for (int i = tid; i < C * K; i += kThreads) {
-        const uint64_t key = sh.list[i];
+        const uint64_t key = all.best[i];
         if (key == 0) continue;
-        const int own = i / K;
-        int above = i - own * K;
-        for (int c = 0; c < C; ++c) {
-          if (c == own) continue;
-          int lo = 0, hi = K;                    // those before lo are above, those from hi on are not
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (sh.list[c * K + mid] > key) lo = mid + 1; else hi = mid;
-          }
-          above += lo;
-        }
-        if (above < K) sh.best[above] = key; else rest.add(key_value(key), k);
+        if (all.rank[i] < K) sh.best[all.rank[i]] = key; else rest.add(key_value(key), k);
       }
-      if (tid < C) rest.add(sh.part[tid], k);
+      if (tid < C) rest.add(all.part[tid], k);
+      warp_merge(rest, k);
+      if (lane == 0) sh.part[1][warp] = rest;
+      __syncthreads();
+      rest = no_sums();
+      if (warp == 0) {
+        if (lane < kTopWarps) rest = sh.part[1][lane];
+        warp_merge(rest, k);
+      }
     }
-    __syncthreads();
   }
-  warp_merge(rest, k);
-  if (lane == 0) sh.part[warp] = rest;
-  __syncthreads();
-  if (warp != 0) return;
-  rest = no_sums();
-  if (lane < kWarps) rest = sh.part[lane];
-  warp_merge(rest, k);
-  if (!counts) {
+  if (warp == 0 && rank == 0 && !live) top_nothing(a, t, lane);
+  if (warp == 0 && rank == 0 && live) {
+    Sums total = no_sums();                            // of the K largest
+    for (int i = lane; i < K; i += 32)
+      if (sh.best[i]) total.add(key_value(sh.best[i]), k);
+    warp_merge(total, k);
+    const float listed = total.s, listed_m = total.m;
+    total.add(rest, k);
+    const bool fine = total.s > 0.f && total.s < INFINITY;
+    const float log_s = fine ? logf(total.s) : NAN, m = total.m;
     for (int i = lane; i < K; i += 32) {
-      a.ids[t * K + i] = -1;
-      a.top[t * K + i] = kNegInf;
+      const uint64_t key = sh.best[i];
+      a.ids[t * K + i] = key && fine ? key_id(key) : -1;
+      a.top[t * K + i] = !fine ? NAN : key ? a.scale.gap(key_value(key), m) - log_s : kNegInf;
     }
     if (lane == 0) {
-      if (a.logps) a.logps[t] = 0.f;
-      if (a.entropy) a.entropy[t] = 0.f;
-      if (a.rest) a.rest[t] = 0.f;
-      if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
+      if (a.logps) a.logps[t] = a.scale.gap(picked, m) - log_s;
+      if (a.entropy) a.entropy[t] = log_s - total.w * kLn2 / total.s;
+      if (a.rest) {
+        // ln of rest / (rest + listed), without the two large logarithms where that is more than nothing
+        const float ratio = listed * ex2((listed_m - ref_of(rest.m)) * k) / rest.s;
+        a.rest[t] = !fine ? NAN : !(rest.s > 0.f) ? kNegInf
+                    : ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(rest.m, m) + logf(rest.s) - log_s;
+      }
+      if (a.stats) a.stats[t] = make_float2(m, total.s);
     }
-    return;
-  }
-  Sums total = no_sums();                        // of the K largest
-  for (int i = lane; i < K; i += 32)
-    if (sh.best[i]) total.add(key_value(sh.best[i]), k);
-  warp_merge(total, k);
-  const float listed = total.s, listed_m = total.m;
-  total.add(rest, k);
-  const bool fine = total.s > 0.f && total.s < INFINITY;
-  const float log_s = fine ? logf(total.s) : NAN, m = total.m;
-  for (int i = lane; i < K; i += 32) {
-    const uint64_t key = sh.best[i];
-    a.ids[t * K + i] = key && fine ? key_id(key) : -1;
-    a.top[t * K + i] = !fine ? NAN : key ? a.scale.gap(key_value(key), m) - log_s : kNegInf;
-  }
-  if (lane == 0) {
-    if (a.logps) a.logps[t] = a.scale.gap(picked, m) - log_s;
-    if (a.entropy) a.entropy[t] = log_s - total.w * kLn2 / total.s;
-    if (a.rest) {
-      // ln of rest / (rest + listed), without the two large logarithms where that is more than nothing
-      const float ratio = listed * ex2((listed_m - ref_of(rest.m)) * k) / rest.s;
-      a.rest[t] = !fine ? NAN : !(rest.s > 0.f) ? kNegInf
-                  : ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(rest.m, m) + logf(rest.s) - log_s;
-    }
-    if (a.stats) a.stats[t] = make_float2(m, total.s);
   }
 }
 
@@ -637,15 +699,22 @@ TopRow row_of(const TopArgs &a) {
   return r;
 }
 
+template <typename E, bool kSplit>
+cudaError_t launch_top_as(const TopRow &r, int C, int slice, cudaStream_t st) {
+  constexpr size_t smem = sizeof(TopShared) + (kSplit ? sizeof(TopGathered) : 0);
+  cudaError_t e = ensure_smem(reinterpret_cast<const void *>(top_kernel<E, kSplit>), smem);
+  if (e != cudaSuccess) return e;
+  return launch(top_kernel<E, kSplit>, dim3((unsigned)(r.T * C)), dim3(kTopThreads), smem, st, C, true, r, C, slice);
+}
+
 template <typename E>
 cudaError_t launch_top(const TopRow &r, int64_t bytes, cudaStream_t st) {
   const int64_t sms = num_sms();
-  if (2 * r.T < sms) {
-    const int c = (int)std::min<int64_t>({std::max<int64_t>(1, 4 * sms / r.T), std::max<int64_t>(1, bytes / (4 << 10)),
-                                          kMaxCluster});
-    return launch(top_kernel<E, 256>, dim3((unsigned)(r.T * c)), dim3(256), 0, st, c, true, r, c, slice_of(bytes, c));
+  if (2 * r.T < sms && bytes > 16 << 10) {
+    const int c = (int)std::min<int64_t>({4 * sms / r.T, bytes / (4 << 10), kMaxCluster});
+    return launch_top_as<E, true>(r, c, slice_of(bytes, c), st);
   }
-  return launch(top_kernel<E, 256>, dim3((unsigned)r.T), dim3(256), 0, st, 1, true, r, 1, slice_of(bytes, 1));
+  return launch_top_as<E, false>(r, 1, slice_of(bytes, 1), st);
 }
 
 // Blocks for each row of the gradient pass, as for the gradient of label log-probabilities.
