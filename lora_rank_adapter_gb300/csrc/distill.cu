@@ -10,9 +10,17 @@
 //              p_v (a_v + 1 - L - P) and outside the list -p_v (L + P) without;  P = sum p_j
 // So whatever the form, a token outside the list has f exp(z_v), one f for its row, and
 // at most LORA_TOP_MAX tokens have a value of their own.
+//
+// Bytes decide: a row is read once and its gradient written once, with two exponentials
+// and some twelve operations an element.
+//   short_kernel    rows of up to 32 KB, held in registers;
+//   held_kernel     longer ones, held in the shared memory of a cluster;
+//   row_kernel      without a gradient, and rows that no cluster holds: these are read twice;
+//   loss_kernel     the weighted sum over the rows.
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -42,57 +50,115 @@ struct Distill {
   float grad_scale;
 };
 
+// ----------------------------------------------------------------------------- a row's record
+// The listed tokens over the lanes of a warp: place i of lane l is entry i * 32 + l.  id -1:
+// no token (out of range, or listed before).
+struct Record {
+  int id[kEach];
+  float z[kEach], lnq[kEach];      // the student's logit, the teacher's log-probability
+};
+
 __device__ __forceinline__ float warp_sum_f(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 
-// A row's record, the listed tokens over the lanes of a warp: place i of lane l is
-// entry i * 32 + l.  id -1: no token (out of range, or listed before).
-struct Record {
-  int id[kEach];
-  float z[kEach], lnq[kEach];      // the student's logit, the teacher's log-probability
-};
+// A row's ids as a warp reads them; true if any is a token.
+__device__ __forceinline__ bool read_ids(const Distill &a, int64_t t, Record &r) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = i * 32 + lane_id();
+    const int64_t id = j < a.K ? a.ids[t * a.K + j] : -1;
+    r.id[i] = id >= 0 && id < a.V ? (int)id : -1;
+    any = any || r.id[i] >= 0;
+  }
+  return __any_sync(0xffffffffu, any);
+}
+template <typename E>
+__device__ __forceinline__ void read_values(const Distill &a, int64_t t, const E *row, Record &r) {
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    r.z[i] = r.lnq[i] = 0.f;
+    if (r.id[i] < 0) continue;
+    r.z[i] = Elem<E>::load(row + r.id[i]);
+    r.lnq[i] = a.teacher[t * a.K + i * 32 + lane_id()];
+  }
+}
+// Entries that name a token listed before them are dropped.  `scratch`: kMaxTop ints.  By a warp.
+__device__ __forceinline__ void drop_repeated(Record &r, int K, int *scratch) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) scratch[i * 32 + lane] = r.id[i];
+  __syncwarp();
+  for (int j = 0; j < K; ++j) {
+    const int other = scratch[j];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (j < i * 32 + lane && r.id[i] == other) r.id[i] = -1;
+  }
+  __syncwarp();
+}
+
+// ln S in two parts, the first one exact: S = 2^n f, ln 2 split as by Cody and Waite
+// ("Software Manual for the Elementary Functions", 1980).
+__device__ __forceinline__ float2 log_parts(float S) {
+  const uint32_t bits = __float_as_uint(S);
+  float n = (float)((int)(bits >> 23) - 127), f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+  if (f > 1.41421356f) {
+    f *= 0.5f;
+    n += 1.f;
+  }
+  return make_float2(n * 0.693359375f, fmaf(n, -2.12194440054690583e-4f, logf(f)));
+}
 
 // What a row's loss and gradient come to, by a warp, from the sums over the tokens that
 // are not listed (m, s).  dz: c times the listed tokens' gradient; f: what exp((x - m) k)
-// of all others is multiplied by.
+// of all others is multiplied by.  Differences of logarithms come to 2^-24 of themselves:
+// the loss of a student near its teacher is a sum of small ones.
 struct RowTerms {
   float loss, f;
   float dz[kEach];
 };
 __device__ __forceinline__ RowTerms row_terms(const Distill &a, const Record &r, float ln_qr, float m, float s, float c) {
-  const float k = a.scale.k;
   float top = kNegInf;
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
     if (r.id[i] >= 0) top = fmaxf(top, r.z[i]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float M = fmaxf(top, m), ref = ref_of(M);
+  float M;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(top));
+  M = fmaxf(M, m);
+  const float ref = ref_of(M);
+  float2 g[kEach];
   float e[kEach], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    e[i] = r.id[i] >= 0 ? ex2((r.z[i] - ref) * k) : 0.f;
+    e[i] = 0.f;
+    if (i * 32 >= a.K) continue;
+    g[i] = a.scale.gap2(r.z[i], ref);
+    if (r.id[i] >= 0) e[i] = expf(g[i].x + g[i].y);
     sum += e[i];
   }
-  const float rest = s * ex2((m - ref) * k), S = warp_sum_f(sum) + rest, ln_S = logf(S);
-  const float p_r = rest / S, ln_pr = a.scale.gap(m, ref) + logf(s) - ln_S;
+  sum = warp_sum_f(sum);
+  const float rest = s * expf(a.scale.gap(m, ref)), S = sum + rest, over = 1.f / S;
+  const float2 ln_S = log_parts(S);
+  const float p_r = rest * over;
+  const float ratio = sum / rest;
+  const float ln_pr = ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(m, ref) + logf(s) - (ln_S.x + ln_S.y);
   float L = 0.f, Q = 0.f, P = 0.f, p[kEach], q[kEach], gap[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const bool there = r.id[i] >= 0;
-    p[i] = e[i] / S;
-    q[i] = there ? expf(r.lnq[i]) : 0.f;
-    gap[i] = a.scale.gap(r.z[i], ref) - ln_S - r.lnq[i];
-    if (!there) {
-      p[i] = gap[i] = 0.f;
-    } else if (a.reverse) {
+    p[i] = q[i] = gap[i] = 0.f;
+    if (i * 32 >= a.K || r.id[i] < 0) continue;
+    p[i] = e[i] * over;
+    gap[i] = (g[i].x - ln_S.x) - r.lnq[i] + (g[i].y - ln_S.y);
+    if (a.reverse) {
       if (p[i] == 0.f) gap[i] = 0.f;      // no 0 * infinity
       L += p[i] * gap[i];
       P += p[i];
     } else {
+      q[i] = expf(r.lnq[i]);
       if (q[i] != 0.f) L -= q[i] * gap[i];
       Q += q[i];
     }
@@ -123,16 +189,477 @@ __device__ __forceinline__ RowTerms row_terms(const Distill &a, const Record &r,
   RowTerms t;
   t.loss = L;
   t.f = s == 0.f ? 0.f : c * F / s;      // s is 0: nothing outside the list has any probability
-  if (!(S > 0.f)) t.f = NAN;             // nor inside: no distribution
+  if (!(S > 0.f)) t.loss = t.f = NAN;    // nor inside: no distribution
 #pragma unroll
   for (int i = 0; i < kEach; ++i) t.dz[i] = c * (a.reverse ? p[i] * (gap[i] + 1.f - L - P) : p[i] * Q - q[i]);
   return t;
 }
 
+// U 16-byte pieces into a running maximum and a pair of partial sums, as absorb() does, with
+// the temperature in both its parts: at a rounded one, ln S would be off by the same in every
+// row, and so would be the loss.
+template <typename E, int U>
+__device__ __forceinline__ void absorb_exact(float &m, uint64_t &s, const uint4 (&q)[U], const Scale &c) {
+  const float mm = fmaxf(m, Elem<E>::largest(q)), r = ref_of(mm), f = ex2(c.two(m - r));
+  const uint64_t r2 = pk2(-r, -r), k2 = pk2(c.k, c.k), l2 = pk2(c.k_lo, c.k_lo);
+  m = mm;
+  s = mul2(s, pk2(f, f));
+  uint64_t t = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint64_t v[Elem<E>::kVec / 2];
+    Elem<E>::pairs(q[u], v);
+#pragma unroll
+    for (int j = 0; j < Elem<E>::kVec / 2; ++j) {
+      const uint64_t d = add2(v[j], r2), e = ex2_2(fma2(d, k2, mul2(d, l2)));
+      if (j & 1) t = add2(t, e); else s = add2(s, e);
+    }
+  }
+  s = add2(s, t);
+}
+
+__device__ __forceinline__ void absorb_exact(float &m, float &s, float v, const Scale &c) {
+  const float mm = fmaxf(m, v), r = ref_of(mm);
+  s = s * ex2(c.two(m - r)) + ex2(c.two(v - r));
+  m = mm;
+}
+// (m, s) of the warp's lanes.
+__device__ __forceinline__ void merge_exact(float &m, float &s, const Scale &c) {
+  float mm;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(mm) : "f"(m));
+  s *= ex2(c.two(m - ref_of(mm)));
+  m = mm;
+  s = warp_sum_f(s);
+}
+
+// ----------------------------------------------------------------------------- short rows
+// A row of some KB in the registers of one warp, or of four that make up a block.  Which of a
+// piece's elements are listed is a set of bits in shared memory, one for each element.
+template <typename E, int kPieces, int kTeam>
+__global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Distill a) {
+  constexpr int kLanes = 32 * kTeam, kRows = kTeam == 1 ? 8 : 1, N = Elem<E>::kVec;
+  constexpr int kWords = kPieces * kTeam * N;            // of 32 elements
+  __shared__ uint32_t bits[kRows][kWords];
+  __shared__ unsigned edge_bits[kRows];
+  __shared__ int scratch[kRows * kTeam][kMaxTop];
+  __shared__ float2 sh[kTeam];
+  auto sync = [] { if (kTeam == 1) __syncwarp(); else __syncthreads(); };
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t t = blockIdx.x * (int64_t)kRows + threadIdx.x / kLanes;
+  if (t >= a.T) return;                                  // whole teams
+  const int tid = threadIdx.x % kLanes, lane = lane_id(), warp = threadIdx.x >> 5, V = (int)a.V;
+  const int mine = threadIdx.x / kLanes;                 // the team
+  E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
+  const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
+  const RowSpan<E> sp(row, V);
+  for (int i = tid; i < kWords; i += kLanes) bits[mine][i] = 0;
+  if (tid == 0) edge_bits[mine] = 0;
+  Record r;
+  const float w = a.weights ? a.weights[t] : 1.f;
+  bool counts = read_ids(a, t, r) && w != 0.f;
+  if (kTeam > 1) counts = __syncthreads_and(counts);     // the same for all
+  sync();
+  if (!counts) {
+    if (tid == 0) a.row_loss[t] = 0.f;
+    if (a.dlogits) zero_span<E, kLanes>(out, 0, V, tid);
+    return;
+  }
+  const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
+  uint4 q[kPieces];
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) q[u] = tid + u * kLanes < sp.vecs ? src[tid + u * kLanes] : Elem<E>::lowest();
+  const int tail = sp.tail();
+  const bool at_head = tid < sp.head, at_tail = tid >= 16 && tid - 16 < V - tail;
+  const int edge_at = at_head ? tid : tail + tid - 16;
+  float edge = kNegInf;
+  if (at_head || at_tail) edge = Elem<E>::load(row + edge_at);
+  read_values(a, t, row, r);
+  const float ln_qr = a.rest ? a.rest[t] : 0.f;
+  // the bits, by the first warp; a bit that was set already is a token listed twice
+  if (warp % kTeam == 0) {
+    bool twice = false;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int id = r.id[i];
+      if (id < 0) continue;
+      if (id >= sp.head && id < tail) {
+        const int b = id - sp.head;
+        twice = twice || (atomicOr(&bits[mine][b >> 5], 1u << (b & 31)) >> (b & 31) & 1u);
+      } else {
+        const int b = id < sp.head ? id : 16 + id - tail;
+        twice = twice || (atomicOr(&edge_bits[mine], 1u << b) >> b & 1u);
+      }
+    }
+    twice = __any_sync(0xffffffffu, twice);
+    if (kTeam > 1 && lane == 0) sh[0].x = twice ? 1.f : 0.f;
+    if (kTeam == 1 && twice) drop_repeated(r, a.K, scratch[warp]);
+  }
+  sync();
+  if (kTeam > 1) {
+    if (sh[0].x != 0.f) drop_repeated(r, a.K, scratch[warp]);
+    __syncthreads();
+  }
+  float m = kNegInf;
+  uint64_t s2 = 0;
+  constexpr int U = kPieces < 4 ? kPieces : 4;
+#pragma unroll
+  for (int u = 0; u < kPieces; u += U) {
+    if (u * kLanes >= sp.vecs) break;
+    uint4 some[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int piece = tid + (u + i) * kLanes;
+      const uint32_t set = bits[mine][piece * N / 32] >> (piece * N % 32) & ((1u << N) - 1u);
+      if (set)
+#pragma unroll
+        for (int x = 0; x < N; ++x)
+          if (set >> x & 1u) Elem<E>::strike(q[u + i], x);
+      some[i] = q[u + i];
+    }
+    absorb_exact<E, U>(m, s2, some, a.scale);
+  }
+  const float2 both = unpk2(s2);
+  float s = both.x + both.y;
+  if ((at_head || at_tail) && edge_bits[mine] >> tid & 1u) edge = kNegInf;
+  const float k = a.scale.k;
+  if (edge != kNegInf) absorb_exact(m, s, edge, a.scale);
+  merge_exact(m, s, a.scale);
+  // past this point the gradient may replace the row: all reads of it come before
+  if (kTeam == 1) __syncwarp();
+  if (kTeam > 1) {
+    if (lane == 0) sh[warp] = make_float2(m, s);
+    __syncthreads();
+    const float2 v = lane < kTeam ? sh[lane % kTeam] : make_float2(kNegInf, 0.f);
+    m = v.x;
+    s = v.y;
+    merge_exact(m, s, a.scale);
+  }
+  const RowTerms x = row_terms(a, r, ln_qr, m, s, w * a.grad_scale * a.scale.hi);
+  if (tid == 0) a.row_loss[t] = x.loss;
+  if (a.dlogits == nullptr) return;
+  const RowGrad g = {ref_of(m), k, 0.f, x.f};
+  const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int i = tid + u * kLanes;
+    if (i >= sp.vecs) break;
+    q[u] = g.piece<E>(q[u]);
+    E *to = out + sp.head + i * N;
+    if (same) {
+      __stcs(reinterpret_cast<uint4 *>(to), q[u]);
+    } else {
+      const E *e = reinterpret_cast<const E *>(&q[u]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) to[j] = e[j];
+    }
+  }
+  if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge));
+  sync();                                                // the listed tokens' places come after the pieces
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (r.id[i] >= 0 && i % kTeam == warp % kTeam) Elem<E>::store(out + r.id[i], x.dz[i]);
+}
+
+// ----------------------------------------------------------------------------- rows held on chip
+// One row is read once: the C blocks of a cluster take a slice each and hold it in shared memory
+// until all of the row's sums are known; its gradient is formed from what they hold.  The clusters
+// stay for row after row.  A loader warp copies slices, chunk by chunk, through a ring of slots
+// that are free again when their chunk's gradient has been formed.  Another warp goes ahead and
+// makes up the rows' records.  The working warps go through the rows without a barrier of the
+// block: each strikes the listed tokens out of its pieces, sends its sums over the rest to every
+// block of the cluster, waits for all of them, and works out the row's terms by itself.
+constexpr int kWorkers = 8;                              // warps that sum and write
+constexpr int kWork = 32 * kWorkers;
+constexpr int kHeldThreads = kWork + 64;                 // and the loader's warp, and the records'
+constexpr int kPer = 4;                                  // 16-byte pieces of a chunk for each thread
+constexpr int kChunk = kPer * kWork;
+constexpr int kSlots = 6;                                // 96 KB: two blocks on an SM
+constexpr int kHeldBlocks = 2;
+constexpr int kSliceBytes = 64 << 10;                    // of a row for a block, where eight blocks suffice
+constexpr int kHeldSmem = kSlots * kChunk * 16;
+constexpr int kAhead = 4;                                // records made up ahead
+
+struct HeldDistill {
+  Distill a;
+  int cluster, slice;      // slice: 16-byte pieces of a block at most, up to kSlots chunks
+};
+
+struct HeldRecord {
+  int id[kMaxTop];
+  float z[kMaxTop], lnq[kMaxTop];
+  float w, ln_qr;
+  int counts;
+};
+
+// A block's slice of a row.
+template <typename E>
+struct Slice {
+  const E *row;
+  int head, vecs, v0, nv;
+  __device__ __forceinline__ Slice(const HeldDistill &h, int64_t t, int rank) {
+    row = static_cast<const E *>(h.a.logits) + t * h.a.ldl;
+    const RowSpan<E> sp(row, (int)h.a.V);
+    head = sp.head;
+    vecs = sp.vecs;
+    v0 = min(rank * h.slice, vecs);
+    nv = min(v0 + h.slice, vecs) - v0;
+  }
+};
+
+// A place in a ring of n: its slot, and the parity of the slot's phase.
+template <int n>
+struct At {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == n) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+template <typename E>
+__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDistill h) {
+  extern __shared__ __align__(128) uint4 ring[];
+  __shared__ HeldRecord records[kAhead];
+  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], ready[2], step, done;
+  __shared__ float2 pairs[2][kMaxCluster * kWorkers];    // (m, s) of every warp of the cluster, two exchanges
+  const Distill &a = h.a;
+  constexpr int N = Elem<E>::kVec;
+  const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, C = h.cluster, V = (int)a.V;
+  const int rank = (int)(blockIdx.x % C);
+  const int64_t clusters = gridDim.x / C;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kWorkers);
+    }
+    for (int i = 0; i < kAhead; ++i) {
+      mbar_init(&made[i], 1);
+      mbar_init(&read[i], kWorkers + 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C == 1 ? kWorkers : 1);
+    mbar_init(&step, kWorkers);
+    mbar_init(&done, C * kWorkers);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  if (C > 1) {                                           // every block's barriers stand before any is written to
+    cluster_arrive();
+    cluster_wait();
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  int64_t t = blockIdx.x / C;
+  At<kAhead> rec;
+
+  if (warp == kWorkers + 1) {                            // the records
+    for (int64_t row_no = 0; t < a.T; t += clusters, ++row_no, rec.next()) {
+      Record r;
+      const float w = a.weights ? a.weights[t] : 1.f;
+      const bool counts = read_ids(a, t, r) && w != 0.f;
+      if (counts) read_values(a, t, static_cast<const E *>(a.logits) + t * a.ldl, r);
+      const float ln_qr = a.rest ? a.rest[t] : 0.f;
+      if (!__all_sync(0xffffffffu, row_no < kAhead || mbar_wait(&read[rec.slot], rec.parity ^ 1))) break;
+      HeldRecord &to = records[rec.slot];
+      if (counts) drop_repeated(r, a.K, to.id);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        to.id[i * 32 + lane] = r.id[i];
+        to.z[i * 32 + lane] = r.z[i];
+        to.lnq[i * 32 + lane] = r.lnq[i];
+      }
+      if (lane == 0) {
+        to.w = w;
+        to.ln_qr = ln_qr;
+        to.counts = counts;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&made[rec.slot]);
+    }
+    return;
+  }
+
+  At<kSlots> at;
+  if (warp == kWorkers) {                                // the loader
+    if (lane != 0) return;
+    bool ok = true, again = false;                       // again: the ring has been filled once
+    for (; t < a.T && ok; t += clusters, rec.next()) {
+      ok = mbar_wait(&made[rec.slot], rec.parity);
+      if (!ok) break;
+      const bool counts = records[rec.slot].counts != 0;
+      mbar_arrive(&read[rec.slot]);
+      if (!counts) continue;
+      const Slice<E> sl(h, t, rank);
+      const uint4 *src = reinterpret_cast<const uint4 *>(sl.row + sl.head) + sl.v0;
+      for (int from = 0; from < sl.nv && ok; from += kChunk) {
+        const uint32_t bytes = (uint32_t)min(kChunk, sl.nv - from) * 16;
+        ok = !again || mbar_wait(&empty[at.slot], at.parity ^ 1);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&full[at.slot], bytes);
+        bulk_load(ring + at.slot * kChunk, src + from, bytes, &full[at.slot]);
+        at.next();
+        again = again || at.parity;
+      }
+    }
+    // The last copies land before the block ends, whoever else waits for them.
+    for (int i = 0; i < kSlots; ++i)
+      if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
+    // And the block does not end before every warp of the cluster has sent its last pair here, also
+    // where a wait ran out: for as many limits as may lie ahead of a warp, whose rows in the ring are
+    // kSlots at most, of kSlots chunks, a record, an exchange and two steps each, and whose records
+    // may be kAhead rows further.
+    if (C > 1)
+      for (int i = 0; i < (kSlots + kAhead) * (kSlots + 4) && !mbar_wait<true>(&done, 0); ++i) {}
+    return;
+  }
+
+  uint32_t count = 0, steps = 0;                         // exchanges, and steps of the block, so far
+  const float k = a.scale.k;
+  for (; t < a.T; t += clusters, rec.next()) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&made[rec.slot], rec.parity))) break;
+    const HeldRecord &of = records[rec.slot];
+    const Slice<E> sl(h, t, rank);
+    E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
+    const int nv = sl.nv, tail = sl.head + sl.vecs * N, first = sl.head + sl.v0 * N;
+    const bool counts = of.counts != 0;
+    const float w = of.w, ln_qr = of.ln_qr;
+    Record r;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      r.id[i] = of.id[i * 32 + lane];
+      r.z[i] = of.z[i * 32 + lane];
+      r.lnq[i] = of.lnq[i * 32 + lane];
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&read[rec.slot]);
+    if (!counts) {
+      if (rank == 0 && tid == 0) a.row_loss[t] = 0.f;
+      zero_span<E, kWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N, tid);
+      continue;
+    }
+    // where in the ring an entry is, if it is in one of this warp's pieces: its element from the slice's start
+    int place[kEach];
+    bool edges = false;                                  // one of them is among the ragged ends
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = r.id[i] - first;
+      place[i] = r.id[i] >= 0 && e >= 0 && e < nv * N && e / N % kWork / 32 == warp ? e : -1;
+      edges = edges || (r.id[i] >= 0 && (r.id[i] < sl.head || r.id[i] >= tail));
+    }
+    // the ragged ends, at most seven elements each: the first block's and the last one's, by warp 0
+    const bool at_head = rank == 0 && tid < sl.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
+    const int edge_at = at_head ? tid : tail + tid - 16;
+    float edge = kNegInf;
+    if (at_head || at_tail) edge = Elem<E>::load(sl.row + edge_at);
+    if (warp == 0 && __any_sync(0xffffffffu, edges))
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        for (int l = 0; l < 32; ++l)
+          if (__shfl_sync(0xffffffffu, r.id[i], l) == edge_at) edge = kNegInf;
+
+    float m = kNegInf;
+    uint64_t s2 = 0;
+    At<kSlots> here = at;
+    bool ok = true;
+    for (int from = 0; from < nv; from += kChunk, here.next()) {
+      ok = mbar_wait(&full[here.slot], here.parity) && ok;
+      uint4 *slot = ring + here.slot * kChunk;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (place[i] >= from * N && place[i] < (from + kChunk) * N)
+          Elem<E>::store(reinterpret_cast<E *>(slot) + (place[i] - from * N), kNegInf);
+      __syncwarp();
+      const int n = min(kChunk, nv - from);
+      uint4 q[kPer];
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) q[u] = tid + u * kWork < n ? slot[tid + u * kWork] : Elem<E>::lowest();
+      absorb_exact<E, kPer>(m, s2, q, a.scale);
+    }
+    const float2 both = unpk2(s2);
+    float s = both.x + both.y;
+    if (edge != kNegInf) absorb_exact(m, s, edge, a.scale);
+    merge_exact(m, s, a.scale);
+    const uint32_t set = count & 1;
+    // In a cluster the pair's own bytes complete the others' barriers: an arrival with release
+    // semantics there would first wait for the last row's gradient to reach memory.  What this
+    // block has read of the row is in the pair, or was in the record before.
+    if (C == 1) {
+      __syncwarp();                                      // every lane's reads of the row come before the arrival
+      if (lane == 0) {
+        pairs[set][warp] = make_float2(m, s);
+        mbar_arrive(&ready[set]);
+      }
+    } else {
+      if (tid == 0) mbar_arrive_expect_tx(&ready[set], C * kWorkers * 8);
+      if (lane < C) st_async_f2(&pairs[set][rank * kWorkers + warp], &ready[set], lane, make_float2(m, s));
+    }
+    ok = mbar_wait<true>(&ready[set], (count >> 1) & 1) && ok;
+    if (!__all_sync(0xffffffffu, ok)) break;             // a wait ran out: the error word is set
+    ++count;
+    m = kNegInf;
+    s = 0.f;
+    for (int i = lane; i < C * kWorkers; i += 32) {
+      const float2 v = pairs[set][i];
+      const float mm = fmaxf(m, v.x), ref = ref_of(mm);
+      s = s * ex2(a.scale.two(m - ref)) + v.y * ex2(a.scale.two(v.x - ref));
+      m = mm;
+    }
+    merge_exact(m, s, a.scale);
+    const RowTerms x = row_terms(a, r, ln_qr, m, s, w * a.grad_scale * a.scale.hi);
+    if (rank == 0 && tid == 0) a.row_loss[t] = x.loss;
+    const RowGrad g = {ref_of(m), k, 0.f, x.f};
+    const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0;
+    // Where the gradient's rows sit at other offsets, warps write each other's elements: all have struck
+    // theirs out before, and the listed tokens' places come after all have written.
+    auto all_here = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&step);
+      const bool met = mbar_wait(&step, steps & 1);
+      ++steps;
+      return __all_sync(0xffffffffu, met);
+    };
+    if (!same && !all_here()) break;
+    uint4 *dst = reinterpret_cast<uint4 *>(out + sl.head) + sl.v0;
+    for (int from = 0; from < nv; from += kChunk, at.next()) {
+      const int n = min(kChunk, nv - from);
+      const uint4 *src = ring + at.slot * kChunk;
+      if (!same) {
+        const int e = first + from * N;                  // the chunk's first element
+        grad_words<E, kWork>(out, reinterpret_cast<const E *>(src) - e, e, e + n * N, -1, g);
+      } else if (n == kChunk) {
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) __stcs(dst + from + tid + u * kWork, g.piece<E>(src[tid + u * kWork]));
+      } else {
+        for (int i = tid; i < n; i += kWork) __stcs(dst + from + i, g.piece<E>(src[i]));
+      }
+      // what was struck out by plain stores lies behind before the next copy comes
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (place[i] >= from * N && place[i] < (from + kChunk) * N) fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[at.slot]);
+    }
+    if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge));
+    __syncwarp();
+    if (!same && !all_here()) break;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const bool end = warp == 0 && ((rank == 0 && r.id[i] >= 0 && r.id[i] < sl.head) || (rank == C - 1 && r.id[i] >= tail));
+      if (place[i] >= 0 || end) Elem<E>::store(out + r.id[i], x.dz[i]);
+    }
+  }
+  if (C > 1 && lane < C) mbar_arrive_remote(&done, lane);
+}
+
+// ----------------------------------------------------------------------------- rows read as they come
+// One row by the C blocks of a cluster, a slice each; for a gradient it is read again.
 constexpr int kThreads = 256;
 
-template <typename E, int kThreads>
-__global__ void __launch_bounds__(kThreads) distill_kernel(Distill a, int C, int slice) {
+template <typename E>
+__global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int slice) {
   constexpr int kWarps = kThreads / 32, N = Elem<E>::kVec, U = 4;
   __shared__ int ids[kMaxTop], next[kMaxTop], head[kThreads];
   __shared__ float logit[kMaxTop], dz[kMaxTop];
@@ -196,14 +723,22 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Distill a, int C, int
         for (int u = 0; u < U; ++u)
           if (p == u * kThreads) Elem<E>::strike(q[u], place % N);
       }
-      absorb<E, U>(m, s2, q, k);
+      absorb_exact<E, U>(m, s2, q, a.scale);
     }
     const float2 both = unpk2(s2);
     s = both.x + both.y;
-    if (rank == 0 && tid < sp.head && !(edges >> tid & 1u)) absorb_one(m, s, Elem<E>::load(row + tid), k);
-    if (rank == C - 1 && tid < V - tail && !(edges >> (16 + tid) & 1u)) absorb_one(m, s, Elem<E>::load(row + tail + tid), k);
+    if (rank == 0 && tid < sp.head && !(edges >> tid & 1u)) absorb_exact(m, s, Elem<E>::load(row + tid), a.scale);
+    if (rank == C - 1 && tid < V - tail && !(edges >> (16 + tid) & 1u)) absorb_exact(m, s, Elem<E>::load(row + tail + tid), a.scale);
   }
-  block_merge<kWarps>(m, s, k, sh);
+  merge_exact(m, s, a.scale);
+  if (lane == 0) sh[warp] = make_float2(m, s);
+  __syncthreads();
+  if (warp == 0) {
+    const float2 v = lane < kWarps ? sh[lane] : make_float2(kNegInf, 0.f);
+    m = v.x;
+    s = v.y;
+    merge_exact(m, s, a.scale);
+  }
   if (C > 1) {
     __syncwarp();
     cluster_wait();
@@ -215,7 +750,7 @@ __global__ void __launch_bounds__(kThreads) distill_kernel(Distill a, int C, int
       const float2 v = lane < C ? pair[lane] : make_float2(kNegInf, 0.f);
       m = v.x;
       s = v.y;
-      warp_merge(m, s, k);
+      merge_exact(m, s, a.scale);
     }
   }
   if (!counts) {
@@ -275,16 +810,80 @@ __global__ void __launch_bounds__(kSumThreads) loss_kernel(const float *row_loss
   if (threadIdx.x == 0) *loss = s[0].value();
 }
 
-int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_up(ceil_div(bytes / 16, parts), 8)); }
+// How a row is cut for the held kernel: slices of at most four chunks (64 KB), so that a third of
+// the ring is always ahead; few rows are cut finer, down to 4 KB a block, as long as all blocks run
+// at once.  Cluster 0: eight blocks' rings do not hold it.
+struct HeldPlan {
+  int cluster, slice;
+};
+HeldPlan plan_held(int64_t T, int64_t bytes) {
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, kSliceBytes));
+  c = std::max(c, std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096));
+  c = std::min<int64_t>(c, kMaxCluster);
+  const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
+  if (slice > kSlots * kChunk) return {0, 0};
+  return {(int)c, (int)slice};
+}
+
+// Clusters of the held kernel that the device holds at once; the last answers are kept.
+int max_clusters(const void *kernel, int cluster) {
+  struct Known {
+    const void *kernel;
+    int dev, cluster, n;
+  };
+  static Known known[32];
+  static int used = 0;
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known &k : known)
+    if (k.n > 0 && k.kernel == kernel && k.dev == dev && k.cluster == cluster) return k.n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cluster);
+  cfg.blockDim = dim3(kHeldThreads);
+  cfg.dynamicSmemBytes = kHeldSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+  known[used++ % 32] = {kernel, dev, cluster, n};
+  return n;
+}
 
 template <typename E>
+cudaError_t launch_held(const Distill &r, const HeldPlan &plan, cudaStream_t st) {
+  const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
+  cudaError_t e = ensure_smem(kernel, kHeldSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t clusters = std::min<int64_t>(r.T, max_clusters(kernel, plan.cluster));
+  return launch(held_kernel<E>, dim3((unsigned)(clusters * plan.cluster)), dim3(kHeldThreads), kHeldSmem, st,
+                plan.cluster, true, HeldDistill{r, plan.cluster, plan.slice});
+}
+
+// 16-byte pieces of one of `parts` slices of a row.
+int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_up(ceil_div(bytes / 16, parts), 8)); }
+
+// Rows of up to kShortest bytes go to a warp's registers, four pieces a lane, up to kShort bytes
+// sixteen, and up to kShortTeam bytes to those of four warps.
+constexpr int64_t kShortest = 2 << 10, kShort = 8 << 10, kShortTeam = 32 << 10;
+template <typename E>
 cudaError_t launch_distill(const Distill &r, int64_t bytes, cudaStream_t st) {
+  const dim3 grid((unsigned)ceil_div(r.T, 8));
+  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1>, grid, dim3(256), 0, st, 1, true, r);
+  if (bytes <= kShort) return launch(short_kernel<E, 16, 1>, grid, dim3(256), 0, st, 1, true, r);
+  if (bytes <= kShortTeam) return launch(short_kernel<E, 16, 4>, dim3((unsigned)r.T), dim3(128), 0, st, 1, true, r);
+  if (r.dlogits)
+    if (const HeldPlan plan = plan_held(r.T, bytes); plan.cluster > 0) return launch_held<E>(r, plan, st);
   const int64_t sms = num_sms();
   int c = 1;
   if (2 * r.T < sms)
     c = (int)std::min<int64_t>({std::max<int64_t>(1, 4 * sms / r.T), std::max<int64_t>(1, bytes / (4 << 10)), kMaxCluster});
-  return launch(distill_kernel<E, kThreads>, dim3((unsigned)(r.T * c)), dim3(kThreads), 0, st, c, true, r, c,
-                slice_of(bytes, c));
+  return launch(row_kernel<E>, dim3((unsigned)(r.T * c)), dim3(kThreads), 0, st, c, true, r, c, slice_of(bytes, c));
 }
 
 }  // namespace

@@ -229,20 +229,32 @@ __device__ __forceinline__ void block_merge(float &m, float &s, float k, float2 
   warp_merge(m, s, k);
 }
 
-// 1 / temperature: for the exponential (times log2(e), rounded once), and in two parts for
-// the few values whose own last bits count.
+// 1 / temperature in two parts: for the exponential (times log2(e)) and by itself.
 struct Scale {
-  float k, hi, lo;
+  float k, k_lo, hi, lo;
   static Scale of(float temperature) {
-    const double inv = 1.0 / (double)temperature;
-    const float hi = (float)inv;
-    return {(float)(inv * 1.4426950408889634074), hi, (float)(inv - (double)hi)};
+    const double inv = 1.0 / (double)temperature, k = inv * 1.4426950408889634074;
+    Scale s;
+    s.k = (float)k;
+    if ((double)s.k >= k) s.k = nextafterf(s.k, 0.f);
+    s.k_lo = fmaxf((float)(k - (double)s.k), 1.17549435e-38f);      // above zero: minus infinity times it stays that
+    s.hi = (float)inv;
+    s.lo = (float)(inv - (double)s.hi);
+    return s;
   }
-  // (x - y) / temperature; the difference's rounding error, exact in fp32, counts too
-  __device__ __forceinline__ float gap(float x, float y) const {
+  // d / temperature in units of log 2, for an exponential
+  __device__ __forceinline__ float two(float d) const { return fmaf(d, k, d * k_lo); }
+  // (x - y) / temperature as a value and what it is off by: the rounding errors of the
+  // difference and of the product are exact in fp32
+  __device__ __forceinline__ float2 gap2(float x, float y) const {
     const float d = __fsub_rn(x, y), b = __fsub_rn(d, x);
-    const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(y, b));
-    return fabsf(d) < INFINITY ? fmaf(d, hi, fmaf(e, hi, d * lo)) : d * hi;
+    const float e = __fsub_rn(__fsub_rn(x, __fsub_rn(d, b)), __fadd_rn(y, b)), p = __fmul_rn(d, hi);
+    if (!(fabsf(p) < INFINITY)) return make_float2(p, 0.f);
+    return make_float2(p, __fmaf_rn(d, hi, -p) + fmaf(e, hi, d * lo));
+  }
+  __device__ __forceinline__ float gap(float x, float y) const {
+    const float2 g = gap2(x, y);
+    return g.x + g.y;
   }
 };
 

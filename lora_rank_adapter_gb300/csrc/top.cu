@@ -135,11 +135,8 @@ __device__ __forceinline__ void warp_merge(Sums &x, float k) {
 constexpr int kTopThreads = 256;
 constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kPer = 4;                                  // 16-byte pieces of a round for each thread
-#ifndef TOPB
-#define TOPB 4
-#endif
-constexpr int kTopBlocks = TOPB;                         // on an SM
-constexpr int kWarpHits = 128;                           // pieces that a warp sets aside
+constexpr int kTopBlocks = 4;                         // on an SM
+constexpr int kWarpHits = 1024 / kTopWarps;                           // pieces that a warp sets aside
 constexpr int kList = 1344;                              // tokens among which the K largest are found
 
 struct TopShared {
