@@ -32,7 +32,8 @@
  * in that row, as the formula does.
  *
  * `temperature` (finite, > 0, log2(e) / temperature finite in fp32) divides the
- * logits: z = logits / temperature.
+ * logits: z = logits / temperature.  (A double where differences of log-probabilities
+ * are what comes out: rounded to fp32 it moves all of a row's by some 1e-7.)
  * `dlogits`, where an operator takes it, is written whole (every row, V
  * columns); it is either `logits` itself (same pointer, same stride: the
  * gradient replaces the logits) or shares no element with them.
@@ -151,7 +152,7 @@ LORA_API lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V
  * -------------------------------------------------------------------------------- */
 #define LORA_TOP_MAX 128
 LORA_API lora_status_t lora_top_logps(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits,
-                           int64_t ldl, const int64_t *labels, float temperature, float *logps, float *entropy,
+                           int64_t ldl, const int64_t *labels, double temperature, float *logps, float *entropy,
                            int64_t *top_ids, float *top_logps, float *rest_logps, float *stats, void *stream);
 
 /* --------------------------------------------------------------------------------
@@ -167,7 +168,7 @@ LORA_API lora_status_t lora_top_logps(lora_dtype_t dtype, int64_t T, int64_t V, 
  * -------------------------------------------------------------------------------- */
 LORA_API lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K,
                            const void *logits, int64_t ldl, const int64_t *labels, const int64_t *top_ids,
-                           float temperature, const float *stats, const float *entropy, const float *dlogps,
+                           double temperature, const float *stats, const float *entropy, const float *dlogps,
                            const float *dentropy, const float *dtop_logps, void *dlogits, int64_t lddl,
                            void *stream);
 
@@ -193,7 +194,7 @@ LORA_API lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, in
 typedef enum { LORA_DISTILL_FORWARD = 0, LORA_DISTILL_REVERSE = 1 } lora_distill_kind_t;
 LORA_API lora_status_t lora_distill_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits,
                            int64_t ldl, const int64_t *top_ids, const float *top_logps, const float *rest_logps,
-                           const float *weights, lora_distill_kind_t kind, float temperature, float *row_loss,
+                           const float *weights, lora_distill_kind_t kind, double temperature, float *row_loss,
                            float *loss, void *dlogits, int64_t lddl, float grad_scale, void *stream);
 
 /* --------------------------------------------------------------------------------

@@ -113,6 +113,10 @@ __device__ __forceinline__ float2 log_parts(float S) {
   return make_float2(n * 0.693359375f, fmaf(n, -2.12194440054690583e-4f, logf(f)));
 }
 
+// What the hardware's 2^x is low by on average (over an octave; at most 1.4e-7): a sum of many
+// such terms is, too.
+constexpr float kLow = 5.2e-8f;
+
 // What a row's loss and gradient come to, by a warp, from the sums over the tokens that
 // are not listed (m, s).  dz: c times the listed tokens' gradient; f: what exp((x - m) k)
 // of all others is multiplied by.  Differences of logarithms come to 2^-24 of themselves:
@@ -141,6 +145,7 @@ __device__ __forceinline__ RowTerms row_terms(const Distill &a, const Record &r,
     sum += e[i];
   }
   sum = warp_sum_f(sum);
+  s = fmaf(s, kLow, s);
   const float rest = s * expf(a.scale.gap(m, ref)), S = sum + rest, over = 1.f / S;
   const float2 ln_S = log_parts(S);
   const float p_r = rest * over;

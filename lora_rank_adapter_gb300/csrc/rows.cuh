@@ -232,8 +232,8 @@ __device__ __forceinline__ void block_merge(float &m, float &s, float k, float2 
 // 1 / temperature in two parts: for the exponential (times log2(e)) and by itself.
 struct Scale {
   float k, k_lo, hi, lo;
-  static Scale of(float temperature) {
-    const double inv = 1.0 / (double)temperature, k = inv * 1.4426950408889634074;
+  static Scale of(double temperature) {
+    const double inv = 1.0 / temperature, k = inv * 1.4426950408889634074;
     Scale s;
     s.k = (float)k;
     if ((double)s.k >= k) s.k = nextafterf(s.k, 0.f);

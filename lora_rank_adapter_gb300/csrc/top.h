@@ -15,7 +15,7 @@ struct TopArgs {
   const void *logits;
   int64_t ldl;
   const int64_t *labels;      // NULL: every row counts
-  float temperature;
+  double temperature;
   float *logps, *entropy;     // [T], NULL: not wanted
   int64_t *top_ids;           // [T][K]
   float *top_logps;           // [T][K]
@@ -42,7 +42,7 @@ struct DistillArgs {
   const float *rest;          // [T] or NULL
   const float *weights;       // [T] or NULL
   bool reverse;
-  float temperature;
+  double temperature;
   float *row_loss, *loss;     // [T], [1]
   void *dlogits;              // NULL: no gradient
   int64_t lddl;

@@ -33,12 +33,13 @@ lora_status_t check_ws(const void *ws, size_t ws_bytes, size_t need) {
 
 // Rows of logits alone.
 lora_status_t check_logits(lora_dtype_t dtype, int64_t T, int64_t V, const void *logits, int64_t ldl,
-                           float temperature, const void *dlogits, int64_t lddl) {
+                           double temperature, const void *dlogits, int64_t lddl) {
   if (dtype != LORA_F32 && dtype != LORA_BF16) return LORA_ERR_UNSUPPORTED;
   if (!size_ok(T) || !size_ok(V)) return LORA_ERR_INVALID_ARG;
   if (V > kMaxVocab) return LORA_ERR_UNSUPPORTED;
   // the kernels scale by log2(e) / temperature
-  if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature * 1.4426950408889634f))
+  const float rounded = (float)temperature;
+  if (!(rounded > 0.f) || !isfinite(rounded) || !isfinite(1.f / rounded * 1.4426950408889634f))
     return LORA_ERR_INVALID_ARG;
   const int e = dtype == LORA_BF16 ? 2 : 4;
   if (T > 0 && V > 0) {
@@ -201,7 +202,7 @@ lora_status_t lora_policy_loss(lora_dtype_t dtype, int64_t T, int64_t V, const v
 }
 
 lora_status_t lora_top_logps(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits, int64_t ldl,
-                             const int64_t *labels, float temperature, float *logps, float *entropy,
+                             const int64_t *labels, double temperature, float *logps, float *entropy,
                              int64_t *top_ids, float *top_logps_out, float *rest_logps, float *stats, void *stream) {
   LORA_TRY(check_logits(dtype, T, V, logits, ldl, temperature, nullptr, 0));
   if (K < 0) return LORA_ERR_INVALID_ARG;
@@ -222,7 +223,7 @@ lora_status_t lora_top_logps(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K
 }
 
 lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits,
-                                      int64_t ldl, const int64_t *labels, const int64_t *top_ids, float temperature,
+                                      int64_t ldl, const int64_t *labels, const int64_t *top_ids, double temperature,
                                       const float *stats, const float *entropy, const float *dlogps,
                                       const float *dentropy, const float *dtop_logps, void *dlogits, int64_t lddl,
                                       void *stream) {
@@ -248,7 +249,7 @@ lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, int64_t V, 
 
 lora_status_t lora_distill_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_t K, const void *logits, int64_t ldl,
                                 const int64_t *top_ids, const float *teacher_logps, const float *rest_logps,
-                                const float *weights, lora_distill_kind_t kind, float temperature, float *row_loss,
+                                const float *weights, lora_distill_kind_t kind, double temperature, float *row_loss,
                                 float *loss, void *dlogits, int64_t lddl, float grad_scale, void *stream) {
   LORA_TRY(check_logits(dtype, T, V, logits, ldl, temperature, dlogits, lddl));
   if (K < 1) return LORA_ERR_INVALID_ARG;

@@ -70,7 +70,7 @@ def lib():
         return _lib
     L = binding.lib()
     i32, i64, u32, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
-    P, sz = ctypes.c_void_p, ctypes.c_size_t
+    P, sz, f64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_double
     TP, PP, HP = ctypes.POINTER(AdamWTensor), ctypes.POINTER(AdamWPlanStruct), ctypes.POINTER(AdamWHyper)
     sig = {
         "lora_train_workspace_size": (sz, [i32, i64, i64]),
@@ -80,9 +80,9 @@ def lib():
                                        P, i64, f32, P, sz, P]),
         "lora_policy_loss": (i32, [i32, i64, i64, P, i64, P, P, P, P, P, f32, f32, f32, f32, P, P, P, i64, f32,
                                    P, sz, P]),
-        "lora_top_logps": (i32, [i32, i64, i64, i32, P, i64, P, f32, P, P, P, P, P, P, P]),
-        "lora_top_logps_backward": (i32, [i32, i64, i64, i32, P, i64, P, P, f32, P, P, P, P, P, P, i64, P]),
-        "lora_distill_loss": (i32, [i32, i64, i64, i32, P, i64, P, P, P, P, i32, f32, P, P, P, i64, f32, P]),
+        "lora_top_logps": (i32, [i32, i64, i64, i32, P, i64, P, f64, P, P, P, P, P, P, P]),
+        "lora_top_logps_backward": (i32, [i32, i64, i64, i32, P, i64, P, P, f64, P, P, P, P, P, P, i64, P]),
+        "lora_distill_loss": (i32, [i32, i64, i64, i32, P, i64, P, P, P, P, i32, f64, P, P, P, i64, f32, P]),
         "lora_scale_gradient": (i32, [i32, i64, i64, P, i64, P, P]),
         "lora_adamw_table_size": (sz, [TP, i32]),
         "lora_adamw_build": (i32, [TP, i32, i32, i32, u32, P, sz, PP, P]),
