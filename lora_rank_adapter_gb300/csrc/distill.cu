@@ -86,18 +86,35 @@ __device__ __forceinline__ void read_values(const Distill &a, int64_t t, const E
     r.lnq[i] = a.teacher[t * a.K + i * 32 + lane_id()];
   }
 }
-// Entries that name a token listed before them are dropped.  `scratch`: kMaxTop ints.  By a warp.
-__device__ __forceinline__ void drop_repeated(Record &r, int K, int *scratch) {
+// Entries that name a token listed before them are dropped.  By a warp, with kSeenWords words of
+// zeros, which it leaves as they were: a set of hashed ids tells which may be a token's second
+// entry (one in a few rows), and only those are looked for among all.
+constexpr int kSeenWords = 128;
+__device__ __forceinline__ void drop_repeated(Record &r, uint32_t *seen) {
   const int lane = lane_id();
+  unsigned again[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) scratch[i * 32 + lane] = r.id[i];
-  __syncwarp();
-  for (int j = 0; j < K; ++j) {
-    const int other = scratch[j];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (j < i * 32 + lane && r.id[i] == other) r.id[i] = -1;
+  for (int i = 0; i < kEach; ++i) {
+    const uint32_t hash = (uint32_t)r.id[i] * 0x9E3779B9u >> 20, bit = 1u << (hash & 31u);
+    again[i] = __ballot_sync(0xffffffffu, r.id[i] >= 0 && (atomicOr(&seen[hash >> 5], bit) & bit) != 0);
   }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (r.id[i] >= 0) seen[(uint32_t)r.id[i] * 0x9E3779B9u >> 25] = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    for (unsigned left = again[i]; left; left &= left - 1) {
+      const int id = __shfl_sync(0xffffffffu, r.id[i], __ffs(left) - 1);
+      bool found = id < 0;                               // dropped meanwhile
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const unsigned same = __ballot_sync(0xffffffffu, r.id[j] == id);
+        const unsigned drop = found ? same : same & (same - 1);
+        found = found || same != 0;
+        if (id >= 0 && drop >> lane & 1u) r.id[j] = -1;
+      }
+    }
   __syncwarp();
 }
 
@@ -240,14 +257,15 @@ __device__ __forceinline__ void merge_exact(float &m, float &s, const Scale &c) 
 // ----------------------------------------------------------------------------- short rows
 // A row of some KB in the registers of one warp, or of four that make up a block.  Which of a
 // piece's elements are listed is a set of bits in shared memory, one for each element.
-template <typename E, int kPieces, int kTeam>
-__global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Distill a) {
-  constexpr int kLanes = 32 * kTeam, kRows = kTeam == 1 ? 8 : 1, N = Elem<E>::kVec;
+template <typename E, int kPieces, int kTeam, int kTeamBlocks>
+__global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
+  constexpr int kLanes = 32 * kTeam, kRows = 4 / kTeam, N = Elem<E>::kVec;
   constexpr int kWords = kPieces * kTeam * N;            // of 32 elements
   __shared__ uint32_t bits[kRows][kWords];
   __shared__ unsigned edge_bits[kRows];
-  __shared__ int scratch[kRows * kTeam][kMaxTop];
+  __shared__ uint32_t seen[4][kSeenWords];               // of each warp
   __shared__ float2 sh[kTeam];
+  static_assert(kTeam == 1 || kTeam == 4, "a warp, or a block of four");
   auto sync = [] { if (kTeam == 1) __syncwarp(); else __syncthreads(); };
   pdl_wait();
   pdl_launch_dependents();
@@ -259,6 +277,7 @@ __global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Di
   const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
   const RowSpan<E> sp(row, V);
   for (int i = tid; i < kWords; i += kLanes) bits[mine][i] = 0;
+  for (int i = lane; i < kSeenWords; i += 32) seen[warp][i] = 0;
   if (tid == 0) edge_bits[mine] = 0;
   Record r;
   const float w = a.weights ? a.weights[t] : 1.f;
@@ -298,11 +317,11 @@ __global__ void __launch_bounds__(kTeam == 1 ? 256 : 32 * kTeam) short_kernel(Di
     }
     twice = __any_sync(0xffffffffu, twice);
     if (kTeam > 1 && lane == 0) sh[0].x = twice ? 1.f : 0.f;
-    if (kTeam == 1 && twice) drop_repeated(r, a.K, scratch[warp]);
+    if (kTeam == 1 && twice) drop_repeated(r, seen[warp]);
   }
   sync();
   if (kTeam > 1) {
-    if (sh[0].x != 0.f) drop_repeated(r, a.K, scratch[warp]);
+    if (sh[0].x != 0.f) drop_repeated(r, seen[warp]);
     __syncthreads();
   }
   float m = kNegInf;
@@ -390,11 +409,90 @@ struct HeldDistill {
   int cluster, slice;      // slice: 16-byte pieces of a block at most, up to kSlots chunks
 };
 
+// A row's record, and what can be told of it ahead of the sums over the rest: with g_j the logits over
+// the temperature, from the largest listed one (top) on,
+//     e_j = exp(g_j), E = sum e_j; forward x_j = q_j, Q their sum and q_r; reverse x_j = g_j - ln q_j, B = sum e_j x_j
 struct HeldRecord {
   int id[kMaxTop];
-  float z[kMaxTop], lnq[kMaxTop];
-  float w, ln_qr;
+  float z[kMaxTop], lnq[kMaxTop], e[kMaxTop], x[kMaxTop];
+  float top, E, B, Q, qr, ln_qr, c;
   int counts;
+};
+__device__ __forceinline__ void foresee(const Distill &a, const Record &r, HeldRecord &to) {
+  const int lane = lane_id();
+  float top = kNegInf, M;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (r.id[i] >= 0) top = fmaxf(top, r.z[i]);
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(top));
+  float E = 0.f, B = 0.f, Q = 0.f;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    if (i * 32 >= a.K) continue;
+    float e = 0.f, x = 0.f;
+    if (r.id[i] >= 0) {
+      const float g = a.scale.gap(r.z[i], ref_of(M));
+      e = expf(g);
+      x = a.reverse ? (e == 0.f ? 0.f : g - r.lnq[i]) : expf(r.lnq[i]);      // no 0 * infinity
+    }
+    E += e;
+    B += e * x;
+    Q += x;
+    to.e[i * 32 + lane] = e;
+    to.x[i * 32 + lane] = x;
+  }
+  E = warp_sum_f(E);
+  B = warp_sum_f(B);
+  Q = warp_sum_f(Q);
+  if (lane != 0) return;
+  to.qr = a.rest && !a.reverse ? expf(to.ln_qr) : 0.f;
+  to.top = M;
+  to.E = E;
+  to.B = B;
+  to.Q = Q + to.qr;
+}
+
+// What a working warp needs of a row once it has the sums (m, s) over the rest: f as in RowTerms, and
+// a listed token's dz from its e and x.
+struct HeldTerms {
+  float f, p, u, v;
+  bool reverse;
+  __device__ __forceinline__ HeldTerms(const Distill &a, const HeldRecord &r, float m, float s) {
+    const float ref = ref_of(fmaxf(r.top, m)), c = r.c;
+    const float lead = a.scale.gap(r.top, ref);
+    s = fmaf(s, kLow, s);
+    const float rest = s * expf(a.scale.gap(m, ref)), listed = r.E * expf(lead), S = listed + rest, over = 1.f / S;
+    const float p_r = rest * over;
+    float F;
+    reverse = a.reverse;
+    p = expf(lead) * over;
+    if (!reverse) {
+      F = r.Q * p_r - r.qr;
+      u = c * p * r.Q;                   // dz = u e - c x
+      v = -c;
+    } else {
+      const float2 ln_S = log_parts(S);
+      const float ln_p = (lead - ln_S.x) - ln_S.y, P = r.E * p;
+      float L = r.E == 0.f ? 0.f : p * r.B + P * ln_p;
+      if (a.rest) {
+        const float ratio = listed / rest;
+        const float ln_pr = ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(m, ref) + logf(s) - (ln_S.x + ln_S.y);
+        const float gap_r = p_r == 0.f ? 0.f : ln_pr - r.ln_qr;
+        L += p_r * gap_r;
+        F = p_r * (gap_r - L);
+        v = ln_p - L;                    // dz = u e (x + v)
+      } else {
+        F = -p_r * (L + P);
+        v = ln_p + 1.f - L - P;
+      }
+      u = c * p;
+    }
+    f = s == 0.f ? 0.f : c * F / s;
+    if (!(S > 0.f)) f = u = NAN;
+  }
+  __device__ __forceinline__ float dz(float e, float x) const {
+    return reverse ? (e == 0.f ? 0.f : u * e * (x + v)) : fmaf(u, e, v * x);
+  }
 };
 
 // A block's slice of a row.
@@ -429,7 +527,9 @@ template <typename E>
 __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDistill h) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ HeldRecord records[kAhead];
-  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], ready[2], step, done;
+  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], step, done;
+  __shared__ float2 sums[kAhead];                        // (m, s) of a row, for its loss
+  __shared__ uint32_t seen[kSeenWords];
   __shared__ float2 pairs[2][kMaxCluster * kWorkers];    // (m, s) of every warp of the cluster, two exchanges
   const Distill &a = h.a;
   constexpr int N = Elem<E>::kVec;
@@ -444,6 +544,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     for (int i = 0; i < kAhead; ++i) {
       mbar_init(&made[i], 1);
       mbar_init(&read[i], kWorkers + 1);
+      mbar_init(&summed[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C == 1 ? kWorkers : 1);
     mbar_init(&step, kWorkers);
@@ -460,27 +561,67 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
   int64_t t = blockIdx.x / C;
   At<kAhead> rec;
 
-  if (warp == kWorkers + 1) {                            // the records
-    for (int64_t row_no = 0; t < a.T; t += clusters, ++row_no, rec.next()) {
+  if (warp == kWorkers + 1) {                            // the records; and the loss of the row that a place was for before
+    for (int i = lane; i < kSeenWords; i += 32) seen[i] = 0;
+    __syncwarp();
+    struct Listed {
       Record r;
-      const float w = a.weights ? a.weights[t] : 1.f;
-      const bool counts = read_ids(a, t, r) && w != 0.f;
-      if (counts) read_values(a, t, static_cast<const E *>(a.logits) + t * a.ldl, r);
-      const float ln_qr = a.rest ? a.rest[t] : 0.f;
-      if (!__all_sync(0xffffffffu, row_no < kAhead || mbar_wait(&read[rec.slot], rec.parity ^ 1))) break;
+      float w, ln_qr;
+      bool counts;
+    };
+    auto read_list = [&](int64_t t, Listed &l) {
+      l.w = a.weights ? a.weights[t] : 1.f;
+      l.ln_qr = a.rest ? a.rest[t] : 0.f;
+      l.counts = read_ids(a, t, l.r) && l.w != 0.f;
+    };
+    Listed now;
+    if (t < a.T) read_list(t, now);
+    for (int64_t n = 0;; ++n, t += clusters, rec.next()) {
+      const int64_t before = t - kAhead * clusters;      // its row
+      if (before >= a.T) break;
       HeldRecord &to = records[rec.slot];
-      if (counts) drop_repeated(r, a.K, to.id);
+      if (t < a.T && now.counts) read_values(a, t, static_cast<const E *>(a.logits) + t * a.ldl, now.r);
+      Listed next;
+      if (t + clusters < a.T) read_list(t + clusters, next);
+      if (n >= kAhead) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&summed[rec.slot], rec.parity ^ 1))) break;
+        if (n % C == rank) {                             // each block in turn
+          float loss = 0.f;
+          if (to.counts) {
+            Record old;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              old.id[i] = to.id[i * 32 + lane];
+              old.z[i] = to.z[i * 32 + lane];
+              old.lnq[i] = to.lnq[i * 32 + lane];
+            }
+            const float2 v = sums[rec.slot];
+            loss = row_terms(a, old, to.ln_qr, v.x, v.y, 0.f).loss;
+          }
+          if (lane == 0) a.row_loss[before] = loss;
+        }
+        if (t >= a.T) continue;
+        if (!__all_sync(0xffffffffu, mbar_wait(&read[rec.slot], rec.parity ^ 1))) break;
+      }
+      if (t >= a.T) continue;
+      const bool counts = now.counts;
+      const float w = now.w, ln_qr = now.ln_qr;
+      Record r = now.r;
+      now = next;
+      if (counts) drop_repeated(r, seen);
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        to.id[i * 32 + lane] = r.id[i];
-        to.z[i * 32 + lane] = r.z[i];
-        to.lnq[i * 32 + lane] = r.lnq[i];
+        to.id[i * 32 + lane] = counts ? r.id[i] : -1;
+        to.z[i * 32 + lane] = counts ? r.z[i] : 0.f;
+        to.lnq[i * 32 + lane] = counts ? r.lnq[i] : 0.f;
       }
       if (lane == 0) {
-        to.w = w;
+        to.c = w * a.grad_scale * a.scale.hi;
         to.ln_qr = ln_qr;
         to.counts = counts;
       }
+      __syncwarp();
+      if (counts) foresee(a, r, to);
       __syncwarp();
       if (lane == 0) mbar_arrive(&made[rec.slot]);
     }
@@ -529,31 +670,35 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     const Slice<E> sl(h, t, rank);
     E *out = static_cast<E *>(a.dlogits) + t * a.lddl;
     const int nv = sl.nv, tail = sl.head + sl.vecs * N, first = sl.head + sl.v0 * N;
-    const bool counts = of.counts != 0;
-    const float w = of.w, ln_qr = of.ln_qr;
-    Record r;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      r.id[i] = of.id[i * 32 + lane];
-      r.z[i] = of.z[i * 32 + lane];
-      r.lnq[i] = of.lnq[i * 32 + lane];
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&read[rec.slot]);
-    if (!counts) {
-      if (rank == 0 && tid == 0) a.row_loss[t] = 0.f;
+    auto leave = [&] {                                   // done with the record
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&read[rec.slot]);
+    };
+    if (of.counts == 0) {
+      if (tid == 0) mbar_arrive(&summed[rec.slot]);
+      leave();
       zero_span<E, kWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N, tid);
       continue;
     }
+    int id[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) id[i] = i * 32 < a.K ? of.id[i * 32 + lane] : -1;
     // where in the ring an entry is, if it is in one of this warp's pieces: its element from the slice's start
     int place[kEach];
+    unsigned touched = 0;                                // chunks with any of them
     bool edges = false;                                  // one of them is among the ragged ends
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int e = r.id[i] - first;
-      place[i] = r.id[i] >= 0 && e >= 0 && e < nv * N && e / N % kWork / 32 == warp ? e : -1;
-      edges = edges || (r.id[i] >= 0 && (r.id[i] < sl.head || r.id[i] >= tail));
+      place[i] = -1;
+      if (i * 32 >= a.K) continue;
+      const int e = id[i] - first;
+      if (id[i] >= 0 && e >= 0 && e < nv * N && e / N % kWork / 32 == warp) {
+        place[i] = e;
+        touched |= 1u << (e / N / kChunk);
+      }
+      edges = edges || (id[i] >= 0 && (id[i] < sl.head || id[i] >= tail));
     }
+    touched = __reduce_or_sync(0xffffffffu, touched);
     // the ragged ends, at most seven elements each: the first block's and the last one's, by warp 0
     const bool at_head = rank == 0 && tid < sl.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
     const int edge_at = at_head ? tid : tail + tid - 16;
@@ -563,7 +708,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
 #pragma unroll
       for (int i = 0; i < kEach; ++i)
         for (int l = 0; l < 32; ++l)
-          if (__shfl_sync(0xffffffffu, r.id[i], l) == edge_at) edge = kNegInf;
+          if (__shfl_sync(0xffffffffu, id[i], l) == edge_at) edge = kNegInf;
 
     float m = kNegInf;
     uint64_t s2 = 0;
@@ -572,11 +717,13 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     for (int from = 0; from < nv; from += kChunk, here.next()) {
       ok = mbar_wait(&full[here.slot], here.parity) && ok;
       uint4 *slot = ring + here.slot * kChunk;
+      if (touched >> (from / kChunk) & 1u) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (place[i] >= from * N && place[i] < (from + kChunk) * N)
-          Elem<E>::store(reinterpret_cast<E *>(slot) + (place[i] - from * N), kNegInf);
-      __syncwarp();
+        for (int i = 0; i < kEach; ++i)
+          if (place[i] >= from * N && place[i] < (from + kChunk) * N)
+            Elem<E>::store(reinterpret_cast<E *>(slot) + (place[i] - from * N), kNegInf);
+        __syncwarp();
+      }
       const int n = min(kChunk, nv - from);
       uint4 q[kPer];
 #pragma unroll
@@ -613,8 +760,11 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       m = mm;
     }
     merge_exact(m, s, a.scale);
-    const RowTerms x = row_terms(a, r, ln_qr, m, s, w * a.grad_scale * a.scale.hi);
-    if (rank == 0 && tid == 0) a.row_loss[t] = x.loss;
+    if (tid == 0) {
+      sums[rec.slot] = make_float2(m, s);
+      mbar_arrive(&summed[rec.slot]);
+    }
+    const HeldTerms x(a, of, m, s);
     const RowGrad g = {ref_of(m), k, 0.f, x.f};
     const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0;
     // Where the gradient's rows sit at other offsets, warps write each other's elements: all have struck
@@ -641,9 +791,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
         for (int i = tid; i < n; i += kWork) __stcs(dst + from + i, g.piece<E>(src[i]));
       }
       // what was struck out by plain stores lies behind before the next copy comes
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (place[i] >= from * N && place[i] < (from + kChunk) * N) fence_proxy_async_smem();
+      if (touched >> (from / kChunk) & 1u) fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[at.slot]);
     }
@@ -652,9 +800,11 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     if (!same && !all_here()) break;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const bool end = warp == 0 && ((rank == 0 && r.id[i] >= 0 && r.id[i] < sl.head) || (rank == C - 1 && r.id[i] >= tail));
-      if (place[i] >= 0 || end) Elem<E>::store(out + r.id[i], x.dz[i]);
+      if (i * 32 >= a.K) continue;
+      const bool end = warp == 0 && ((rank == 0 && id[i] >= 0 && id[i] < sl.head) || (rank == C - 1 && id[i] >= tail));
+      if (place[i] >= 0 || end) Elem<E>::store(out + id[i], x.dz(of.e[i * 32 + lane], of.x[i * 32 + lane]));
     }
+    leave();
   }
   if (C > 1 && lane < C) mbar_arrive_remote(&done, lane);
 }
@@ -875,13 +1025,29 @@ int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_
 
 // Rows of up to kShortest bytes go to a warp's registers, four pieces a lane, up to kShort bytes
 // sixteen, and up to kShortTeam bytes to those of four warps.
-constexpr int64_t kShortest = 2 << 10, kShort = 8 << 10, kShortTeam = 32 << 10;
+#ifndef SB1
+#define SB1 6
+#endif
+#ifndef SMID
+#define SMID 2
+#endif
+#ifndef SB2
+#define SB2 7
+#endif
+#ifndef SB3
+#define SB3 6
+#endif
+#ifndef SB4
+#define SB4 4
+#endif
+constexpr int64_t kShortest = 2 << 10, kShortTeam = 32 << 10;
 template <typename E>
 cudaError_t launch_distill(const Distill &r, int64_t bytes, cudaStream_t st) {
-  const dim3 grid((unsigned)ceil_div(r.T, 8));
-  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1>, grid, dim3(256), 0, st, 1, true, r);
-  if (bytes <= kShort) return launch(short_kernel<E, 16, 1>, grid, dim3(256), 0, st, 1, true, r);
-  if (bytes <= kShortTeam) return launch(short_kernel<E, 16, 4>, dim3((unsigned)r.T), dim3(128), 0, st, 1, true, r);
+  const dim3 fourth((unsigned)ceil_div(r.T, 4)), each((unsigned)r.T);
+  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1, SB1>, fourth, dim3(128), 0, st, 1, true, r);
+  if (bytes <= (4 << 10) * SMID) return launch(short_kernel<E, 4, 4, SB2>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 16 << 10) return launch(short_kernel<E, 8, 4, SB3>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= kShortTeam) return launch(short_kernel<E, 16, 4, SB4>, each, dim3(128), 0, st, 1, true, r);
   if (r.dlogits)
     if (const HeldPlan plan = plan_held(r.T, bytes); plan.cluster > 0) return launch_held<E>(r, plan, st);
   const int64_t sms = num_sms();
