@@ -396,11 +396,20 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
 constexpr int kWorkers = 8;                              // warps that sum and write
 constexpr int kWork = 32 * kWorkers;
 constexpr int kHeldThreads = kWork + 64;                 // and the loader's warp, and the records'
-constexpr int kPer = 4;                                  // 16-byte pieces of a chunk for each thread
+#ifndef KPER
+#define KPER 4
+#endif
+#ifndef KSLOTS
+#define KSLOTS 6
+#endif
+#ifndef KSLICE
+#define KSLICE 64
+#endif
+constexpr int kPer = KPER;                                  // 16-byte pieces of a chunk for each thread
 constexpr int kChunk = kPer * kWork;
-constexpr int kSlots = 6;                                // 96 KB: two blocks on an SM
+constexpr int kSlots = KSLOTS;                                // 96 KB: two blocks on an SM
 constexpr int kHeldBlocks = 2;
-constexpr int kSliceBytes = 64 << 10;                    // of a row for a block, where eight blocks suffice
+constexpr int kSliceBytes = KSLICE << 10;                    // of a row for a block, where eight blocks suffice
 constexpr int kHeldSmem = kSlots * kChunk * 16;
 constexpr int kAhead = 4;                                // records made up ahead
 
@@ -415,8 +424,10 @@ struct HeldDistill {
 struct HeldRecord {
   int id[kMaxTop];
   float z[kMaxTop], lnq[kMaxTop], e[kMaxTop], x[kMaxTop];
+  int place[kMaxTop];                                    // its element from the start of the block's slice, -1: not in a piece of it
+  unsigned touched[kWorkers];                            // chunks in which a warp has any
   float top, E, B, Q, qr, ln_qr, c;
-  int counts;
+  int counts, edges;                                     // edges: any among the ragged ends
 };
 __device__ __forceinline__ void foresee(const Distill &a, const Record &r, HeldRecord &to) {
   const int lane = lane_id();
@@ -461,7 +472,7 @@ struct HeldTerms {
     const float ref = ref_of(fmaxf(r.top, m)), c = r.c;
     const float lead = a.scale.gap(r.top, ref);
     s = fmaf(s, kLow, s);
-    const float rest = s * expf(a.scale.gap(m, ref)), listed = r.E * expf(lead), S = listed + rest, over = 1.f / S;
+    const float rest = s * expf(a.scale.gap(m, ref)), listed = r.E * expf(lead), S = listed + rest, over = __fdividef(1.f, S);
     const float p_r = rest * over;
     float F;
     reverse = a.reverse;
@@ -475,7 +486,7 @@ struct HeldTerms {
       const float ln_p = (lead - ln_S.x) - ln_S.y, P = r.E * p;
       float L = r.E == 0.f ? 0.f : p * r.B + P * ln_p;
       if (a.rest) {
-        const float ratio = listed / rest;
+        const float ratio = __fdividef(listed, rest);
         const float ln_pr = ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(m, ref) + logf(s) - (ln_S.x + ln_S.y);
         const float gap_r = p_r == 0.f ? 0.f : ln_pr - r.ln_qr;
         L += p_r * gap_r;
@@ -487,7 +498,7 @@ struct HeldTerms {
       }
       u = c * p;
     }
-    f = s == 0.f ? 0.f : c * F / s;
+    f = s == 0.f ? 0.f : __fdividef(c * F, s);
     if (!(S > 0.f)) f = u = NAN;
   }
   __device__ __forceinline__ float dz(float e, float x) const {
@@ -620,8 +631,24 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
         to.ln_qr = ln_qr;
         to.counts = counts;
       }
+      if (lane < kWorkers) to.touched[lane] = 0;
       __syncwarp();
-      if (counts) foresee(a, r, to);
+      if (counts) {
+        foresee(a, r, to);
+        const Slice<E> sl(h, t, rank);
+        const int first = sl.head + sl.v0 * N, tail = sl.head + sl.vecs * N;
+        bool edges = false;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const int e = r.id[i] - first;
+          const bool here = r.id[i] >= 0 && e >= 0 && e < sl.nv * N;
+          to.place[i * 32 + lane] = here ? e : -1;
+          if (here) atomicOr(&to.touched[e / N % kWork / 32], 1u << (e / N / kChunk));
+          edges = edges || (r.id[i] >= 0 && (r.id[i] < sl.head || r.id[i] >= tail));
+        }
+        edges = __any_sync(0xffffffffu, edges);
+        if (lane == 0) to.edges = edges;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&made[rec.slot]);
     }
@@ -680,35 +707,24 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       zero_span<E, kWork>(out, rank == 0 ? 0 : first, rank == C - 1 ? V : first + nv * N, tid);
       continue;
     }
-    int id[kEach];
+    const unsigned touched = of.touched[warp];
+    // the elements of entries in this warp's pieces
+    auto each_place = [&](auto &&f) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) id[i] = i * 32 < a.K ? of.id[i * 32 + lane] : -1;
-    // where in the ring an entry is, if it is in one of this warp's pieces: its element from the slice's start
-    int place[kEach];
-    unsigned touched = 0;                                // chunks with any of them
-    bool edges = false;                                  // one of them is among the ragged ends
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      place[i] = -1;
-      if (i * 32 >= a.K) continue;
-      const int e = id[i] - first;
-      if (id[i] >= 0 && e >= 0 && e < nv * N && e / N % kWork / 32 == warp) {
-        place[i] = e;
-        touched |= 1u << (e / N / kChunk);
+      for (int i = 0; i < kEach; ++i) {
+        if (i * 32 >= a.K) continue;
+        const int place = of.place[i * 32 + lane];
+        if (place >= 0 && place / N % kWork / 32 == warp) f(i, place);
       }
-      edges = edges || (id[i] >= 0 && (id[i] < sl.head || id[i] >= tail));
-    }
-    touched = __reduce_or_sync(0xffffffffu, touched);
+    };
     // the ragged ends, at most seven elements each: the first block's and the last one's, by warp 0
     const bool at_head = rank == 0 && tid < sl.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
     const int edge_at = at_head ? tid : tail + tid - 16;
     float edge = kNegInf;
     if (at_head || at_tail) edge = Elem<E>::load(sl.row + edge_at);
-    if (warp == 0 && __any_sync(0xffffffffu, edges))
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        for (int l = 0; l < 32; ++l)
-          if (__shfl_sync(0xffffffffu, id[i], l) == edge_at) edge = kNegInf;
+    if (warp == 0 && of.edges)
+      for (int j = 0; j < a.K; ++j)
+        if (of.id[j] == edge_at) edge = kNegInf;
 
     float m = kNegInf;
     uint64_t s2 = 0;
@@ -718,10 +734,10 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       ok = mbar_wait(&full[here.slot], here.parity) && ok;
       uint4 *slot = ring + here.slot * kChunk;
       if (touched >> (from / kChunk) & 1u) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          if (place[i] >= from * N && place[i] < (from + kChunk) * N)
-            Elem<E>::store(reinterpret_cast<E *>(slot) + (place[i] - from * N), kNegInf);
+        each_place([&](int, int place) {
+          if (place >= from * N && place < (from + kChunk) * N)
+            Elem<E>::store(reinterpret_cast<E *>(slot) + (place - from * N), kNegInf);
+        });
         __syncwarp();
       }
       const int n = min(kChunk, nv - from);
@@ -798,12 +814,15 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge));
     __syncwarp();
     if (!same && !all_here()) break;
+    if (touched) each_place([&](int i, int place) {
+      Elem<E>::store(out + first + place, x.dz(of.e[i * 32 + lane], of.x[i * 32 + lane]));
+    });
+    if (warp == 0 && of.edges)
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      if (i * 32 >= a.K) continue;
-      const bool end = warp == 0 && ((rank == 0 && id[i] >= 0 && id[i] < sl.head) || (rank == C - 1 && id[i] >= tail));
-      if (place[i] >= 0 || end) Elem<E>::store(out + id[i], x.dz(of.e[i * 32 + lane], of.x[i * 32 + lane]));
-    }
+      for (int i = 0; i < kEach; ++i) {
+        const int j = i * 32 + lane, id = of.id[j];
+        if ((rank == 0 && id >= 0 && id < sl.head) || (rank == C - 1 && id >= tail)) Elem<E>::store(out + id, x.dz(of.e[j], of.x[j]));
+      }
     leave();
   }
   if (C > 1 && lane < C) mbar_arrive_remote(&done, lane);
