@@ -396,26 +396,23 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
 constexpr int kWorkers = 8;                              // warps that sum and write
 constexpr int kWork = 32 * kWorkers;
 constexpr int kHeldThreads = kWork + 64;                 // and the loader's warp, and the records'
-#ifndef KPER
-#define KPER 4
-#endif
-#ifndef KSLOTS
-#define KSLOTS 6
-#endif
-#ifndef KSLICE
-#define KSLICE 64
-#endif
-constexpr int kPer = KPER;                                  // 16-byte pieces of a chunk for each thread
-constexpr int kChunk = kPer * kWork;
-constexpr int kSlots = KSLOTS;                                // 96 KB: two blocks on an SM
 constexpr int kHeldBlocks = 2;
-constexpr int kSliceBytes = KSLICE << 10;                    // of a row for a block, where eight blocks suffice
-constexpr int kHeldSmem = kSlots * kChunk * 16;
+// Chunks of kPer 16-byte pieces for each thread, kSlots of them in a block's ring, and as much of a row
+// for a block where eight blocks suffice.  bf16, bound by its instructions, gains from long chunks and
+// three blocks for a row of 256 KB; fp32, bound by its bytes, from chunks on their way ahead.  Of the
+// copy rate, 28 KB x 3 (slices of 84 KB) / 16 KB x 6 (64 KB): rows of 128256 bf16 83 % / 77, of 200000
+// 81 / 64, of 50257 66 / 64; rows of 32000 fp32 81 / 92, of 128256 88 / 92.
+template <typename E>
+struct Ring {
+  static constexpr bool kLong = sizeof(E) == 2;
+  static constexpr int kPer = kLong ? 7 : 4, kSlots = kLong ? 3 : 6, kChunk = kPer * kWork;
+  static constexpr int kSliceBytes = (kLong ? 84 : 64) << 10, kSmem = kSlots * kChunk * 16;
+};
 constexpr int kAhead = 4;                                // records made up ahead
 
 struct HeldDistill {
   Distill a;
-  int cluster, slice;      // slice: 16-byte pieces of a block at most, up to kSlots chunks
+  int cluster, slice;      // slice: 16-byte pieces of a block at most, up to a ring
 };
 
 // A row's record, and what can be told of it ahead of the sums over the rest: with g_j the logits over
@@ -538,12 +535,12 @@ template <typename E>
 __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDistill h) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ HeldRecord records[kAhead];
-  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], step, done;
+  __shared__ uint64_t full[Ring<E>::kSlots], empty[Ring<E>::kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], step, done;
   __shared__ float2 sums[kAhead];                        // (m, s) of a row, for its loss
   __shared__ uint32_t seen[kSeenWords];
   __shared__ float2 pairs[2][kMaxCluster * kWorkers];    // (m, s) of every warp of the cluster, two exchanges
   const Distill &a = h.a;
-  constexpr int N = Elem<E>::kVec;
+  constexpr int N = Elem<E>::kVec, kPer = Ring<E>::kPer, kSlots = Ring<E>::kSlots, kChunk = Ring<E>::kChunk;
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, C = h.cluster, V = (int)a.V;
   const int rank = (int)(blockIdx.x % C);
   const int64_t clusters = gridDim.x / C;
@@ -835,7 +832,8 @@ constexpr int kThreads = 256;
 template <typename E>
 __global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int slice) {
   constexpr int kWarps = kThreads / 32, N = Elem<E>::kVec, U = 4;
-  __shared__ int ids[kMaxTop], next[kMaxTop], head[kThreads];
+  __shared__ int ids[kMaxTop], next[kMaxTop], head[kThreads];      // each thread's listed tokens: a chain
+  __shared__ uint32_t rounds[kThreads];          // the rounds, modulo 32, that they are met in
   __shared__ float logit[kMaxTop], dz[kMaxTop];
   __shared__ float2 sh[kWarps], pair[kMaxCluster];
   __shared__ unsigned edges;                     // listed ones among the ragged ends
@@ -850,9 +848,11 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int sli
   const int v0 = min(rank * slice, sp.vecs), v1 = min(v0 + slice, sp.vecs), tail = sp.tail();
   const int e0 = rank == 0 ? 0 : sp.head + v0 * N, e1 = rank == C - 1 ? V : sp.head + v1 * N;
   const float k = a.scale.k;
+  int mark = -1;
   if (tid < kMaxTop) {
     const int64_t id = tid < K ? a.ids[t * K + tid] : -1;
-    ids[tid] = id >= 0 && id < V ? (int)id : -1;
+    mark = id >= 0 && id < V ? (int)id : -1;
+    ids[tid] = mark;
   }
   if (C > 1) cluster_arrive();                   // no block is written to before it runs
   if (tid == 0) {
@@ -860,43 +860,54 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int sli
     edges = 0;
   }
   head[tid] = -1;
-  __syncthreads();
-  int mark = tid < kMaxTop ? ids[tid] : -1;
-  for (int j = 0; j < tid && mark >= 0; ++j)
-    if (ids[j] == mark) mark = -1;               // listed before
+  rounds[tid] = 0;
+  const bool any = __syncthreads_or(mark >= 0);
   const float w = weight;
-  const bool counts = __syncthreads_or(mark >= 0) && w != 0.f;
-  if (tid < kMaxTop) {
-    ids[tid] = mark;
-    logit[tid] = mark >= 0 && counts ? Elem<E>::load(row + mark) : 0.f;
-  }
-  if (mark >= e0 && mark < e1) {
-    if (mark < sp.head) {
-      atomicOr(&edges, 1u << mark);
-    } else if (mark >= tail) {
-      atomicOr(&edges, 1u << (16 + mark - tail));
+  const bool counts = any && w != 0.f;
+  // each token into the chain of the thread that meets it, in this slice or at its like in another;
+  // one that an earlier entry names is dropped (and stays in the chain, which does no harm)
+  float z = 0.f;
+  const bool within = mark >= sp.head && mark < tail;
+  if (counts && mark >= 0) {
+    z = Elem<E>::load(row + mark);               // needed at the end
+    if (within) {
+      const int at = (mark - sp.head) / N - v0 + 2 * sp.vecs / kThreads * kThreads + kThreads * 2;
+      next[tid] = atomicExch(&head[at % kThreads], tid);
+      if (mark >= e0 && mark < e1) atomicOr(&rounds[at % kThreads], 1u << (((mark - sp.head) / N - v0) / (U * kThreads) & 31));
     } else {
-      const int owner = ((mark - sp.head) / N - v0) % kThreads;
-      next[tid] = atomicExch(&head[owner], tid);
+      atomicOr(&edges, 1u << (mark < sp.head ? mark : 16 + mark - tail));
     }
   }
   __syncthreads();
+  if (counts && mark >= 0) {
+    bool again = false;
+    if (within) {
+      const int at = (mark - sp.head) / N - v0 + 2 * sp.vecs / kThreads * kThreads + kThreads * 2;
+      for (int j = head[at % kThreads]; j >= 0; j = next[j]) again = again || (j < tid && ids[j] == mark);
+    } else {
+      for (int j = 0; j < tid; ++j) again = again || ids[j] == mark;
+    }
+    if (again) mark = -1;
+  }
   float m = kNegInf, s = 0.f;
   if (counts) {
     const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
     const int mine = head[tid];
+    const uint32_t met = rounds[tid];
     uint64_t s2 = 0;
-    for (int i = v0 + tid; i < v1; i += U * kThreads) {
+    int n = 0;
+    for (int i = v0 + tid; i < v1; i += U * kThreads, ++n) {
       uint4 q[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) q[u] = i + u * kThreads < v1 ? src[i + u * kThreads] : Elem<E>::lowest();
-      for (int j = mine; j >= 0; j = next[j]) {
-        const int place = ids[j] - sp.head, p = place / N - i;
-        if (p < 0 || p >= U * kThreads) continue;
+      if (met >> (n & 31) & 1u)
+        for (int j = mine; j >= 0; j = next[j]) {
+          const int place = ids[j] - sp.head, p = place / N - i;
+          if (p < 0 || p >= U * kThreads) continue;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (p == u * kThreads) Elem<E>::strike(q[u], place % N);
-      }
+          for (int u = 0; u < U; ++u)
+            if (p == u * kThreads) Elem<E>::strike(q[u], place % N);
+        }
       absorb_exact<E, U>(m, s2, q, a.scale);
     }
     const float2 both = unpk2(s2);
@@ -906,7 +917,9 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int sli
   }
   merge_exact(m, s, a.scale);
   if (lane == 0) sh[warp] = make_float2(m, s);
-  __syncthreads();
+  if (tid < kMaxTop) logit[tid] = z;
+  __syncthreads();                               // (the ids are those of the chains until here)
+  if (tid < kMaxTop) ids[tid] = mark;
   if (warp == 0) {
     const float2 v = lane < kWarps ? sh[lane] : make_float2(kNegInf, 0.f);
     m = v.x;
@@ -932,6 +945,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int sli
     if (a.dlogits) zero_span<E, kThreads>(out, e0, e1, tid);
     return;
   }
+  __syncthreads();
   if (warp == 0) {
     Record r;
 #pragma unroll
@@ -984,23 +998,23 @@ __global__ void __launch_bounds__(kSumThreads) loss_kernel(const float *row_loss
   if (threadIdx.x == 0) *loss = s[0].value();
 }
 
-// How a row is cut for the held kernel: slices of at most four chunks (64 KB), so that a third of
-// the ring is always ahead; few rows are cut finer, down to 4 KB a block, as long as all blocks run
-// at once.  Cluster 0: eight blocks' rings do not hold it.
+// How a row is cut for the held kernel: into few slices; few rows are cut finer, down to 4 KB a block,
+// as long as all blocks run at once.  Cluster 0: eight blocks' rings do not hold it.
 struct HeldPlan {
   int cluster, slice;
 };
+template <typename E>
 HeldPlan plan_held(int64_t T, int64_t bytes) {
-  int64_t c = std::max<int64_t>(1, ceil_div(bytes, kSliceBytes));
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, Ring<E>::kSliceBytes));
   c = std::max(c, std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096));
   c = std::min<int64_t>(c, kMaxCluster);
   const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
-  if (slice > kSlots * kChunk) return {0, 0};
+  if (slice > Ring<E>::kSlots * Ring<E>::kChunk) return {0, 0};
   return {(int)c, (int)slice};
 }
 
 // Clusters of the held kernel that the device holds at once; the last answers are kept.
-int max_clusters(const void *kernel, int cluster) {
+int max_clusters(const void *kernel, int cluster, size_t smem) {
   struct Known {
     const void *kernel;
     int dev, cluster, n;
@@ -1016,7 +1030,7 @@ int max_clusters(const void *kernel, int cluster) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cluster);
   cfg.blockDim = dim3(kHeldThreads);
-  cfg.dynamicSmemBytes = kHeldSmem;
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = cluster;
@@ -1032,10 +1046,10 @@ int max_clusters(const void *kernel, int cluster) {
 template <typename E>
 cudaError_t launch_held(const Distill &r, const HeldPlan &plan, cudaStream_t st) {
   const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
-  cudaError_t e = ensure_smem(kernel, kHeldSmem);
+  cudaError_t e = ensure_smem(kernel, Ring<E>::kSmem);
   if (e != cudaSuccess) return e;
-  const int64_t clusters = std::min<int64_t>(r.T, max_clusters(kernel, plan.cluster));
-  return launch(held_kernel<E>, dim3((unsigned)(clusters * plan.cluster)), dim3(kHeldThreads), kHeldSmem, st,
+  const int64_t clusters = std::min<int64_t>(r.T, max_clusters(kernel, plan.cluster, Ring<E>::kSmem));
+  return launch(held_kernel<E>, dim3((unsigned)(clusters * plan.cluster)), dim3(kHeldThreads), Ring<E>::kSmem, st,
                 plan.cluster, true, HeldDistill{r, plan.cluster, plan.slice});
 }
 
@@ -1044,31 +1058,16 @@ int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_
 
 // Rows of up to kShortest bytes go to a warp's registers, four pieces a lane, up to kShort bytes
 // sixteen, and up to kShortTeam bytes to those of four warps.
-#ifndef SB1
-#define SB1 6
-#endif
-#ifndef SMID
-#define SMID 2
-#endif
-#ifndef SB2
-#define SB2 7
-#endif
-#ifndef SB3
-#define SB3 6
-#endif
-#ifndef SB4
-#define SB4 4
-#endif
 constexpr int64_t kShortest = 2 << 10, kShortTeam = 32 << 10;
 template <typename E>
 cudaError_t launch_distill(const Distill &r, int64_t bytes, cudaStream_t st) {
   const dim3 fourth((unsigned)ceil_div(r.T, 4)), each((unsigned)r.T);
-  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1, SB1>, fourth, dim3(128), 0, st, 1, true, r);
-  if (bytes <= (4 << 10) * SMID) return launch(short_kernel<E, 4, 4, SB2>, each, dim3(128), 0, st, 1, true, r);
-  if (bytes <= 16 << 10) return launch(short_kernel<E, 8, 4, SB3>, each, dim3(128), 0, st, 1, true, r);
-  if (bytes <= kShortTeam) return launch(short_kernel<E, 16, 4, SB4>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1, 6>, fourth, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 8 << 10) return launch(short_kernel<E, 4, 4, 8>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 16 << 10) return launch(short_kernel<E, 8, 4, 8>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= kShortTeam) return launch(short_kernel<E, 16, 4, 4>, each, dim3(128), 0, st, 1, true, r);
   if (r.dlogits)
-    if (const HeldPlan plan = plan_held(r.T, bytes); plan.cluster > 0) return launch_held<E>(r, plan, st);
+    if (const HeldPlan plan = plan_held<E>(r.T, bytes); plan.cluster > 0) return launch_held<E>(r, plan, st);
   const int64_t sms = num_sms();
   int c = 1;
   if (2 * r.T < sms)

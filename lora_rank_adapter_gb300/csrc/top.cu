@@ -410,8 +410,9 @@ __global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, 
     }
     sums.add(q, g, k);
   }
-  Sums rest = sums.sums();                             // of all but the block's K largest
+  Sums rest = no_sums();                               // of all but the block's K largest
   if (K == 0) {
+    rest = sums.sums();
     if (at_head || at_tail) rest.add(edge, k);
   } else {
     if (lane == 0 && hits > kWarpHits) sh.overflow = 1;
@@ -440,26 +441,27 @@ __global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, 
     }
     const uint64_t least = rank_list(sh.list, n, K, sh.best);
     if (tid == 0) sh.listed = sh.overflow = 0;
-    auto left = [&](float v, int id) {
-      if (!(v >= kLowest && key_of(v, id) >= least)) rest.add(v, k);
+    // a token that stays: not among the K largest
+    const float least_v = least ? key_value(least) : kLowest;
+    const int least_id = least ? key_id(least) : V;
+    auto stays = [&](float v, int id) { return !(v > least_v || (v == least_v && id <= least_id)); };
+    auto left = [&](uint4 q, int id) {
+      float v[N];
+      Elem<E>::unpack(q, v);
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (!stays(v[e], id + e)) Elem<E>::strike(q, e);
+      const uint4 one[1] = {q};
+      sums.add(one, Elem<E>::largest(one), k);
     };
     if (all) {
-      rest = no_sums();
-      for (int i = sl.v0 + tid; i < sl.v1; i += kThreads) {
-        float v[N];
-        Elem<E>::unpack(sl.pieces()[i], v);
-        for (int e = 0; e < N; ++e) left(v[e], sl.head + i * N + e);
-      }
+      sums = PairSums<E>();
+      for (int i = sl.v0 + tid; i < sl.v1; i += kThreads) left(sl.pieces()[i], sl.head + i * N);
     } else {
-      for (int j = lane; j < hits; j += 32) {
-        float v[N];
-        Elem<E>::unpack(sh.piece[warp][j], v);
-        const int id = sl.head + sh.at[warp][j] * N;
-#pragma unroll
-        for (int e = 0; e < N; ++e) left(v[e], id + e);
-      }
+      for (int j = lane; j < hits; j += 32) left(sh.piece[warp][j], sl.head + sh.at[warp][j] * N);
     }
-    if (at_head || at_tail) left(edge, edge_at);
+    rest = sums.sums();
+    if ((at_head || at_tail) && stays(edge, edge_at)) rest.add(edge, k);
   }
   warp_merge(rest, k);
   if (lane == 0) sh.part[0][warp] = rest;
