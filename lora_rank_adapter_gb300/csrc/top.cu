@@ -132,25 +132,27 @@ __device__ __forceinline__ void warp_merge(Sums &x, float k) {
 }
 
 // ----------------------------------------------------------------------------- the K largest
-constexpr int kTopThreads = 256;
-constexpr int kTopWarps = kTopThreads / 32;
 constexpr int kPer = 4;                                  // 16-byte pieces of a round for each thread
-constexpr int kTopBlocks = 4;                         // on an SM
-constexpr int kWarpHits = 1024 / kTopWarps;                           // pieces that a warp sets aside
 constexpr int kList = 1344;                              // tokens among which the K largest are found
+constexpr int kFew = 192;                                // that are compared with each other
 
+template <int kThreads>
 struct TopShared {
-  uint4 piece[kTopWarps][kWarpHits];
-  int at[kTopWarps][kWarpHits];
-  float tops[kTopThreads];
+  static constexpr int kWarps = kThreads / 32;
+  static constexpr int kWarpHits = kThreads == 256 ? 176 : 128;      // pieces that a warp sets aside
+  uint4 piece[kWarps][kWarpHits];
+  int at[kWarps][kWarpHits];
+  float tops[kThreads];
   uint64_t list[kList];
+  uint64_t few[kFew];
   uint64_t best[kMaxTop];
-  Sums part[2][kTopWarps];
+  Sums part[2][kWarps];
   unsigned count[256];           // of the digit's values, where all tokens are gone through
-  int hits[kTopWarps];
+  int hits[kWarps];
   float bar;
-  int listed, overflow;
+  int listed, overflow, kept;
   uint32_t digit, left;
+  uint64_t least;
   int64_t label;
 };
 // What the first block of a cluster gets from all.
@@ -162,16 +164,16 @@ struct TopGathered {
 
 // What a token has to reach to be one of the K largest: a value that K of the threads' largest
 // values reach, and few more.  By a warp; at least the lowest finite value.  Each of kEach values
-// of a lane stands for kTopWarps / kEach threads, the largest of theirs: the fewer, the shorter the
+// of a lane stands for kWarps / kEach threads, the largest of theirs: the fewer, the shorter the
 // search, and the more threads reach what it finds (n ln(n / (n - K)) of n values, not K).
-template <int kEach>
+template <int kEach, int kWarps>
 __device__ __forceinline__ float bar_among(const float *tops, int K) {
   uint32_t o[kEach], hi = 0, lo = 0xffffu;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     float v = tops[lane_id() + 32 * i];
 #pragma unroll
-    for (int j = i + kEach; j < kTopWarps; j += kEach) v = fmaxf(v, tops[lane_id() + 32 * j]);
+    for (int j = i + kEach; j < kWarps; j += kEach) v = fmaxf(v, tops[lane_id() + 32 * j]);
     o[i] = order_of(v) >> 16;
     hi = max(hi, o[i]);
     lo = min(lo, o[i]);
@@ -190,43 +192,71 @@ __device__ __forceinline__ float bar_among(const float *tops, int K) {
   }
   return value_of((t < 0x80u ? 0x80u : t) << 16);        // 0x80 << 16: the lowest finite value
 }
+template <int kWarps>
 __device__ __forceinline__ float bar_of(const float *tops, int K) {
-  if (K <= 16) return bar_among<1>(tops, K);
-  if (K <= 32) return bar_among<2>(tops, K);
-  if (K <= 64) return bar_among<4>(tops, K);
-  return bar_among<8>(tops, K);
+  if (K <= 16) return bar_among<1, kWarps>(tops, K);
+  if (K <= 32) return bar_among<2, kWarps>(tops, K);
+  if (kWarps == 4 || K <= 64) return bar_among<4, kWarps>(tops, K);
+  return bar_among<kWarps, kWarps>(tops, K);
 }
 
 // The K largest of n keys into best, in order, the rest of it 0.  Returns the least key
-// that belongs to them.  Each key is compared with all by as many lanes as there are.
-__device__ __forceinline__ uint64_t rank_list(const uint64_t *list, int n, int K, uint64_t *best) {
+// that belongs to them.  Each key is compared with all by as many lanes as there are; of many
+// keys, those below one that K of them reach are left out first.
+template <int kThreads>
+__device__ __forceinline__ uint64_t rank_list(TopShared<kThreads> &sh, int n, int K) {
+  const uint64_t *list = sh.list;
+  if (n > kFew) {
+    if (threadIdx.x < 32) {
+      const int lane = lane_id();
+      uint64_t t = 0;
+      for (int b = 63; b >= 0; --b) {
+        const uint64_t c = t | 1ull << b;
+        int reach = 0;
+        for (int i = lane; i < n; i += 32) reach += list[i] >= c;
+        reach = __reduce_add_sync(0xffffffffu, reach);
+        if (reach >= K) t = c;
+        if (reach >= K && reach <= K + K / 4 + 16) break;
+      }
+      if (lane == 0) {
+        sh.least = t;
+        sh.kept = 0;
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads)
+      if (list[i] >= sh.least) sh.few[atomicAdd(&sh.kept, 1)] = list[i];
+    __syncthreads();
+    list = sh.few;
+    n = sh.kept;
+  }
   int g = 1;
-  while (g < 32 && 2 * g * n <= kTopThreads) g *= 2;
+  while (g < 32 && 2 * g * n <= kThreads) g *= 2;
   const int sub = threadIdx.x & (g - 1);
-  for (int from = 0; from < n; from += kTopThreads / g) {
+  for (int from = 0; from < n; from += kThreads / g) {
     const int i = from + (int)threadIdx.x / g;
     const uint64_t key = i < n ? list[i] : 0;
     int rank = 0;
     for (int j = sub; j < n; j += g) rank += list[j] > key;
     for (int o = g >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
-    if (sub == 0 && i < n && rank < K) best[rank] = key;
+    if (sub == 0 && i < n && rank < K) sh.best[rank] = key;
   }
-  for (int i = n + (int)threadIdx.x; i < K; i += kTopThreads) best[i] = 0;
+  for (int i = n + (int)threadIdx.x; i < K; i += kThreads) sh.best[i] = 0;
   __syncthreads();
-  return K > 0 && n >= K ? best[K - 1] : 0;
+  return K > 0 && n >= K ? sh.best[K - 1] : 0;
 }
 
 // The K largest of elements [e0, e1) whatever they are: digits of eight bits from the
 // highest on, the elements read again for each, then those above the K-th, and the
 // first ones that equal it.  Into list; returns how many.
-template <typename E>
-__device__ __noinline__ int select_all(TopShared &sh, const E *row, int e0, int e1, int K) {
+template <typename E, int kThreads>
+__device__ __noinline__ int select_all(TopShared<kThreads> &sh, const E *row, int e0, int e1, int K) {
   const int tid = threadIdx.x;
   uint32_t prefix = 0, left = K;      // the K-th largest's digits so far, its rank among those that share them
   for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kTopThreads) sh.count[i] = 0;
+    for (int i = tid; i < 256; i += kThreads) sh.count[i] = 0;
     __syncthreads();
-    for (int i = e0 + tid; i < e1; i += kTopThreads) {
+    for (int i = e0 + tid; i < e1; i += kThreads) {
       const float v = Elem<E>::load(row + i);
       const uint32_t o = order_of(v);
       if (v >= kLowest && (shift == 24 || o >> (shift + 8) == prefix >> (shift + 8)))
@@ -247,7 +277,7 @@ __device__ __noinline__ int select_all(TopShared &sh, const E *row, int e0, int 
   }
   if (tid == 0) sh.listed = 0;
   __syncthreads();
-  for (int i = e0 + tid; i < e1; i += kTopThreads) {
+  for (int i = e0 + tid; i < e1; i += kThreads) {
     const float v = Elem<E>::load(row + i);
     if (v >= kLowest && order_of(v) > prefix) {
       const int n = atomicAdd(&sh.listed, 1);
@@ -257,7 +287,7 @@ __device__ __noinline__ int select_all(TopShared &sh, const E *row, int e0, int 
   __syncthreads();
   int have = min(sh.listed, K);
   __syncthreads();
-  for (int from = e0; from < e1 && have < K; from += kTopThreads) {
+  for (int from = e0; from < e1 && have < K; from += kThreads) {
     const int i = from + tid;
     float v = kNegInf;
     if (i < e1) v = Elem<E>::load(row + i);
@@ -266,7 +296,7 @@ __device__ __noinline__ int select_all(TopShared &sh, const E *row, int e0, int 
     if (lane_id() == 0) sh.hits[tid >> 5] = __popc(mask);
     __syncthreads();
     int before = have, all = 0;
-    for (int w = 0; w < kTopThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < tid >> 5) before += sh.hits[w];
       all += sh.hits[w];
     }
@@ -292,7 +322,7 @@ struct TopRow {
 };
 
 // A block's slice of a row.
-template <typename E>
+template <typename E, int kThreads>
 struct TopSlice {
   const E *row;
   int head, vecs, v0, v1, rounds;
@@ -303,7 +333,7 @@ struct TopSlice {
     vecs = sp.vecs;
     v0 = min(rank * slice, vecs);
     v1 = min(v0 + slice, vecs);
-    rounds = max(1, (v1 - v0 + kPer * kTopThreads - 1) / (kPer * kTopThreads));
+    rounds = max(1, (v1 - v0 + kPer * kThreads - 1) / (kPer * kThreads));
   }
   __device__ __forceinline__ const uint4 *pieces() const { return reinterpret_cast<const uint4 *>(row + head); }
 };
@@ -321,12 +351,13 @@ __device__ __forceinline__ void top_nothing(const TopRow &a, int64_t t, int lane
   if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
 }
 
-template <typename E, bool kSplit>
-__global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, int clusters, int slice) {
-  constexpr int N = Elem<E>::kVec, kThreads = kTopThreads;
+template <typename E, int kThreads, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) top_kernel(TopRow a, int clusters, int slice) {
+  using Shared = TopShared<kThreads>;
+  constexpr int N = Elem<E>::kVec, kTopWarps = kThreads / 32, kWarpHits = Shared::kWarpHits;
   using Peak = typename Elem<E>::Peak;
   extern __shared__ __align__(16) unsigned char dynamic[];
-  TopShared &sh = *reinterpret_cast<TopShared *>(dynamic);
+  Shared &sh = *reinterpret_cast<Shared *>(dynamic);
   const int C = kSplit ? clusters : 1;
   const int rank = (int)(blockIdx.x % C), tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, K = a.K, V = (int)a.V;
   const float k = a.scale.k;
@@ -347,7 +378,7 @@ __global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, 
     if (warp == 0) top_nothing(a, t, lane);
     return;
   }
-  TopSlice<E> sl(a, t, rank, slice);
+  TopSlice<E, kThreads> sl(a, t, rank, slice);
   if (!live) sl.v1 = sl.v0;
   const int tail = sl.head + sl.vecs * N;
   float picked = 0.f;
@@ -382,7 +413,7 @@ __global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, 
         sh.tops[tid] = top;
         __syncthreads();
         if (warp == 0) {
-          const float b = bar_of(sh.tops, K);
+          const float b = bar_of<kTopWarps>(sh.tops, K);
           if (lane == 0) sh.bar = b;
         }
         __syncthreads();
@@ -437,9 +468,9 @@ __global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, 
     const bool all = sh.overflow || n > kList;         // more tokens than can be set aside
     if (all) {
       __syncthreads();
-      n = select_all<E>(sh, sl.row, rank == 0 ? 0 : sl.head + sl.v0 * N, rank == C - 1 ? V : sl.head + sl.v1 * N, K);
+      n = select_all<E, kThreads>(sh, sl.row, rank == 0 ? 0 : sl.head + sl.v0 * N, rank == C - 1 ? V : sl.head + sl.v1 * N, K);
     }
-    const uint64_t least = rank_list(sh.list, n, K, sh.best);
+    const uint64_t least = rank_list<kThreads>(sh, n, K);
     if (tid == 0) sh.listed = sh.overflow = 0;
     // a token that stays: not among the K largest
     const float least_v = least ? key_value(least) : kLowest;
@@ -473,7 +504,7 @@ __global__ void __launch_bounds__(kTopThreads, kTopBlocks) top_kernel(TopRow a, 
   }
   if (kSplit) {
     // every block's K largest and sums to the first block, which finds the K largest of all
-    TopGathered &all = *reinterpret_cast<TopGathered *>(dynamic + sizeof(TopShared));
+    TopGathered &all = *reinterpret_cast<TopGathered *>(dynamic + sizeof(Shared));
     __syncwarp();
     cluster_wait();
     uint32_t to, part;
@@ -698,12 +729,12 @@ TopRow row_of(const TopArgs &a) {
   return r;
 }
 
-template <typename E, bool kSplit>
+template <typename E, int kThreads, bool kSplit>
 cudaError_t launch_top_as(const TopRow &r, int C, int slice, cudaStream_t st) {
-  constexpr size_t smem = sizeof(TopShared) + (kSplit ? sizeof(TopGathered) : 0);
-  cudaError_t e = ensure_smem(reinterpret_cast<const void *>(top_kernel<E, kSplit>), smem);
+  constexpr size_t smem = sizeof(TopShared<kThreads>) + (kSplit ? sizeof(TopGathered) : 0);
+  cudaError_t e = ensure_smem(reinterpret_cast<const void *>(top_kernel<E, kThreads, kSplit>), smem);
   if (e != cudaSuccess) return e;
-  return launch(top_kernel<E, kSplit>, dim3((unsigned)(r.T * C)), dim3(kTopThreads), smem, st, C, true, r, C, slice);
+  return launch(top_kernel<E, kThreads, kSplit>, dim3((unsigned)(r.T * C)), dim3(kThreads), smem, st, C, true, r, C, slice);
 }
 
 template <typename E>
@@ -711,9 +742,10 @@ cudaError_t launch_top(const TopRow &r, int64_t bytes, cudaStream_t st) {
   const int64_t sms = num_sms();
   if (2 * r.T < sms && bytes > 16 << 10) {
     const int c = (int)std::min<int64_t>({4 * sms / r.T, bytes / (4 << 10), kMaxCluster});
-    return launch_top_as<E, true>(r, c, slice_of(bytes, c), st);
+    return launch_top_as<E, 256, true>(r, c, slice_of(bytes, c), st);
   }
-  return launch_top_as<E, false>(r, 1, slice_of(bytes, 1), st);
+  if (bytes <= 16 << 10) return launch_top_as<E, 128, false>(r, 1, slice_of(bytes, 1), st);
+  return launch_top_as<E, 256, false>(r, 1, slice_of(bytes, 1), st);
 }
 
 // Blocks for each row of the gradient pass, as for the gradient of label log-probabilities.
