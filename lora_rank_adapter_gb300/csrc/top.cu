@@ -352,7 +352,7 @@ __device__ __forceinline__ void top_nothing(const TopRow &a, int64_t t, int lane
 }
 
 template <typename E, int kThreads, bool kSplit>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) top_kernel(TopRow a, int clusters, int slice) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 8) top_kernel(TopRow a, int clusters, int slice) {
   using Shared = TopShared<kThreads>;
   constexpr int N = Elem<E>::kVec, kTopWarps = kThreads / 32, kWarpHits = Shared::kWarpHits;
   using Peak = typename Elem<E>::Peak;
@@ -393,14 +393,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) top_kernel(TopRow a
   float top = kNegInf, bar = INFINITY;                 // a thread's largest value so far; what a token has to reach
   int hits = 0;                                        // the warp's
   int next = 1;                                        // the round that raises the bar next
+  // a round's pieces are on their way while the one before it is gone through
+  uint4 ahead[kPer];
+  auto load = [&](int n) {
+    const int i = sl.v0 + n * kPer * kThreads + tid;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) ahead[u] = i + u * kThreads < sl.v1 ? sl.pieces()[i + u * kThreads] : Elem<E>::lowest();
+  };
+  constexpr bool kAhead = kThreads == 256;             // (short rows: more blocks on an SM instead)
+  if (kAhead) load(0);
   for (int n = 0; n < sl.rounds; ++n) {
     const int i = sl.v0 + n * kPer * kThreads + tid;
     uint4 q[kPer];
     Peak peak[kPer];
+    if (!kAhead) load(n);
 #pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      q[u] = i + u * kThreads < sl.v1 ? sl.pieces()[i + u * kThreads] : Elem<E>::lowest();
-    }
+    for (int u = 0; u < kPer; ++u) q[u] = ahead[u];
+    if (kAhead && n + 1 < sl.rounds) load(n + 1);
 #pragma unroll
     for (int u = 0; u < kPer; ++u) peak[u] = Elem<E>::peak(q[u]);
     auto largest = [&] {
