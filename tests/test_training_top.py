@@ -174,6 +174,7 @@ def test_masks_infinities_and_nan(V, dtype):
     x[9, :-1] = -INF                # one column left, and it is the label
     labels[9] = V - 1
     x[10, :] = torch.finfo(dtype).max      # equal and huge: uniform
+    x[11, ::3], x[11, 1::3], x[11, 2::3] = low, -INF, low * 0.75      # nothing but masks of three kinds
     K = 9
     got, want = call(x, K, labels), oracle(x, K, labels)
     check(got, want, torch.tensor([0, 1, 2, 6, 7, 8, 9, 10, 11]))
@@ -189,6 +190,18 @@ def test_masks_infinities_and_nan(V, dtype):
         assert bool(d[[7, 8]].eq(0).all()) and bool(d[[3, 4, 5]].isnan().any(1).all())
         assert bool(d[[0, 1, 2, 6, 9, 10, 11]].isfinite().all())
         assert bool(d[0, 5:].eq(0).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("temp", [1e-3, 0.02, 50.0, 1e20, 3e37])
+def test_far_temperatures(dtype, temp):
+    """Rows whose exponentials are all but one zero, and rows that are all but uniform, masks among them."""
+    _, x, labels = make(6, 3001, dtype, seed=12)
+    x[1::2, 5::7] = -INF
+    x[2, 9::11] = torch.finfo(dtype).min
+    x[4] *= 1e30
+    x[5, 1000:] = -INF
+    check(call(x, 20, labels, temp), oracle(x, 20, labels, temp))
 
 
 def oracle_gradient(w, x, labels, ids, gl, gh, gt, temp):
