@@ -397,16 +397,15 @@ constexpr int kWorkers = 8;                              // warps that sum and w
 constexpr int kWork = 32 * kWorkers;
 constexpr int kHeldThreads = kWork + 64;                 // and the loader's warp, and the records'
 constexpr int kHeldBlocks = 2;
-// Chunks of kPer 16-byte pieces for each thread, kSlots of them in a block's ring, and as much of a row
-// for a block where eight blocks suffice.  bf16, bound by its instructions, gains from long chunks and
-// three blocks for a row of 256 KB; fp32, bound by its bytes, from chunks on their way ahead.  Of the
-// copy rate, 28 KB x 3 (slices of 84 KB) / 16 KB x 6 (64 KB): rows of 128256 bf16 83 % / 77, of 200000
-// 81 / 64, of 50257 66 / 64; rows of 32000 fp32 81 / 92, of 128256 88 / 92.
+// Chunks of kPer 16-byte pieces for each thread, kSlots of them in a block's ring.  bf16, bound by its
+// instructions, gains from long chunks; fp32, bound by its bytes, from chunks on their way ahead.  Of the
+// copy rate, 28 KB x 3 / 16 KB x 6: rows of 128256 bf16 83 % / 76, of 200000 81 / 80, of 100000 70 / 70;
+// rows of 32000 fp32 81 / 91, of 128256 88 / 89.
 template <typename E>
 struct Ring {
   static constexpr bool kLong = sizeof(E) == 2;
   static constexpr int kPer = kLong ? 7 : 4, kSlots = kLong ? 3 : 6, kChunk = kPer * kWork;
-  static constexpr int kSliceBytes = (kLong ? 84 : 64) << 10, kSmem = kSlots * kChunk * 16;
+  static constexpr int kSmem = kSlots * kChunk * 16;
 };
 constexpr int kAhead = 4;                                // records made up ahead
 
@@ -998,21 +997,6 @@ __global__ void __launch_bounds__(kSumThreads) loss_kernel(const float *row_loss
   if (threadIdx.x == 0) *loss = s[0].value();
 }
 
-// How a row is cut for the held kernel: into few slices; few rows are cut finer, down to 4 KB a block,
-// as long as all blocks run at once.  Cluster 0: eight blocks' rings do not hold it.
-struct HeldPlan {
-  int cluster, slice;
-};
-template <typename E>
-HeldPlan plan_held(int64_t T, int64_t bytes) {
-  int64_t c = std::max<int64_t>(1, ceil_div(bytes, Ring<E>::kSliceBytes));
-  c = std::max(c, std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096));
-  c = std::min<int64_t>(c, kMaxCluster);
-  const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
-  if (slice > Ring<E>::kSlots * Ring<E>::kChunk) return {0, 0};
-  return {(int)c, (int)slice};
-}
-
 // Clusters of the held kernel that the device holds at once; the last answers are kept.
 int max_clusters(const void *kernel, int cluster, size_t smem) {
   struct Known {
@@ -1038,9 +1022,33 @@ int max_clusters(const void *kernel, int cluster, size_t smem) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+  if (ensure_smem(kernel, smem) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1)
+    return 1;
   known[used++ % 32] = {kernel, dev, cluster, n};
   return n;
+}
+
+// How a row is cut for the held kernel: over the fewest blocks whose rings hold it, or one more where
+// that brings more blocks to work (clusters of seven leave many of them out); few rows are cut finer,
+// down to 4 KB a block, as long as all blocks run at once.  Cluster 0: eight blocks' rings do not hold it.
+struct HeldPlan {
+  int cluster, slice;
+};
+template <typename E>
+HeldPlan plan_held(int64_t T, int64_t bytes) {
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, Ring<E>::kSmem));
+  const int64_t fine = std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096);
+  const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
+  if (fine > c) {
+    c = std::min<int64_t>(fine, kMaxCluster);
+  } else if (c > 4 && c < kMaxCluster) {
+    auto blocks = [&](int64_t n) { return n * max_clusters(kernel, (int)n, Ring<E>::kSmem); };
+    if (16 * blocks(c + 1) > 17 * blocks(c)) ++c;
+  }
+  c = std::min<int64_t>(c, kMaxCluster);
+  const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
+  if (slice > Ring<E>::kSlots * Ring<E>::kChunk) return {0, 0};
+  return {(int)c, (int)slice};
 }
 
 template <typename E>

@@ -14,6 +14,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -132,7 +133,6 @@ __device__ __forceinline__ void warp_merge(Sums &x, float k) {
 }
 
 // ----------------------------------------------------------------------------- the K largest
-constexpr int kPer = 4;                                  // 16-byte pieces of a round for each thread
 constexpr int kList = 1344;                              // tokens among which the K largest are found
 constexpr int kFew = 192;                                // that are compared with each other
 
@@ -155,10 +155,9 @@ struct TopShared {
   uint64_t least;
   int64_t label;
 };
-// What the first block of a cluster gets from all.
+// What a block of a cluster gets from all: their K largest, and the first block their sums.
 struct TopGathered {
-  uint64_t best[kMaxCluster * kMaxTop];
-  int rank[kMaxCluster * kMaxTop];
+  uint64_t best[kMaxCluster][kMaxTop];
   Sums part[kMaxCluster];
 };
 
@@ -322,7 +321,7 @@ struct TopRow {
 };
 
 // A block's slice of a row.
-template <typename E, int kThreads>
+template <typename E, int kPieces>      // of a round
 struct TopSlice {
   const E *row;
   int head, vecs, v0, v1, rounds;
@@ -333,7 +332,7 @@ struct TopSlice {
     vecs = sp.vecs;
     v0 = min(rank * slice, vecs);
     v1 = min(v0 + slice, vecs);
-    rounds = max(1, (v1 - v0 + kPer * kThreads - 1) / (kPer * kThreads));
+    rounds = max(1, (v1 - v0 + kPieces - 1) / kPieces);
   }
   __device__ __forceinline__ const uint4 *pieces() const { return reinterpret_cast<const uint4 *>(row + head); }
 };
@@ -352,9 +351,10 @@ __device__ __forceinline__ void top_nothing(const TopRow &a, int64_t t, int lane
 }
 
 template <typename E, int kThreads, bool kSplit>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 8) top_kernel(TopRow a, int clusters, int slice) {
+__global__ void __launch_bounds__(kThreads, kSplit ? 2 : kThreads == 256 ? 3 : 8) top_kernel(TopRow a, int clusters, int slice) {
   using Shared = TopShared<kThreads>;
   constexpr int N = Elem<E>::kVec, kTopWarps = kThreads / 32, kWarpHits = Shared::kWarpHits;
+  constexpr int kPer = kSplit ? 8 : 4;                   // 16-byte pieces of a round for each thread: a cut row takes one or two
   using Peak = typename Elem<E>::Peak;
   extern __shared__ __align__(16) unsigned char dynamic[];
   Shared &sh = *reinterpret_cast<Shared *>(dynamic);
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 8) top_kernel(
     if (warp == 0) top_nothing(a, t, lane);
     return;
   }
-  TopSlice<E, kThreads> sl(a, t, rank, slice);
+  TopSlice<E, kPer * kThreads> sl(a, t, rank, slice);
   if (!live) sl.v1 = sl.v0;
   const int tail = sl.head + sl.vecs * N;
   float picked = 0.f;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 8) top_kernel(
 #pragma unroll
     for (int u = 0; u < kPer; ++u) ahead[u] = i + u * kThreads < sl.v1 ? sl.pieces()[i + u * kThreads] : Elem<E>::lowest();
   };
-  constexpr bool kAhead = kThreads == 256;             // (short rows: more blocks on an SM instead)
+  constexpr bool kAhead = kThreads == 256 && !kSplit;  // (short rows: more blocks on an SM instead)
   if (kAhead) load(0);
   for (int n = 0; n < sl.rounds; ++n) {
     const int i = sl.v0 + n * kPer * kThreads + tid;
@@ -413,7 +413,10 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 8) top_kernel(
 #pragma unroll
     for (int u = 0; u < kPer; ++u) peak[u] = Elem<E>::peak(q[u]);
     auto largest = [&] {
-      return Elem<E>::value(Elem<E>::higher(Elem<E>::higher(peak[0], peak[1]), Elem<E>::higher(peak[2], peak[3])));
+      Peak p = Elem<E>::higher(Elem<E>::higher(peak[0], peak[1]), Elem<E>::higher(peak[2], peak[3]));
+#pragma unroll
+      for (int u = 4; u < kPer; ++u) p = Elem<E>::higher(p, peak[u]);
+      return Elem<E>::value(p);
     };
     float g = largest();
     if (K > 0) {
@@ -512,57 +515,84 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 8) top_kernel(
     warp_merge(rest, k);
   }
   if (kSplit) {
-    // every block's K largest and sums to the first block, which finds the K largest of all
+    // Every block's K largest to all blocks; each then ranks its own among all, a lane for each list, and
+    // sends what is among the K largest to its place in the first block, the rest of its sums with it.
     TopGathered &all = *reinterpret_cast<TopGathered *>(dynamic + sizeof(Shared));
+    auto at = [](const void *local, int cta) {
+      uint32_t remote;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(cta));
+      return remote;
+    };
+    __syncwarp();
+    cluster_wait();                                      // all blocks run
+    for (int i = tid; i < kMaxCluster * kMaxTop; i += kThreads) {
+      const int c = i % kMaxCluster, j = i / kMaxCluster;
+      if (j >= K) break;
+      if (c < C) asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at(&all.best[rank][j], c)), "l"(sh.best[j]) : "memory");
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (rank == 0) {                                     // (its own list is in all.best)
+      for (int i = tid; i < K; i += kThreads) sh.best[i] = 0;
+    }
+    __syncwarp();
+    cluster_arrive();                                    // the first block's list is clear
+    static_assert(kMaxCluster == 8, "eight lanes for each token");
+    Sums beyond = no_sums();                             // of this block's tokens that are not among the K largest
+    uint64_t mine[kMaxTop * kMaxCluster / kThreads];
+    int place[kMaxTop * kMaxCluster / kThreads];
+#pragma unroll
+    for (int n = 0; n < kMaxTop * kMaxCluster / kThreads; ++n) {
+      const int j = (n * kThreads + tid) / kMaxCluster, c = tid % kMaxCluster;
+      mine[n] = 0;
+      place[n] = 0;
+      if (n * kThreads / kMaxCluster >= K) continue;     // the same for the whole block
+      if (j < K) mine[n] = all.best[rank][j];
+      if (c == rank) {
+        place[n] = j;
+      } else if (c < C && mine[n]) {
+        const uint64_t *list = all.best[c];
+        int lo = 0, hi = K;                              // those before lo are above, those from hi on are not
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (list[mid] > mine[n]) lo = mid + 1; else hi = mid;
+        }
+        place[n] = lo;
+      }
+#pragma unroll
+      for (int o = 1; o < kMaxCluster; o *= 2) place[n] += __shfl_xor_sync(0xffffffffu, place[n], o);
+      if (mine[n] && c == 0 && place[n] >= K) beyond.add(key_value(mine[n]), k);
+    }
+    warp_merge(beyond, k);
+    if (lane == 0) sh.part[1][warp] = beyond;
+    __syncthreads();
+    if (warp == 0) {
+      beyond = no_sums();
+      if (lane < kTopWarps) beyond = sh.part[1][lane];
+      warp_merge(beyond, k);
+      rest.add(beyond, k);
+    }
     __syncwarp();
     cluster_wait();
-    uint32_t to, part;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(to) : "r"(smem_u32(all.best + rank * K)));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(part) : "r"(smem_u32(all.part + rank)));
-    for (int i = tid; i < K; i += kThreads)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8 * i), "l"(sh.best[i]) : "memory");
+#pragma unroll
+    for (int n = 0; n < kMaxTop * kMaxCluster / kThreads; ++n)
+      if (mine[n] && tid % kMaxCluster == 0 && place[n] < K)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at(&sh.best[place[n]], 0)), "l"(mine[n]) : "memory");
     if (tid == 0) {
+      const uint32_t part = at(&all.part[rank], 0);
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part), "f"(rest.m) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 4), "f"(rest.s) : "memory");
       asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(part + 8), "f"(rest.w) : "memory");
     }
-    if (rank == 0)
-      for (int i = tid; i < C * K; i += kThreads) all.rank[i] = i % K;
     __syncwarp();
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;                               // nothing is sent from here on
-    {
-      rest = no_sums();
-      // a token's rank: its place in its own list, and those above it in each of the others
-      for (int i = tid; i < C * C * K; i += kThreads) {
-        const int c = i / (C * K), own = i - c * (C * K);
-        const uint64_t key = all.best[own];
-        if (key == 0 || own / K == c) continue;
-        const uint64_t *list = all.best + c * K;
-        int lo = 0, hi = K;                            // those before lo are above, those from hi on are not
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (list[mid] > key) lo = mid + 1; else hi = mid;
-        }
-        if (lo > 0) atomicAdd(&all.rank[own], lo);
-      }
-      for (int i = tid; i < K; i += kThreads) sh.best[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < C * K; i += kThreads) {
-        const uint64_t key = all.best[i];
-        if (key == 0) continue;
-        if (all.rank[i] < K) sh.best[all.rank[i]] = key; else rest.add(key_value(key), k);
-      }
-      if (tid < C) rest.add(all.part[tid], k);
+    rest = no_sums();
+    if (warp == 0) {
+      if (lane < C) rest = all.part[lane];
       warp_merge(rest, k);
-      if (lane == 0) sh.part[1][warp] = rest;
-      __syncthreads();
-      rest = no_sums();
-      if (warp == 0) {
-        if (lane < kTopWarps) rest = sh.part[1][lane];
-        warp_merge(rest, k);
-      }
     }
   }
   if (warp == 0 && rank == 0 && !live) top_nothing(a, t, lane);
@@ -746,13 +776,48 @@ cudaError_t launch_top_as(const TopRow &r, int C, int slice, cudaStream_t st) {
   return launch(top_kernel<E, kThreads, kSplit>, dim3((unsigned)(r.T * C)), dim3(kThreads), smem, st, C, true, r, C, slice);
 }
 
+// Clusters of `size` blocks of the kernel for cut rows that the device holds at once; the last answers
+// are kept.
+template <typename E>
+int clusters_at_once(int size) {
+  struct Known {
+    int dev, size, n;
+  };
+  static Known known[32];
+  static int used = 0;
+  static std::mutex mu;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known &k : known)
+    if (k.n > 0 && k.dev == dev && k.size == size) return k.n;
+  constexpr size_t smem = sizeof(TopShared<256>) + sizeof(TopGathered);
+  const void *kernel = reinterpret_cast<const void *>(top_kernel<E, 256, true>);
+  if (ensure_smem(kernel, smem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+  known[used++ % 32] = {dev, size, n};
+  return n;
+}
+
+// A row goes to one block, of fewer threads where it is short; rows that leave SMs idle that way are cut
+// over the blocks of a cluster, down to 4 KB a block, one block an SM: rows of 128256 bf16, K = 20, one block
+// an SM / two: 32 rows 10.3 us / 13.5, 76 rows 12.6 / 13.8; 97 rows over three blocks each 20.5, over one 15.2.
 template <typename E>
 cudaError_t launch_top(const TopRow &r, int64_t bytes, cudaStream_t st) {
-  const int64_t sms = num_sms();
-  if (2 * r.T < sms && bytes > 16 << 10) {
-    const int c = (int)std::min<int64_t>({4 * sms / r.T, bytes / (4 << 10), kMaxCluster});
-    return launch_top_as<E, 256, true>(r, c, slice_of(bytes, c), st);
-  }
+  if (bytes > 8 << 10)
+    for (int c = (int)std::min<int64_t>({kMaxCluster, bytes / (4 << 10), num_sms() / r.T}); c > 1; --c)
+      if (r.T <= clusters_at_once<E>(c)) return launch_top_as<E, 256, true>(r, c, slice_of(bytes, c), st);
   if (bytes <= 16 << 10) return launch_top_as<E, 128, false>(r, 1, slice_of(bytes, 1), st);
   return launch_top_as<E, 256, false>(r, 1, slice_of(bytes, 1), st);
 }
