@@ -1,11 +1,13 @@
-"""Fine-tunes the LoRA adapters of a small frozen model on preference pairs, or on rollouts
-with advantages: logits -> loss with its gradient -> adapter gradients -> AdamW.
+"""Fine-tunes the LoRA adapters of a small frozen model on preference pairs, on rollouts with
+advantages, or on a teacher's record: logits -> loss with its gradient -> adapter gradients -> AdamW.
 
-  python examples/preference_finetune.py [--loss preference|policy] [--steps 30] [--state-bits 8|32]
+  python examples/preference_finetune.py [--loss preference|policy|distill] [--steps 30] [--state-bits 8|32]
+                                          [--entropy-bonus 0.001]
 
 The model is a frozen random embedding, a hidden layer and an output layer, both of the latter
-with an adapter (lora_linear).  The reference model is the same with the adapters off.  Inputs
-are random sequences made from a seed.
+with an adapter (lora_linear).  The reference model is the same with the adapters off; the teacher
+the same with adapters of its own, of which the record holds the 32 most probable tokens of each
+row and the mass of the rest.  Inputs are random sequences made from a seed.
 """
 import argparse
 import os
@@ -59,9 +61,10 @@ def batch(gen, device, sequences, longest=40, prompt=6):
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--loss", choices=("preference", "policy"), default="preference")
+    ap.add_argument("--loss", choices=("preference", "policy", "distill"), default="preference")
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--state-bits", type=int, choices=(8, 32), default=8)
+    ap.add_argument("--entropy-bonus", type=float, default=0.0, help="of the policy loss")
     ap.add_argument("--seed", type=int, default=0)
     args = ap.parse_args(argv)
     device = "cuda:0"
@@ -79,14 +82,25 @@ def main(argv=None):
     advantages = torch.randn(8, generator=gen, device=device)[of]
     per_sequence = torch.zeros(8, device=device).index_add_(0, of, counted)
     weights = 1.0 / (8 * per_sequence.clamp(min=1))[of]
+    if args.loss == "distill":               # the teacher: other adapters on the same frozen weights
+        teacher = Model(device, torch.Generator(device).manual_seed(args.seed))
+        with torch.no_grad():
+            for _, B in teacher.adapters:
+                B.normal_(0.0, 0.3, generator=gen)
+            record = torch_ops.top_logps(teacher.logits(ids), 32)
+        weights = counted / counted.sum()
     losses = []
     for step in range(args.steps):
         logits = model.logits(ids)
         if args.loss == "preference":
             loss, _, _ = torch_ops.preference_loss(logits, labels, cu, ref_seq, beta=0.1)
-        else:
+        elif args.loss == "policy":
             loss, _, _ = torch_ops.policy_loss(logits, labels, ref_tok, advantages, weights, ref_logps=ref_tok,
                                                clip_high=0.28, kl_beta=0.02)
+            if args.entropy_bonus:
+                loss = loss - args.entropy_bonus * (weights * torch_ops.top_logps(logits, 0, labels).entropy).sum()
+        else:
+            loss, _ = torch_ops.distill_loss(logits, record.ids, record.logps, record.rest, weights)
         opt.zero_grad()
         loss.backward()
         opt.step()

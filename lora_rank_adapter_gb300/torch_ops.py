@@ -16,19 +16,22 @@ the fused pair forward_h_ / backward_ex:
 with gradients dx = scale * dout @ B^T @ A^T, dA = scale * x^T @ (dout @ B^T),
 dB = scale * (x @ A)^T @ dout and dbase = dout.
 
-`token_logps`, `preference_loss` and `policy_loss` are the differentiable forms of the
-loss operators of `training`, and `AdamW` an optimizer on lora_grad_norm / lora_adamw:
+`token_logps`, `top_logps`, `preference_loss`, `policy_loss` and `distill_loss` are the
+differentiable forms of the loss operators of `training`, and `AdamW` an optimizer on
+lora_grad_norm / lora_adamw:
     loss, pair_loss, seq_logps = preference_loss(logits, labels, cu_seqlens, ref_logps, beta=0.1)
     loss.backward(); optimizer.step()
+    record = top_logps(teacher_logits, 64)
+    loss, row_loss = distill_loss(logits, record.ids, record.logps, record.rest)
 The losses form their gradient with the forward pass, while a row is at hand; the
 backward pass multiplies it by the incoming gradient in place (no pass over it when
 that is 1; a bf16 gradient is rounded once more unless that is a power of two) and
 hands it on, so it can be taken once and has no gradient of its own: second
 derivatives (create_graph) through a loss raise.  That pass is Python, so
-torch.compile runs the two losses outside its graph (fullgraph=True refuses them);
-token_logps is two opaque nodes.
+torch.compile runs the losses outside its graph (fullgraph=True refuses them);
+token_logps and top_logps are two opaque nodes each.
 """
-from typing import List, Optional, Sequence
+from typing import List, NamedTuple, Optional, Sequence
 
 import torch
 
@@ -263,6 +266,64 @@ def _(logits, labels, old_logps, advantages, weights, ref_logps, clip_low, clip_
             logits.new_empty(logits.shape if with_gradient else (0, 0))]
 
 
+@torch.library.custom_op(f"{NS}::top_logps", mutates_args=(), device_types="cuda")
+def top_logps_op(logits: torch.Tensor, labels: Optional[torch.Tensor], k: int,
+                 temperature: float) -> List[torch.Tensor]:
+    """(top_ids [T, K], top_logps [T, K], entropy [T], rest_logps [T], logps [T], or [0] without
+    labels, stats [T, 2])."""
+    T, dev, f32 = logits.shape[0], logits.device, torch.float32
+    ids = torch.empty((T, k), dtype=torch.int64, device=dev)
+    top, stats = torch.empty((T, k), dtype=f32, device=dev), torch.empty((T, 2), dtype=f32, device=dev)
+    entropy, rest = torch.empty(T, dtype=f32, device=dev), torch.empty(T, dtype=f32, device=dev)
+    logps = torch.empty(0 if labels is None else T, dtype=f32, device=dev)
+    training.lora_top_logps(logits, ids, top, labels=labels, logps=None if labels is None else logps, entropy=entropy,
+                            rest_logps=rest, stats=stats, temperature=temperature)
+    return [ids, top, entropy, rest, logps, stats]
+
+
+@top_logps_op.register_fake
+def _(logits, labels, k, temperature):
+    T = logits.shape[0]
+    new = lambda *shape: logits.new_empty(shape, dtype=torch.float32)  # noqa: E731
+    return [logits.new_empty((T, k), dtype=torch.int64), new(T, k), new(T), new(T), new(0 if labels is None else T),
+            new(T, 2)]
+
+
+@torch.library.custom_op(f"{NS}::top_logps_backward", mutates_args=(), device_types="cuda")
+def top_logps_backward_op(logits: torch.Tensor, labels: Optional[torch.Tensor], ids: torch.Tensor, stats: torch.Tensor,
+                          entropy: torch.Tensor, dlogps: Optional[torch.Tensor], dentropy: Optional[torch.Tensor],
+                          dtop: Optional[torch.Tensor], temperature: float) -> torch.Tensor:
+    """dlogits from the gradients of the results (None: zero)."""
+    dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    training.lora_top_logps_backward(logits, stats, dlogits, labels=labels, top_ids=ids, entropy=entropy, dlogps=dlogps,
+                                     dentropy=dentropy, dtop_logps=dtop, temperature=temperature)
+    return dlogits
+
+
+@top_logps_backward_op.register_fake
+def _(logits, labels, ids, stats, entropy, dlogps, dentropy, dtop, temperature):
+    return logits.new_empty(logits.shape)
+
+
+@torch.library.custom_op(f"{NS}::distill_loss", mutates_args=(), device_types="cuda")
+def distill_loss_op(logits: torch.Tensor, top_ids: torch.Tensor, top_logps: torch.Tensor,
+                    rest_logps: Optional[torch.Tensor], weights: Optional[torch.Tensor], kind: str, temperature: float,
+                    with_gradient: bool) -> List[torch.Tensor]:
+    """(loss [], row_loss [T], dlogits: empty without a gradient)."""
+    dev = logits.device
+    loss, row = torch.empty((), dtype=torch.float32, device=dev), torch.empty(logits.shape[0], device=dev)
+    d = torch.empty(logits.shape if with_gradient else (0, 0), dtype=logits.dtype, device=dev)
+    training.lora_distill_loss(logits, top_ids, top_logps, row, loss, rest_logps=rest_logps, weights=weights,
+                               dlogits=d if with_gradient else None, kind=kind, temperature=temperature)
+    return [loss, row, d]
+
+
+@distill_loss_op.register_fake
+def _(logits, top_ids, top_logps, rest_logps, weights, kind, temperature, with_gradient):
+    return [logits.new_empty((), dtype=torch.float32), logits.new_empty((logits.shape[0],), dtype=torch.float32),
+            logits.new_empty(logits.shape if with_gradient else (0, 0))]
+
+
 class TokenLogpsFn(torch.autograd.Function):
     """logps[t] = log_softmax(logits[t] / temperature)[labels[t]]."""
 
@@ -338,6 +399,57 @@ class PolicyLossFn(torch.autograd.Function):
         return (_hand_on(ctx, dloss),) + (None,) * 10
 
 
+class TopLogpsFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, labels, k, temperature):
+        ids, top, entropy, rest, logps, stats = top_logps_op(logits, labels, k, temperature)
+        ctx.save_for_backward(logits, labels, ids, stats, entropy)
+        ctx.temperature = temperature
+        ctx.mark_non_differentiable(ids, rest)
+        ctx.set_materialize_grads(False)
+        return ids, top, entropy, rest, logps
+
+    @staticmethod
+    def backward(ctx, _ids, dtop, dentropy, _rest, dlogps):
+        logits, labels, ids, stats, entropy = ctx.saved_tensors
+        dense = lambda g: None if g is None else g.contiguous()  # noqa: E731
+        d = top_logps_backward_op(logits, labels, ids, stats, entropy, None if labels is None else dense(dlogps),
+                                  dense(dentropy), dense(dtop), ctx.temperature)
+        return d, None, None, None
+
+
+class DistillLossFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, anchor, *args):
+        loss, row, d = distill_loss_op(logits, *args, anchor is not None)
+        ctx.save_for_backward(anchor)
+        ctx.dlogits = d if anchor is not None else None
+        ctx.mark_non_differentiable(row)
+        return loss, row
+
+    @staticmethod
+    def backward(ctx, dloss, *_):
+        return (_hand_on(ctx, dloss),) + (None,) * 7
+
+
+class TopLogps(NamedTuple):
+    """What top_logps returns; label_logps is None without labels."""
+    ids: torch.Tensor
+    logps: torch.Tensor
+    entropy: torch.Tensor
+    rest: torch.Tensor
+    label_logps: Optional[torch.Tensor]
+
+
+def top_logps(logits: torch.Tensor, k: int, labels: Optional[torch.Tensor] = None, temperature: float = 1.0) -> TopLogps:
+    """The k most probable tokens of each row of logits [T, V] (ids and logps [T, k], -1 and minus
+    infinity where there are fewer), its entropy [T], the log of the mass of all other tokens
+    (rest [T]), and the log-probabilities of labels [T], where given.  logps, entropy and
+    label_logps are differentiable in the logits; ids and rest are not."""
+    ids, top, entropy, rest, of_labels = TopLogpsFn.apply(logits, labels, int(k), float(temperature))
+    return TopLogps(ids, top, entropy, rest, None if labels is None else of_labels)
+
+
 def token_logps(logits: torch.Tensor, labels: torch.Tensor, temperature: float = 1.0) -> torch.Tensor:
     """Differentiable log-probabilities [T] of labels [T] (int64; 0 where a label is outside
     [0, V)) under logits [T, V]."""
@@ -360,6 +472,18 @@ def policy_loss(logits, labels, old_logps, advantages, weights=None, ref_logps=N
     is differentiable in the logits."""
     return PolicyLossFn.apply(logits, _anchor(logits), labels, old_logps, advantages, weights, ref_logps,
                               float(clip_low), float(clip_high), float(kl_beta), float(temperature))
+
+
+def distill_loss(logits, top_ids, top_logps, rest_logps=None, weights=None, kind="forward", temperature=1.0):
+    """(loss, row_loss [T]): the divergence of logits [T, V] from a teacher's record (what
+    top_logps returns for its logits at the same temperature), summed with the rows' weights
+    (None: their mean); the loss is differentiable in the logits.  kind: "forward" for
+    KL(teacher || student), "reverse" for KL(student || teacher); with rest_logps all tokens
+    that are not listed count as one, without they do not."""
+    if weights is None:
+        weights = torch.full((logits.shape[0],), 1.0 / max(1, logits.shape[0]), device=logits.device)
+    return DistillLossFn.apply(logits, _anchor(logits), top_ids, top_logps, rest_logps, weights, kind,
+                               float(temperature))
 
 
 # ----------------------------------------------------------------------------- optimizer
