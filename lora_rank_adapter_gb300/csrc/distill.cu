@@ -118,104 +118,129 @@ __device__ __forceinline__ void drop_repeated(Record &r, uint32_t *seen) {
   __syncwarp();
 }
 
-// ln S in two parts, the first one exact: S = 2^n f, ln 2 split as by Cody and Waite
-// ("Software Manual for the Elementary Functions", 1980).
-__device__ __forceinline__ float2 log_parts(float S) {
-  const uint32_t bits = __float_as_uint(S);
-  float n = (float)((int)(bits >> 23) - 127), f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
-  if (f > 1.41421356f) {
-    f *= 0.5f;
-    n += 1.f;
-  }
-  return make_float2(n * 0.693359375f, fmaf(n, -2.12194440054690583e-4f, logf(f)));
-}
-
-// What the hardware's 2^x is low by on average (over an octave; at most 1.4e-7): a sum of many
-// such terms is, too.
-constexpr float kLow = 5.2e-8f;
-
-// What a row's loss and gradient come to, by a warp, from the sums over the tokens that
-// are not listed (m, s).  dz: c times the listed tokens' gradient; f: what exp((x - m) k)
-// of all others is multiplied by.  Differences of logarithms come to 2^-24 of themselves:
-// the loss of a student near its teacher is a sum of small ones.
-struct RowTerms {
-  float loss, f;
-  float dz[kEach];
+// What can be told of a row ahead of the sums over the tokens that are not listed, by a warp.  With g_j the
+// listed logits over the temperature, from the largest one (the top) on: e_j = exp(g_j); forward x_j = q_j,
+// reverse x_j = g_j - ln q_j.  The sums leave the top out: a sure model's other probabilities are what
+// its loss and gradient come from, and next to a 1 they would lose their last bits.
+struct Ahead {
+  float top, E, Q, B;            // the largest logit; sums of e_j, of q_j and the rest's q_r, of e_j x_j
+  float x_top, qr, ln_qr, c;     // c: what the gradient is multiplied by
+  int at;                        // the top's entry
 };
-__device__ __forceinline__ RowTerms row_terms(const Distill &a, const Record &r, float ln_qr, float m, float s, float c) {
+struct Entries {
+  float e[kEach], x[kEach], y[kEach];      // y_j = g_j - ln q_j
+};
+__device__ __forceinline__ Ahead foresee(const Distill &a, const Record &r, float ln_qr, float c, Entries &of) {
+  float (&e)[kEach] = of.e, (&x)[kEach] = of.x, (&y)[kEach] = of.y;
+  Ahead h;
   float top = kNegInf;
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
     if (r.id[i] >= 0) top = fmaxf(top, r.z[i]);
-  float M;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(top));
-  M = fmaxf(M, m);
-  const float ref = ref_of(M);
-  float2 g[kEach];
-  float e[kEach], sum = 0.f;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(h.top) : "f"(top));
+  h.at = -1;
+  float E = 0.f, B = 0.f, Q = 0.f, x_top = 0.f;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    e[i] = 0.f;
+    e[i] = x[i] = y[i] = 0.f;
     if (i * 32 >= a.K) continue;
-    g[i] = a.scale.gap2(r.z[i], ref);
-    if (r.id[i] >= 0) e[i] = expf(g[i].x + g[i].y);
-    sum += e[i];
-  }
-  sum = warp_sum_f(sum);
-  s = fmaf(s, kLow, s);
-  const float rest = s * expf(a.scale.gap(m, ref)), S = sum + rest, over = 1.f / S;
-  const float2 ln_S = log_parts(S);
-  const float p_r = rest * over;
-  const float ratio = sum / rest;
-  const float ln_pr = ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(m, ref) + logf(s) - (ln_S.x + ln_S.y);
-  float L = 0.f, Q = 0.f, P = 0.f, p[kEach], q[kEach], gap[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    p[i] = q[i] = gap[i] = 0.f;
-    if (i * 32 >= a.K || r.id[i] < 0) continue;
-    p[i] = e[i] * over;
-    gap[i] = (g[i].x - ln_S.x) - r.lnq[i] + (g[i].y - ln_S.y);
-    if (a.reverse) {
-      if (p[i] == 0.f) gap[i] = 0.f;      // no 0 * infinity
-      L += p[i] * gap[i];
-      P += p[i];
-    } else {
-      q[i] = expf(r.lnq[i]);
-      if (q[i] != 0.f) L -= q[i] * gap[i];
-      Q += q[i];
+    if (r.id[i] >= 0) {
+      const float g = a.scale.gap(r.z[i], ref_of(h.top));
+      e[i] = expf(g);
+      y[i] = g - r.lnq[i];
+      x[i] = a.reverse ? (e[i] == 0.f ? 0.f : y[i]) : expf(r.lnq[i]);      // no 0 * infinity
     }
-  }
-  L = warp_sum_f(L);
-  float F;      // the mass that the gradient leaves outside the list
-  if (a.reverse) {
-    if (a.rest) {
-      const float gap_r = p_r == 0.f ? 0.f : ln_pr - ln_qr;
-      L += p_r * gap_r;
-      F = p_r * (gap_r - L);
-      P = 1.f;
-    } else {
-      P = warp_sum_f(P);
-      F = -p_r * (L + P);
+    const unsigned tops = __ballot_sync(0xffffffffu, r.id[i] >= 0 && r.z[i] == h.top);
+    if (h.at < 0 && tops) {
+      h.at = i * 32 + __ffs(tops) - 1;
+      x_top = __shfl_sync(0xffffffffu, x[i], h.at & 31);
     }
-  } else {
-    Q = warp_sum_f(Q);
-    F = 0.f;
-    if (a.rest) {
-      const float qr = expf(ln_qr);
-      if (qr != 0.f) L -= qr * (ln_pr - ln_qr);
-      Q += qr;
-      F = -qr;
-    }
-    F += p_r * Q;
+    if (h.at == i * 32 + lane_id()) continue;
+    E += e[i];
+    B += e[i] * x[i];
+    Q += x[i];
   }
-  RowTerms t;
-  t.loss = L;
-  t.f = s == 0.f ? 0.f : c * F / s;      // s is 0: nothing outside the list has any probability
-  if (!(S > 0.f)) t.loss = t.f = NAN;    // nor inside: no distribution
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) t.dz[i] = c * (a.reverse ? p[i] * (gap[i] + 1.f - L - P) : p[i] * Q - q[i]);
-  return t;
+  h.E = warp_sum_f(E);
+  h.B = warp_sum_f(B);
+  h.qr = a.rest && !a.reverse ? expf(ln_qr) : 0.f;
+  h.Q = warp_sum_f(Q) + h.qr;
+  h.x_top = x_top;
+  h.ln_qr = ln_qr;
+  h.c = c;
+  return h;
 }
+
+// The row's terms once the sums (m, s) over the tokens that are not listed are there.  f: what
+// exp((x - m) k) of these is multiplied by; dz(): c times a listed token's gradient.
+struct Terms {
+  float f, u, v, dz_top, p, rest_term;
+  float2 ln_p;                           // of the top, in two parts; with its e and y an entry's ln p - ln q
+  int at;
+  bool reverse, fine;
+  __device__ __forceinline__ Terms(const Distill &a, const Ahead &h, float m, float s, bool want_loss) {
+    const float c = h.c;
+    reverse = a.reverse;
+    at = h.at;
+    s = fmaf(s, kLow, s);
+    const bool leads = h.top >= m;       // the top is the row's largest
+    const float lead = leads ? 0.f : a.scale.gap(h.top, ref_of(m)), e_top = h.top == kNegInf ? 0.f : expf(lead);
+    const float rest = leads ? s * expf(a.scale.gap(m, ref_of(h.top))) : s;
+    const float others = h.E * e_top + rest, S = e_top + others, over = __fdividef(1.f, S);
+    const float p_r = rest * over, p_others = others * over;
+    p = e_top * over;
+    float F, gap_r = 0.f;
+    if (reverse || want_loss) {
+      const float2 ln_S = leads ? log1_parts(others) : log_parts(S);
+      ln_p = make_float2(lead - ln_S.x, -ln_S.y);
+      if (a.rest) {
+        const float ratio = __fdividef(e_top + h.E * e_top, rest);
+        const float ln_pr = ratio < 1e30f ? -log1pf(ratio)
+                                          : a.scale.gap(m, ref_of(fmaxf(h.top, m))) + logf(s) - (ln_S.x + ln_S.y);
+        const float mass = reverse ? p_r : h.qr;
+        gap_r = mass == 0.f ? 0.f : ln_pr - h.ln_qr;      // no 0 * infinity
+        rest_term = mass * (reverse ? gap_r : -gap_r);
+      } else {
+        rest_term = 0.f;
+      }
+    }
+    if (!reverse) {
+      const float Q = h.Q + h.x_top;
+      F = Q * p_r - h.qr;
+      u = c * p * Q;                     // p_j Q - q_j
+      v = -c;
+      dz_top = c * (h.Q - p_others * Q);
+    } else {
+      const float lp = ln_p.x + ln_p.y, gap_top = (h.x_top + ln_p.x) + ln_p.y;
+      const bool listed = p != 0.f;
+      float L = (listed ? p * h.B + h.E * p * lp : 0.f) + rest_term;      // without the top's
+      const float all = listed ? fmaf(p, gap_top, L) : L, more = a.rest ? 0.f : p_r;
+      F = a.rest ? p_r * (gap_r - all) : -p_r * (all + 1.f - p_r);
+      v = lp - all + more;               // p_j (gap_j - L), without the rest p_j (gap_j + 1 - L - P)
+      dz_top = c * p * (p_others * gap_top - L + more);
+      if (!listed) dz_top = 0.f;
+      u = c * p;
+    }
+    f = s == 0.f ? 0.f : __fdividef(c * F, s);      // s is 0: nothing outside the list has any probability
+    fine = S > 0.f && h.top < INFINITY;
+    if (!fine) f = u = dz_top = NAN;     // nor inside: no distribution
+  }
+  __device__ __forceinline__ float dz(int entry, float e, float x) const {
+    if (entry == at) return dz_top;
+    return reverse ? (e == 0.f ? 0.f : u * e * (x + v)) : fmaf(u, e, v * x);
+  }
+  // The row's loss, by a warp (want_loss).
+  __device__ __forceinline__ float loss(int K, const Entries &of) const {
+    float L = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (i * 32 >= K) continue;
+      const float mass = reverse ? of.e[i] * p : of.x[i], gap = (of.y[i] + ln_p.x) + ln_p.y;
+      if (mass != 0.f) L += reverse ? mass * gap : -mass * gap;
+    }
+    L = warp_sum_f(L) + rest_term;
+    return fine ? L : NAN;
+  }
+};
 
 // U 16-byte pieces into a running maximum and a pair of partial sums, as absorb() does, with
 // the temperature in both its parts: at a rounded one, ln S would be off by the same in every
@@ -359,8 +384,14 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
     s = v.y;
     merge_exact(m, s, a.scale);
   }
-  const RowTerms x = row_terms(a, r, ln_qr, m, s, w * a.grad_scale * a.scale.hi);
-  if (tid == 0) a.row_loss[t] = x.loss;
+  Entries of;
+  const bool tells = warp % kTeam == 0;                  // the loss, a warp of the team
+  const Ahead ahead = foresee(a, r, ln_qr, w * a.grad_scale * a.scale.hi, of);
+  const Terms x(a, ahead, m, s, tells);
+  if (tells) {
+    const float L = x.loss(a.K, of);
+    if (lane == 0) a.row_loss[t] = L;
+  }
   if (a.dlogits == nullptr) return;
   const RowGrad g = {ref_of(m), k, 0.f, x.f};
   const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
@@ -382,7 +413,7 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
   sync();                                                // the listed tokens' places come after the pieces
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
-    if (r.id[i] >= 0 && i % kTeam == warp % kTeam) Elem<E>::store(out + r.id[i], x.dz[i]);
+    if (r.id[i] >= 0 && i % kTeam == warp % kTeam) Elem<E>::store(out + r.id[i], x.dz(i * 32 + lane, of.e[i], of.x[i]));
 }
 
 // ----------------------------------------------------------------------------- rows held on chip
@@ -414,92 +445,13 @@ struct HeldDistill {
   int cluster, slice;      // slice: 16-byte pieces of a block at most, up to a ring
 };
 
-// A row's record, and what can be told of it ahead of the sums over the rest: with g_j the logits over
-// the temperature, from the largest listed one (top) on,
-//     e_j = exp(g_j), E = sum e_j; forward x_j = q_j, Q their sum and q_r; reverse x_j = g_j - ln q_j, B = sum e_j x_j
 struct HeldRecord {
   int id[kMaxTop];
-  float z[kMaxTop], lnq[kMaxTop], e[kMaxTop], x[kMaxTop];
+  float e[kMaxTop], x[kMaxTop], y[kMaxTop];
   int place[kMaxTop];                                    // its element from the start of the block's slice, -1: not in a piece of it
   unsigned touched[kWorkers];                            // chunks in which a warp has any
-  float top, E, B, Q, qr, ln_qr, c;
+  Ahead ahead;
   int counts, edges;                                     // edges: any among the ragged ends
-};
-__device__ __forceinline__ void foresee(const Distill &a, const Record &r, HeldRecord &to) {
-  const int lane = lane_id();
-  float top = kNegInf, M;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (r.id[i] >= 0) top = fmaxf(top, r.z[i]);
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(M) : "f"(top));
-  float E = 0.f, B = 0.f, Q = 0.f;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    if (i * 32 >= a.K) continue;
-    float e = 0.f, x = 0.f;
-    if (r.id[i] >= 0) {
-      const float g = a.scale.gap(r.z[i], ref_of(M));
-      e = expf(g);
-      x = a.reverse ? (e == 0.f ? 0.f : g - r.lnq[i]) : expf(r.lnq[i]);      // no 0 * infinity
-    }
-    E += e;
-    B += e * x;
-    Q += x;
-    to.e[i * 32 + lane] = e;
-    to.x[i * 32 + lane] = x;
-  }
-  E = warp_sum_f(E);
-  B = warp_sum_f(B);
-  Q = warp_sum_f(Q);
-  if (lane != 0) return;
-  to.qr = a.rest && !a.reverse ? expf(to.ln_qr) : 0.f;
-  to.top = M;
-  to.E = E;
-  to.B = B;
-  to.Q = Q + to.qr;
-}
-
-// What a working warp needs of a row once it has the sums (m, s) over the rest: f as in RowTerms, and
-// a listed token's dz from its e and x.
-struct HeldTerms {
-  float f, p, u, v;
-  bool reverse;
-  __device__ __forceinline__ HeldTerms(const Distill &a, const HeldRecord &r, float m, float s) {
-    const float ref = ref_of(fmaxf(r.top, m)), c = r.c;
-    const float lead = a.scale.gap(r.top, ref);
-    s = fmaf(s, kLow, s);
-    const float rest = s * expf(a.scale.gap(m, ref)), listed = r.E * expf(lead), S = listed + rest, over = __fdividef(1.f, S);
-    const float p_r = rest * over;
-    float F;
-    reverse = a.reverse;
-    p = expf(lead) * over;
-    if (!reverse) {
-      F = r.Q * p_r - r.qr;
-      u = c * p * r.Q;                   // dz = u e - c x
-      v = -c;
-    } else {
-      const float2 ln_S = log_parts(S);
-      const float ln_p = (lead - ln_S.x) - ln_S.y, P = r.E * p;
-      float L = r.E == 0.f ? 0.f : p * r.B + P * ln_p;
-      if (a.rest) {
-        const float ratio = __fdividef(listed, rest);
-        const float ln_pr = ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(m, ref) + logf(s) - (ln_S.x + ln_S.y);
-        const float gap_r = p_r == 0.f ? 0.f : ln_pr - r.ln_qr;
-        L += p_r * gap_r;
-        F = p_r * (gap_r - L);
-        v = ln_p - L;                    // dz = u e (x + v)
-      } else {
-        F = -p_r * (L + P);
-        v = ln_p + 1.f - L - P;
-      }
-      u = c * p;
-    }
-    f = s == 0.f ? 0.f : __fdividef(c * F, s);
-    if (!(S > 0.f)) f = u = NAN;
-  }
-  __device__ __forceinline__ float dz(float e, float x) const {
-    return reverse ? (e == 0.f ? 0.f : u * e * (x + v)) : fmaf(u, e, v * x);
-  }
 };
 
 // A block's slice of a row.
@@ -595,15 +547,15 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
         if (n % C == rank) {                             // each block in turn
           float loss = 0.f;
           if (to.counts) {
-            Record old;
+            Entries old;
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
-              old.id[i] = to.id[i * 32 + lane];
-              old.z[i] = to.z[i * 32 + lane];
-              old.lnq[i] = to.lnq[i * 32 + lane];
+              old.e[i] = to.e[i * 32 + lane];
+              old.x[i] = to.x[i * 32 + lane];
+              old.y[i] = to.y[i * 32 + lane];
             }
             const float2 v = sums[rec.slot];
-            loss = row_terms(a, old, to.ln_qr, v.x, v.y, 0.f).loss;
+            loss = Terms(a, to.ahead, v.x, v.y, true).loss(a.K, old);
           }
           if (lane == 0) a.row_loss[before] = loss;
         }
@@ -619,18 +571,20 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         to.id[i * 32 + lane] = counts ? r.id[i] : -1;
-        to.z[i * 32 + lane] = counts ? r.z[i] : 0.f;
-        to.lnq[i * 32 + lane] = counts ? r.lnq[i] : 0.f;
       }
-      if (lane == 0) {
-        to.c = w * a.grad_scale * a.scale.hi;
-        to.ln_qr = ln_qr;
-        to.counts = counts;
-      }
+      if (lane == 0) to.counts = counts;
       if (lane < kWorkers) to.touched[lane] = 0;
       __syncwarp();
       if (counts) {
-        foresee(a, r, to);
+        Entries of;
+        const Ahead ahead = foresee(a, r, ln_qr, w * a.grad_scale * a.scale.hi, of);
+        if (lane == 0) to.ahead = ahead;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          to.e[i * 32 + lane] = of.e[i];
+          to.x[i * 32 + lane] = of.x[i];
+          to.y[i * 32 + lane] = of.y[i];
+        }
         const Slice<E> sl(h, t, rank);
         const int first = sl.head + sl.v0 * N, tail = sl.head + sl.vecs * N;
         bool edges = false;
@@ -776,7 +730,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       sums[rec.slot] = make_float2(m, s);
       mbar_arrive(&summed[rec.slot]);
     }
-    const HeldTerms x(a, of, m, s);
+    const Terms x(a, of.ahead, m, s, false);
     const RowGrad g = {ref_of(m), k, 0.f, x.f};
     const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0;
     // Where the gradient's rows sit at other offsets, warps write each other's elements: all have struck
@@ -811,13 +765,13 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     __syncwarp();
     if (!same && !all_here()) break;
     if (touched) each_place([&](int i, int place) {
-      Elem<E>::store(out + first + place, x.dz(of.e[i * 32 + lane], of.x[i * 32 + lane]));
+      Elem<E>::store(out + first + place, x.dz(i * 32 + lane, of.e[i * 32 + lane], of.x[i * 32 + lane]));
     });
     if (warp == 0 && of.edges)
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int j = i * 32 + lane, id = of.id[j];
-        if ((rank == 0 && id >= 0 && id < sl.head) || (rank == C - 1 && id >= tail)) Elem<E>::store(out + id, x.dz(of.e[j], of.x[j]));
+        if ((rank == 0 && id >= 0 && id < sl.head) || (rank == C - 1 && id >= tail)) Elem<E>::store(out + id, x.dz(j, of.e[j], of.x[j]));
       }
     leave();
   }
@@ -954,13 +908,16 @@ __global__ void __launch_bounds__(kThreads) row_kernel(Distill a, int C, int sli
       r.z[i] = logit[j];
       r.lnq[i] = r.id[i] >= 0 ? a.teacher[t * K + j] : 0.f;
     }
-    const RowTerms x = row_terms(a, r, a.rest ? a.rest[t] : 0.f, m, s, w * a.grad_scale * a.scale.hi);
+    Entries of;
+    const Ahead ahead = foresee(a, r, a.rest ? a.rest[t] : 0.f, w * a.grad_scale * a.scale.hi, of);
+    const Terms x(a, ahead, m, s, true);
+    const float L = x.loss(K, of);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) dz[i * 32 + lane] = x.dz[i];
+    for (int i = 0; i < kEach; ++i) dz[i * 32 + lane] = x.dz(i * 32 + lane, of.e[i], of.x[i]);
     if (lane == 0) {
       m_of = ref_of(m);
       f_of = x.f;
-      if (rank == 0) a.row_loss[t] = x.loss;
+      if (rank == 0) a.row_loss[t] = L;
     }
   }
   __syncthreads();

@@ -258,6 +258,26 @@ struct Scale {
   }
 };
 
+// What the hardware's 2^x is low by on average (over an octave; at most 1.4e-7): a sum of many
+// such terms is, too.
+constexpr float kLow = 5.2e-8f;
+
+// ln S in two parts, the first one exact: S = 2^n f, ln 2 split as by Cody and Waite
+// ("Software Manual for the Elementary Functions", 1980).
+__device__ __forceinline__ float2 log_parts(float S) {
+  const uint32_t bits = __float_as_uint(S);
+  float n = (float)((int)(bits >> 23) - 127), f = __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);
+  if (f > 1.41421356f) {
+    f *= 0.5f;
+    n += 1.f;
+  }
+  return make_float2(n * 0.693359375f, fmaf(n, -2.12194440054690583e-4f, logf(f)));
+}
+// ln (1 + O): where O is little, all of its bits count.
+__device__ __forceinline__ float2 log1_parts(float O) {
+  return O < 0.5f ? make_float2(0.f, log1pf(O)) : log_parts(1.f + O);
+}
+
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kSplit ? 2 : kThreads == 256 ? 3 : 8
   Shared &sh = *reinterpret_cast<Shared *>(dynamic);
   const int C = kSplit ? clusters : 1;
   const int rank = (int)(blockIdx.x % C), tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, K = a.K, V = (int)a.V;
-  const float k = a.scale.k;
+  const float k = a.scale.k + a.scale.k_lo;
   pdl_wait();
   pdl_launch_dependents();
   const int64_t t = blockIdx.x / C;
@@ -597,29 +597,45 @@ __global__ void __launch_bounds__(kThreads, kSplit ? 2 : kThreads == 256 ? 3 : 8
   }
   if (warp == 0 && rank == 0 && !live) top_nothing(a, t, lane);
   if (warp == 0 && rank == 0 && live) {
-    Sums total = no_sums();                            // of the K largest
+    // the K largest but the first, which is the row's largest: its own 1 stays out of the sum, next to which
+    // a sure model's other probabilities would lose their last bits
+    const uint64_t first = K > 0 ? sh.best[0] : 0;
+    Sums total = no_sums();
     for (int i = lane; i < K; i += 32)
-      if (sh.best[i]) total.add(key_value(sh.best[i]), k);
+      if (i > 0 && sh.best[i]) total.add(key_value(sh.best[i]), k);
     warp_merge(total, k);
-    const float listed = total.s, listed_m = total.m;
-    total.add(rest, k);
-    const bool fine = total.s > 0.f && total.s < INFINITY;
-    const float log_s = fine ? logf(total.s) : NAN, m = total.m;
+    const float one = first ? 1.f : 0.f, m = first ? key_value(first) : rest.m;
+    Sums others = rest;
+    others.s = fmaf(others.s, kLow, others.s);
+    others.move(fmaxf(others.m, m), k);      // (m: a NaN or an infinity among the rest shows in the sums)
+    const float rest_s = others.s;
+    total.move(fmaxf(total.m, m), k);
+    const float listed = one + total.s;
+    others.s += total.s;
+    others.w += total.w;
+    const float S = one + others.s;
+    const bool fine = S > 0.f && S < INFINITY && m < INFINITY;
+    const float2 log_s = !fine ? make_float2(NAN, NAN) : first ? log1_parts(others.s) : log_parts(S);
+    auto logp = [&](float v) {
+      const float2 g = a.scale.gap2(v, m);
+      return (g.x - log_s.x) + (g.y - log_s.y);
+    };
     for (int i = lane; i < K; i += 32) {
       const uint64_t key = sh.best[i];
       a.ids[t * K + i] = key && fine ? key_id(key) : -1;
-      a.top[t * K + i] = !fine ? NAN : key ? a.scale.gap(key_value(key), m) - log_s : kNegInf;
+      a.top[t * K + i] = !fine ? NAN : key ? logp(key_value(key)) : kNegInf;
     }
     if (lane == 0) {
-      if (a.logps) a.logps[t] = a.scale.gap(picked, m) - log_s;
-      if (a.entropy) a.entropy[t] = log_s - total.w * kLn2 / total.s;
+      if (a.logps) a.logps[t] = logp(picked);
+      if (a.entropy) a.entropy[t] = log_s.x + (log_s.y - others.w * kLn2 / S);
       if (a.rest) {
-        // ln of rest / (rest + listed), without the two large logarithms where that is more than nothing
-        const float ratio = listed * ex2((listed_m - ref_of(rest.m)) * k) / rest.s;
+        // ln of rest / (rest + listed), without the large logarithms where that is more than nothing
+        const float ratio = listed / rest_s;
+        const float2 far = a.scale.gap2(rest.m, m);
         a.rest[t] = !fine ? NAN : !(rest.s > 0.f) ? kNegInf
-                    : ratio < 1e30f ? -log1pf(ratio) : a.scale.gap(rest.m, m) + logf(rest.s) - log_s;
+                    : ratio < 1e30f ? -log1pf(ratio) : (far.x - log_s.x) + (far.y - log_s.y) + logf(rest.s);
       }
-      if (a.stats) a.stats[t] = make_float2(m, total.s);
+      if (a.stats) a.stats[t] = make_float2(m, S);
     }
   }
 }
