@@ -187,7 +187,7 @@ LORA_API lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, in
  *              shorter list); one that its row lists again counts where it comes first.
  *   top_logps  float [T][K];  rest_logps  float [T] or NULL: at the temperature of this call
  *   weights    float [T] or NULL for 1.  A row of weight 0 or without a listed token is
- *              IGNORED: its row_loss and its gradient are zero and its logits are not read.
+ *              IGNORED: its row_loss and its gradient are zero, and its logits do not matter
  *   row_loss   float [T], none of the inputs;  loss  float [1]
  *   dlogits    NULL, or grad_scale * d loss / d logits
  * -------------------------------------------------------------------------------- */

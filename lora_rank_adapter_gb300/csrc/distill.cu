@@ -177,6 +177,7 @@ struct Terms {
   float2 ln_p;                           // of the top, in two parts; with its e and y an entry's ln p - ln q
   int at;
   bool reverse, fine;
+  Terms() = default;
   __device__ __forceinline__ Terms(const Distill &a, const Ahead &h, float m, float s, bool want_loss) {
     const float c = h.c;
     reverse = a.reverse;
@@ -290,6 +291,10 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
   __shared__ unsigned edge_bits[kRows];
   __shared__ uint32_t seen[4][kSeenWords];               // of each warp
   __shared__ float2 sh[kTeam];
+  // of a block's row: what its second warp works out ahead, and the terms, by its first
+  __shared__ Ahead ahead_of;
+  __shared__ float e_of[kMaxTop], x_of[kMaxTop], m_of;
+  __shared__ Terms terms_of;
   static_assert(kTeam == 1 || kTeam == 4, "a warp, or a block of four");
   auto sync = [] { if (kTeam == 1) __syncwarp(); else __syncthreads(); };
   pdl_wait();
@@ -323,8 +328,12 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
   const int edge_at = at_head ? tid : tail + tid - 16;
   float edge = kNegInf;
   if (at_head || at_tail) edge = Elem<E>::load(row + edge_at);
-  read_values(a, t, row, r);
-  const float ln_qr = a.rest ? a.rest[t] : 0.f;
+  const bool tells = kTeam == 1 || warp == 1;            // the warp that looks ahead, and tells the loss
+  float ln_qr = 0.f;
+  if (tells) {
+    read_values(a, t, row, r);
+    if (a.rest) ln_qr = a.rest[t];
+  }
   // the bits, by the first warp; a bit that was set already is a token listed twice
   if (warp % kTeam == 0) {
     bool twice = false;
@@ -374,20 +383,40 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
   const float k = a.scale.k;
   if (edge != kNegInf) absorb_exact(m, s, edge, a.scale);
   merge_exact(m, s, a.scale);
-  // past this point the gradient may replace the row: all reads of it come before
-  if (kTeam == 1) __syncwarp();
-  if (kTeam > 1) {
-    if (lane == 0) sh[warp] = make_float2(m, s);
-    __syncthreads();
-    const float2 v = lane < kTeam ? sh[lane % kTeam] : make_float2(kNegInf, 0.f);
-    m = v.x;
-    s = v.y;
-    merge_exact(m, s, a.scale);
-  }
   Entries of;
-  const bool tells = warp % kTeam == 0;                  // the loss, a warp of the team
-  const Ahead ahead = foresee(a, r, ln_qr, w * a.grad_scale * a.scale.hi, of);
-  const Terms x(a, ahead, m, s, tells);
+  Ahead ahead;
+  if (tells) ahead = foresee(a, r, ln_qr, w * a.grad_scale * a.scale.hi, of);
+  // past the barrier the gradient may replace the row: all reads of it come before
+  Terms x;
+  if (kTeam == 1) {
+    __syncwarp();
+    x = Terms(a, ahead, m, s, true);
+  } else {
+    if (lane == 0) sh[warp] = make_float2(m, s);
+    if (tells) {
+      if (lane == 0) ahead_of = ahead;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        e_of[i * 32 + lane] = of.e[i];
+        x_of[i * 32 + lane] = of.x[i];
+      }
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const float2 v = lane < kTeam ? sh[lane % kTeam] : make_float2(kNegInf, 0.f);
+      m = v.x;
+      s = v.y;
+      merge_exact(m, s, a.scale);
+      const Terms made(a, ahead_of, m, s, true);
+      if (lane == 0) {
+        terms_of = made;
+        m_of = m;
+      }
+    }
+    __syncthreads();
+    x = terms_of;
+    m = m_of;
+  }
   if (tells) {
     const float L = x.loss(a.K, of);
     if (lane == 0) a.row_loss[t] = L;
@@ -413,7 +442,10 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
   sync();                                                // the listed tokens' places come after the pieces
 #pragma unroll
   for (int i = 0; i < kEach; ++i)
-    if (r.id[i] >= 0 && i % kTeam == warp % kTeam) Elem<E>::store(out + r.id[i], x.dz(i * 32 + lane, of.e[i], of.x[i]));
+    if (r.id[i] >= 0 && i % kTeam == warp % kTeam) {
+      const int j = i * 32 + lane;
+      Elem<E>::store(out + r.id[i], kTeam == 1 ? x.dz(j, of.e[i], of.x[i]) : x.dz(j, e_of[j], x_of[j]));
+    }
 }
 
 // ----------------------------------------------------------------------------- rows held on chip
