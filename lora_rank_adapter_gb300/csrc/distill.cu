@@ -1053,16 +1053,18 @@ cudaError_t launch_held(const Distill &r, const HeldPlan &plan, cudaStream_t st)
 // 16-byte pieces of one of `parts` slices of a row.
 int slice_of(int64_t bytes, int parts) { return (int)std::max<int64_t>(8, round_up(ceil_div(bytes / 16, parts), 8)); }
 
-// Rows of up to kShortest bytes go to a warp's registers, four pieces a lane, up to kShort bytes
-// sixteen, and up to kShortTeam bytes to those of four warps.
-constexpr int64_t kShortest = 2 << 10, kShortTeam = 32 << 10;
+// Short rows by how many of a row's pieces a lane holds: rows of up to 8 KB go to a warp, up to 32 KB to
+// a block of four.  What counts is how many rows are under way on an SM, since each is a chain of
+// dependent loads (weight, ids, logits) and short sums: 8192 rows of 1900 bf16 24 us with a warp each and
+// six blocks of four warps an SM, 40 with four warps each; of 4000 40 and 46; of 4099, four warps each, 46.
 template <typename E>
 cudaError_t launch_distill(const Distill &r, int64_t bytes, cudaStream_t st) {
   const dim3 fourth((unsigned)ceil_div(r.T, 4)), each((unsigned)r.T);
-  if (bytes <= kShortest) return launch(short_kernel<E, 4, 1, 6>, fourth, dim3(128), 0, st, 1, true, r);
-  if (bytes <= 8 << 10) return launch(short_kernel<E, 4, 4, 8>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 2 << 10) return launch(short_kernel<E, 4, 1, 8>, fourth, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 4 << 10) return launch(short_kernel<E, 8, 1, 6>, fourth, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 8 << 10) return launch(short_kernel<E, 16, 1, 4>, fourth, dim3(128), 0, st, 1, true, r);
   if (bytes <= 16 << 10) return launch(short_kernel<E, 8, 4, 8>, each, dim3(128), 0, st, 1, true, r);
-  if (bytes <= kShortTeam) return launch(short_kernel<E, 16, 4, 4>, each, dim3(128), 0, st, 1, true, r);
+  if (bytes <= 32 << 10) return launch(short_kernel<E, 16, 4, 4>, each, dim3(128), 0, st, 1, true, r);
   if (r.dlogits)
     if (const HeldPlan plan = plan_held<E>(r.T, bytes); plan.cluster > 0) return launch_held<E>(r, plan, st);
   const int64_t sms = num_sms();
