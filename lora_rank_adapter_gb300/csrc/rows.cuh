@@ -237,7 +237,7 @@ struct Scale {
     Scale s;
     s.k = (float)k;
     if ((double)s.k >= k) s.k = nextafterf(s.k, 0.f);
-    s.k_lo = fmaxf((float)(k - (double)s.k), 1.17549435e-38f);      // above zero: minus infinity times it stays that
+    s.k_lo = fmaxf((float)(k - (double)s.k), nextafterf(0.f, 1.f));      // above zero: minus infinity times it stays that
     s.hi = (float)inv;
     s.lo = (float)(inv - (double)s.hi);
     return s;

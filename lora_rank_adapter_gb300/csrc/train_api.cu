@@ -263,7 +263,7 @@ lora_status_t lora_distill_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_
   LORA_TRY(check_ptr(row_loss, T, 4));
   LORA_TRY(check_ptr(loss, 1, 4));
   // the sum takes the weights once more, after the rows' losses have been written
-  for (const float *in : {teacher_logps, rest_logps, weights})
+  for (const float *in : {teacher_logps, rest_logps, weights, (const float *)loss})
     if (T > 0 && row_loss == in) return LORA_ERR_INVALID_ARG;
   DistillArgs a{};
   a.dtype = dtype; a.T = T; a.V = V; a.K = K; a.logits = logits; a.ldl = ldl; a.ids = top_ids;

@@ -134,7 +134,7 @@ def check(row, loss, d, want):
 
 
 SIZES = [(1, 1, 1), (3, 2, 5), (2, 7, 3), (5, 8, 8), (4, 9, 2), (3, 255, 128), (40, 300, 64), (7, 1001, 20), (2, 2049, 1),
-         (3, 8192, 128), (2, 32003, 17), (1, 128256, 20), (160, 17001, 64), (90, 20001, 100), (3, 450000, 30)]
+         (3, 8192, 128), (2, 32003, 17), (1, 128256, 20), (160, 17001, 64), (90, 20001, 100), (3, 450000, 30), (2, 300001, 9)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -229,6 +229,21 @@ def test_masks_and_infinities(V):
             assert bool(row[2].isfinite())
         for t in (4, 5, 6):
             assert math.isnan(row[t]) and bool(d[t].isnan().any()), t
+
+
+@pytest.mark.parametrize("V", [60, 9001, 40001])
+@pytest.mark.parametrize("temp", [1e-3, 0.02, 50.0, 1e20, 3e37])
+def test_far_temperatures(V, temp):
+    """Students of one token, and uniform ones with masks: all but zero and all but equal probabilities."""
+    T, K = 4, 6
+    _, x, ids, _, _, w = make(T, V, K, F32, seed=12)
+    x[1, V - 20:] = -INF
+    top = torch.log_softmax(torch.randn(T, K + 1, generator=torch.Generator().manual_seed(5)), 1).to(DEV)
+    top, rest = top[:, :K].contiguous(), top[:, K].contiguous()
+    for kind in ("forward", "reverse"):
+        d = torch.empty_like(x)
+        row, loss = call(x, ids, top, rest, w, kind, d, temp)
+        check(row, loss, d, oracle(x, ids, top, rest, w, kind, temp))
 
 
 def test_gradient_against_differences():

@@ -32,7 +32,7 @@ def back(L, lab=FAKE, ids=FAKE, stats=FAKE, H=FAKE, gl=FAKE, gh=FAKE, gt=FAKE, d
                                      gt, d, ldd, NULL)
 
 
-def distill(L, ids=FAKE, q=FAKE, rest=NULL, w=NULL, kind=0, row=FAR, loss=FAR, d=NULL, ldd=0, gs=1.0, **k):
+def distill(L, ids=FAKE, q=FAKE, rest=NULL, w=NULL, kind=0, row=FAR, loss=ctypes.c_void_p(0x30000), d=NULL, ldd=0, gs=1.0, **k):
     k = {**ROWS, **k}
     return L.lora_distill_loss(k["dt"], k["T"], k["V"], k["K"], k["x"], k["ld"], ids, q, rest, w, kind, k["temp"], row,
                                loss, d, ldd, gs, NULL)
@@ -74,7 +74,7 @@ def test_distill_arguments(L):
                            ({"rest": ODD2}, ALIGNMENT), ({"w": ODD2}, ALIGNMENT), ({"row": ODD2}, ALIGNMENT),
                            ({"loss": ODD2}, ALIGNMENT), ({"gs": NAN}, INVALID), ({"gs": INF}, INVALID),
                            ({"d": FAR, "ldd": 5}, INVALID), ({"d": FAKE, "ldd": 40}, INVALID), ({"d": ODD1, "ldd": 33}, ALIGNMENT),
-                           ({"row": FAKE, "w": FAKE}, INVALID), ({"row": FAKE, "q": FAKE}, INVALID),
+                           ({"row": FAKE, "w": FAKE}, INVALID), ({"loss": FAR}, INVALID), ({"row": FAKE, "q": FAKE}, INVALID),
                            ({"row": FAR, "rest": FAR}, INVALID)]:
         assert distill(L, **change) == status, change
 
