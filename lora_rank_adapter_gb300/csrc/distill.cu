@@ -456,21 +456,26 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
 // makes up the rows' records.  The working warps go through the rows without a barrier of the
 // block: each strikes the listed tokens out of its pieces, sends its sums over the rest to every
 // block of the cluster, waits for all of them, and works out the row's terms by itself.
+//
+// 6001 rows of 128256 bf16, 64 listed, 25 % ignored (1.2 GB read, 1.5 GB written): 503 us, 5.4 TB/s, 79 %
+// of the copy rate; read twice they took 696.  fp32 is bound by its bytes (1144 rows of 128256: 89 %); bf16 by
+// the chain from a row's last chunk to its gradient (an exchange, some logarithms) and by its instructions,
+// of which eight warps find a place in six cycles of ten.  What it came from: 655 us with each warp working
+// out all of a row's terms and repeated tokens found by comparing all with all, 590 with a warp of its own
+// for the records, 517 with what hangs on the list alone worked out there, the sums' exchange as it is.  The
+// ring: of the copy rate, chunks of 16 KB x 6 / 28 KB x 3 / 20 KB x 5: rows of 128256 bf16 79 % / 83 / 81, of 100000
+// 74 / 73 / 86, of 200000 79 / 79 / 86, of 50257 68 / 67 / 86, of 65536 fp32 91 / 85 / 91: the fewer blocks hold a
+// row, the better, and a last chunk that is short costs less of a short one.  Ten and twelve working warps:
+// 520 and 509 us.
 constexpr int kWorkers = 8;                              // warps that sum and write
 constexpr int kWork = 32 * kWorkers;
 constexpr int kHeldThreads = kWork + 64;                 // and the loader's warp, and the records'
 constexpr int kHeldBlocks = 2;
-// Chunks of kPer 16-byte pieces for each thread, kSlots of them in a block's ring.  bf16, bound by its
-// instructions, gains from long chunks; fp32, bound by its bytes, from chunks on their way ahead.  Of the
-// copy rate, 28 KB x 3 / 16 KB x 6: rows of 128256 bf16 83 % / 76, of 200000 81 / 80, of 100000 70 / 70;
-// rows of 32000 fp32 81 / 91, of 128256 88 / 89.
-template <typename E>
-struct Ring {
-  static constexpr bool kLong = sizeof(E) == 2;
-  static constexpr int kPer = kLong ? 7 : 4, kSlots = kLong ? 3 : 6, kChunk = kPer * kWork;
-  static constexpr int kSmem = kSlots * kChunk * 16;
-};
-constexpr int kAhead = 4;                                // records made up ahead
+constexpr int kPer = 5;                                  // 16-byte pieces of a chunk for each thread
+constexpr int kChunk = kPer * kWork;
+constexpr int kSlots = 5;
+constexpr int kRing = kSlots * kChunk * 16;              // 100 KB: with the rest two blocks' on an SM
+constexpr int kAhead = 2;                                // records made up ahead
 
 struct HeldDistill {
   Distill a;
@@ -518,12 +523,12 @@ template <typename E>
 __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDistill h) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ HeldRecord records[kAhead];
-  __shared__ uint64_t full[Ring<E>::kSlots], empty[Ring<E>::kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], step, done;
+  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], step, done;
   __shared__ float2 sums[kAhead];                        // (m, s) of a row, for its loss
   __shared__ uint32_t seen[kSeenWords];
   __shared__ float2 pairs[2][kMaxCluster * kWorkers];    // (m, s) of every warp of the cluster, two exchanges
   const Distill &a = h.a;
-  constexpr int N = Elem<E>::kVec, kPer = Ring<E>::kPer, kSlots = Ring<E>::kSlots, kChunk = Ring<E>::kChunk;
+  constexpr int N = Elem<E>::kVec;
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5, C = h.cluster, V = (int)a.V;
   const int rank = (int)(blockIdx.x % C);
   const int64_t clusters = gridDim.x / C;
@@ -723,10 +728,18 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
         __syncwarp();
       }
       const int n = min(kChunk, nv - from);
-      uint4 q[kPer];
+      if (n == kChunk) {
+        uint4 q[kPer];
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) q[u] = tid + u * kWork < n ? slot[tid + u * kWork] : Elem<E>::lowest();
-      absorb_exact<E, kPer>(m, s2, q, a.scale);
+        for (int u = 0; u < kPer; ++u) q[u] = slot[tid + u * kWork];
+        absorb_exact<E, kPer>(m, s2, q, a.scale);
+      } else {
+#pragma unroll 1
+        for (int i = tid; i < n; i += kWork) {
+          const uint4 q[1] = {slot[i]};
+          absorb_exact<E, 1>(m, s2, q, a.scale);
+        }
+      }
     }
     const float2 both = unpk2(s2);
     float s = both.x + both.y;
@@ -1025,28 +1038,28 @@ struct HeldPlan {
 };
 template <typename E>
 HeldPlan plan_held(int64_t T, int64_t bytes) {
-  int64_t c = std::max<int64_t>(1, ceil_div(bytes, Ring<E>::kSmem));
+  int64_t c = std::max<int64_t>(1, ceil_div(bytes, kRing));
   const int64_t fine = std::min(kHeldBlocks * num_sms() / std::max<int64_t>(T, 1), bytes / 4096);
   const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
   if (fine > c) {
     c = std::min<int64_t>(fine, kMaxCluster);
   } else if (c > 4 && c < kMaxCluster) {
-    auto blocks = [&](int64_t n) { return n * max_clusters(kernel, (int)n, Ring<E>::kSmem); };
+    auto blocks = [&](int64_t n) { return n * max_clusters(kernel, (int)n, kRing); };
     if (16 * blocks(c + 1) > 17 * blocks(c)) ++c;
   }
   c = std::min<int64_t>(c, kMaxCluster);
   const int64_t slice = std::max<int64_t>(8, round_up(ceil_div(bytes / 16, c), 8));
-  if (slice > Ring<E>::kSlots * Ring<E>::kChunk) return {0, 0};
+  if (slice > kSlots * kChunk) return {0, 0};
   return {(int)c, (int)slice};
 }
 
 template <typename E>
 cudaError_t launch_held(const Distill &r, const HeldPlan &plan, cudaStream_t st) {
   const void *kernel = reinterpret_cast<const void *>(held_kernel<E>);
-  cudaError_t e = ensure_smem(kernel, Ring<E>::kSmem);
+  cudaError_t e = ensure_smem(kernel, kRing);
   if (e != cudaSuccess) return e;
-  const int64_t clusters = std::min<int64_t>(r.T, max_clusters(kernel, plan.cluster, Ring<E>::kSmem));
-  return launch(held_kernel<E>, dim3((unsigned)(clusters * plan.cluster)), dim3(kHeldThreads), Ring<E>::kSmem, st,
+  const int64_t clusters = std::min<int64_t>(r.T, max_clusters(kernel, plan.cluster, kRing));
+  return launch(held_kernel<E>, dim3((unsigned)(clusters * plan.cluster)), dim3(kHeldThreads), kRing, st,
                 plan.cluster, true, HeldDistill{r, plan.cluster, plan.slice});
 }
 
