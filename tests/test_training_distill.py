@@ -304,6 +304,32 @@ def test_many_rows_in_place(T, V, dtype):
         assert torch.equal(copy, d) and torch.equal(again[0], row) and torch.equal(again[1], loss)
 
 
+@pytest.mark.parametrize("V,dtype", [(70001, BF16), (128256, BF16), (130000, F32)])
+def test_long_runs_of_ignored_rows(V, dtype):
+    """Clusters that come for thousands of rows, all but a few of them ignored, alone and in runs."""
+    g = torch.Generator(DEV).manual_seed(7)
+    T, K, live = 3000, 5, 40
+    x = torch.full((T, V), NAN, dtype=dtype, device=DEV)
+    ids = torch.randint(0, V, (T, K), generator=g, device=DEV)
+    top = torch.log_softmax(torch.randn((T, K + 1), generator=g, device=DEV), 1)[:, :K].contiguous()
+    w = torch.zeros(T, device=DEV)
+    rows = torch.cat([torch.randperm(T, generator=g, device=DEV)[:live], torch.arange(1500, 1520, device=DEV)]).unique()
+    x[rows] = (torch.randn((len(rows), V), generator=g, device=DEV) * 3).to(dtype)
+    w[rows] = 0.5
+    d = torch.full_like(x, 3.0)
+    for _ in range(3):
+        row, loss = call(x, ids, top, None, w, "forward", d)
+    some = rows[::9]
+    want = oracle(x[some], ids[some], top[some], None, w[some], "forward")
+    close(row[some], want["row"], want["row_tol"])
+    close(d[some], want["d"], want["d_tol"] + (2.0 ** -8 if dtype == BF16 else 2.0 ** -23) * want["d"].abs() + 1e-30)
+    off = torch.ones(T, dtype=torch.bool, device=DEV)
+    off[rows] = False
+    assert bool(row[off].eq(0).all()) and not bool(d[off].any()) and bool(row[rows].ne(0).all())
+    # every row once: the loss is their sum
+    close(loss[0], (w.double() * row.double()).sum().cpu(), 1e-6 * float((w * row).abs().sum()))
+
+
 def test_two_streams_and_a_graph():
     _, x, ids, top, rest, w = make(30, 32003, 20, BF16, seed=1)
     _, y, ids2, top2, rest2, w2 = make(3, 128256, 64, F32, seed=2)
