@@ -350,6 +350,18 @@ __device__ __forceinline__ void top_nothing(const TopRow &a, int64_t t, int lane
   if (a.stats) a.stats[t] = make_float2(0.f, 1.f);
 }
 
+// One pass over a row, by a block, or by the blocks of a cluster with a slice each (kSplit).  In
+// rounds of kPer pieces a thread it adds up s and w and keeps each thread's largest value; in rounds
+// 1, 2, 4, ... and at the end K of the threads' largest make a bar that the K largest tokens of the
+// row reach.  A piece that reaches the bar is set aside and not summed, so that what is left outside
+// the K largest is a sum of its own.  At the end the few tokens above the last bar are put in order,
+// the others of the pieces that were set aside join the sums.  Where places run out, select_all.
+//
+// Bound by instructions: 4096 rows of 128256 bf16, K = 64: 55 thousand warp instructions a row, 2.6 a
+// cycle and SM, 260 us, 4.0 TB/s, 60 % of the copy rate; with K = 0 34 thousand and 168 us, 93 %.
+// Three blocks of 256 threads an SM: of 128 threads 288-300 us, of 512 333.  2049 rows of 50001 fp32,
+// K = 1, 30 % ignored: 64 us, 66 %.  One row of 128256 bf16, K = 20: 8.5 us in a graph, of which a launch
+// takes about three, the rest the chain load, bar, order, two exchanges.
 template <typename E, int kThreads, bool kSplit>
 __global__ void __launch_bounds__(kThreads, kSplit ? 2 : kThreads == 256 ? 3 : 8) top_kernel(TopRow a, int clusters, int slice) {
   using Shared = TopShared<kThreads>;
@@ -672,6 +684,9 @@ struct TopGradRow {
   int64_t lddl;
 };
 
+// Bound by HBM: 2731 rows of 128256 bf16, K = 8, 20 % ignored (0.56 GB read, 0.70 GB written) 193 us,
+// 6.5 TB/s, 96 % of the copy rate.  Where logits and gradient lie at other offsets within 16 bytes it
+// writes words: 333 rows of 32001 fp32 18 us, 4.7 TB/s.
 constexpr int kGradThreads = 256;
 
 template <typename E>
