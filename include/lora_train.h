@@ -188,7 +188,7 @@ LORA_API lora_status_t lora_top_logps_backward(lora_dtype_t dtype, int64_t T, in
  *   top_logps  float [T][K];  rest_logps  float [T] or NULL: at the temperature of this call
  *   weights    float [T] or NULL for 1.  A row of weight 0 or without a listed token is
  *              IGNORED: its row_loss and its gradient are zero, and its logits do not matter
- *   row_loss   float [T], none of the inputs;  loss  float [1], not in row_loss
+ *   row_loss   float [T], sharing no place with the inputs;  loss  float [1], not in row_loss
  *   dlogits    NULL, or grad_scale * d loss / d logits
  * -------------------------------------------------------------------------------- */
 typedef enum { LORA_DISTILL_FORWARD = 0, LORA_DISTILL_REVERSE = 1 } lora_distill_kind_t;

@@ -263,8 +263,13 @@ lora_status_t lora_distill_loss(lora_dtype_t dtype, int64_t T, int64_t V, int32_
   LORA_TRY(check_ptr(row_loss, T, 4));
   LORA_TRY(check_ptr(loss, 1, 4));
   // the sum takes the weights once more, after the rows' losses have been written
-  for (const float *in : {teacher_logps, rest_logps, weights, (const float *)loss})
-    if (T > 0 && row_loss == in) return LORA_ERR_INVALID_ARG;
+  auto meets = [&](const void *p, int64_t bytes) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(p), row = reinterpret_cast<uintptr_t>(row_loss);
+    return p != nullptr && from < row + 4 * (uintptr_t)T && row < from + (uintptr_t)bytes;
+  };
+  if (meets(top_ids, 8 * T * K) || meets(teacher_logps, 4 * T * K) || meets(rest_logps, 4 * T) || meets(weights, 4 * T) ||
+      meets(loss, 4))
+    return LORA_ERR_INVALID_ARG;
   DistillArgs a{};
   a.dtype = dtype; a.T = T; a.V = V; a.K = K; a.logits = logits; a.ldl = ldl; a.ids = top_ids;
   a.teacher = teacher_logps; a.rest = rest_logps; a.weights = weights; a.reverse = kind == LORA_DISTILL_REVERSE;

@@ -330,6 +330,50 @@ def test_long_runs_of_ignored_rows(V, dtype):
     close(loss[0], (w.double() * row.double()).sum().cpu(), 1e-6 * float((w * row).abs().sum()))
 
 
+def test_results_that_lie_beside_the_inputs():
+    """One buffer of weights, row losses, the loss and the rest, with no gap between them."""
+    T, V, K = 37, 500, 9
+    _, x, ids, top, rest, w = make(T, V, K, F32, seed=3)
+    for kind in ("forward", "reverse"):
+        want = call(x, ids, top, rest, w, kind)
+        buf = torch.cat([w, torch.full((T + 1,), 5.0, device=DEV), rest])
+        row, loss = buf[T:2 * T], buf[2 * T:2 * T + 1]
+        training.lora_distill_loss(x, ids, top, row, loss, rest_logps=buf[2 * T + 1:], weights=buf[:T], kind=kind)
+        assert torch.equal(row, want[0]) and torch.equal(loss, want[1])
+        assert torch.equal(buf[:T], w) and torch.equal(buf[2 * T + 1:], rest)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [300, 9001, 40001])
+def test_rows_far_apart(V, dtype):
+    """Offsets of rows and of their gradients beyond 2^31 elements."""
+    T, K, ld = 3, 12, (1 << 30) + 8
+    _, x, ids, top, rest, w = make(T, V, K, dtype, seed=V)
+    d = torch.empty_like(x)
+    want = call(x, ids, top, rest, w, "forward", d)
+    far = torch.empty(2 * ld + V, dtype=dtype, device=DEV).as_strided((T, V), (ld, 1))
+    far.copy_(x)
+    row, loss = call(far, ids, top, rest, w, "forward")
+    check(row, loss, None, oracle(x, ids, top, rest, w, "forward"))
+    got = call(far, ids, top, rest, w, "forward", far)
+    check(*got, far, oracle(x, ids, top, rest, w, "forward"))
+    check(*want, d, oracle(x, ids, top, rest, w, "forward"))
+
+
+@pytest.mark.parametrize("V,dtype", [(140003, F32), (210001, F32), (420001, BF16)])
+def test_many_rows_of_a_long_vocabulary(V, dtype):
+    """One block a row, of more rounds than the word that says in which of them a listed token is met."""
+    T, K = 80, 128
+    _, x, ids, top, rest, w = make(T, V, K, dtype, seed=V)
+    ids[:, ::5] = torch.arange(V - 26, V, device=DEV)           # the same tokens late in each row, some twice
+    want = oracle(x, ids, top, rest, w, "reverse")
+    row, loss = call(x, ids, top, rest, w, "reverse")
+    check(row, loss, None, want)
+    d = torch.empty_like(x)
+    row, loss = call(x, ids, top, rest, w, "reverse", d)
+    check(row, loss, d, want)
+
+
 def test_two_streams_and_a_graph():
     _, x, ids, top, rest, w = make(30, 32003, 20, BF16, seed=1)
     _, y, ids2, top2, rest2, w2 = make(3, 128256, 64, F32, seed=2)

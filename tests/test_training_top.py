@@ -360,6 +360,31 @@ def test_captured_and_replayed():
     check(out, oracle(x, K, labels))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [300, 40001])
+def test_rows_far_apart(V, dtype):
+    """Offsets of rows and of their gradients beyond 2^31 elements."""
+    T, K, ld = 3, 12, (1 << 30) + 8
+    _, x, labels = make(T, V, dtype, seed=V, ignored=0.0)
+    far = torch.empty(2 * ld + V, dtype=dtype, device=DEV).as_strided((T, V), (ld, 1))
+    far.copy_(x)
+    out = call(far, K, labels)
+    check(out, oracle(x, K, labels))
+    near = call(x, K, labels)
+    g = torch.randn(T, device=DEV)
+    d = torch.empty_like(x)
+    training.lora_top_logps_backward(x, near["stats"], d, labels=labels, entropy=near["H"], dlogps=g, dentropy=g)
+    training.lora_top_logps_backward(far, near["stats"], far, labels=labels, entropy=near["H"], dlogps=g, dentropy=g)
+    assert torch.equal(far, d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [2, 160])
+def test_long_vocabulary(T, dtype):
+    _, x, labels = make(T, 500003 if T > 2 else 1000003, dtype, seed=T, ignored=0.0)
+    check(call(x, 128, labels), oracle(x, 128, labels))
+
+
 def test_no_rows_and_no_columns():
     call(torch.empty((0, 100), device=DEV), 5, torch.empty(0, dtype=torch.int64, device=DEV))
     out = call(torch.empty((3, 0), device=DEV), 5)

@@ -79,6 +79,15 @@ def test_distill_arguments(L):
         assert distill(L, **change) == status, change
 
 
+def test_row_losses_share_no_place_with_what_is_read(L):
+    """Parts of the rows' losses (24 bytes from FAR on) within an input or around the loss."""
+    far = FAR.value
+    at = lambda offset: ctypes.c_void_p(far + offset)  # noqa: E731
+    for name, size in (("ids", 6 * 4 * 8), ("q", 6 * 4 * 4), ("rest", 24), ("w", 24), ("loss", 4)):
+        for offset in (8 - size, 16):
+            assert distill(L, **{name: at(offset)}) == INVALID, (name, offset)
+
+
 def test_binding_refuses_tensors_that_do_not_belong(gpus):
     """What the binding itself refuses, by tensors that only say where they are."""
     _, calls = gpus
