@@ -429,18 +429,20 @@ __global__ void __launch_bounds__(128, kTeamBlocks) short_kernel(Distill a) {
   if (a.dlogits == nullptr) return;
   const RowGrad g = {ref_of(m), k, 0.f, x.f};
   const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
+  E *to = out + sp.head + tid * N;
+  if (same) {
 #pragma unroll
-  for (int u = 0; u < kPieces; ++u) {
-    const int i = tid + u * kLanes;
-    if (i >= sp.vecs) break;
-    q[u] = g.piece<E>(q[u]);
-    E *to = out + sp.head + i * N;
-    if (same) {
-      __stcs(reinterpret_cast<uint4 *>(to), q[u]);
-    } else {
-      const E *e = reinterpret_cast<const E *>(&q[u]);
+    for (int u = 0; u < kPieces; ++u) {
+      if (tid + u * kLanes >= sp.vecs) break;
+      __stcs(reinterpret_cast<uint4 *>(to + u * kLanes * N), g.piece<E>(q[u]));
+    }
+  } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) to[j] = e[j];
+    for (int u = 0; u < kPieces; ++u) {
+      const int have = sp.vecs - (tid - lane + u * kLanes);      // pieces from the warp's first on
+      if (have <= 0) break;
+      // (4-byte elements one by one: 4000 rows of 4099 fp32 39 us, 42 by pieces; of bf16 46 and 31)
+      store_run(to + u * kLanes * N, g.piece<E>(q[u]), min(32, have));
     }
   }
   if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge));
@@ -528,7 +530,7 @@ template <typename E>
 __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDistill h) {
   extern __shared__ __align__(128) uint4 ring[];
   __shared__ HeldRecord records[kAhead];
-  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], step, done;
+  __shared__ uint64_t full[kSlots], empty[kSlots], made[kAhead], read[kAhead], summed[kAhead], ready[2], done;
   __shared__ float2 sums[kAhead];                        // (m, s) of a row, for its loss
   __shared__ uint32_t seen[kSeenWords];
   __shared__ float2 pairs[2][kMaxCluster * kWorkers];    // (m, s) of every warp of the cluster, two exchanges
@@ -548,7 +550,6 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       mbar_init(&summed[i], 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(&ready[i], C == 1 ? kWorkers : 1);
-    mbar_init(&step, kWorkers);
     mbar_init(&done, C * kWorkers);
     fence_barrier_init();
   }
@@ -674,14 +675,14 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       if (again || i < at.slot) mbar_wait(&full[i], i < at.slot ? at.parity : at.parity ^ 1);
     // And the block does not end before every warp of the cluster has sent its last pair here, also
     // where a wait ran out: for as many limits as may lie ahead of a warp, whose rows in the ring are
-    // kSlots at most, of kSlots chunks, a record, an exchange and two steps each, and whose records
-    // may be kAhead rows further.
+    // kSlots at most, of kSlots chunks, a record and an exchange each, and whose records may be
+    // kAhead rows further.
     if (C > 1)
-      for (int i = 0; i < (kSlots + kAhead) * (kSlots + 4) && !mbar_wait<true>(&done, 0); ++i) {}
+      for (int i = 0; i < (kSlots + kAhead) * (kSlots + 2) && !mbar_wait<true>(&done, 0); ++i) {}
     return;
   }
 
-  uint32_t count = 0, steps = 0;                         // exchanges, and steps of the block, so far
+  uint32_t count = 0;                                    // exchanges so far
   const float k = a.scale.k;
   for (; t < a.T; t += clusters, rec.next()) {
     if (!__all_sync(0xffffffffu, mbar_wait(&made[rec.slot], rec.parity))) break;
@@ -700,15 +701,16 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       continue;
     }
     const unsigned touched = of.touched[warp];
-    // the elements of entries in this warp's pieces
-    auto each_place = [&](auto &&f) {
+    // the entries' elements that are this warp's by owner(place)
+    auto each_place = [&](auto &&owner, auto &&f) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         if (i * 32 >= a.K) continue;
         const int place = of.place[i * 32 + lane];
-        if (place >= 0 && place / N % kWork / 32 == warp) f(i, place);
+        if (place >= 0 && owner(place) == warp) f(i, place);
       }
     };
+    auto reads = [](int place) { return place / N % kWork / 32; };
     // the ragged ends, at most seven elements each: the first block's and the last one's, by warp 0
     const bool at_head = rank == 0 && tid < sl.head, at_tail = rank == C - 1 && tid >= 16 && tid - 16 < V - tail;
     const int edge_at = at_head ? tid : tail + tid - 16;
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
       ok = mbar_wait(&full[here.slot], here.parity) && ok;
       uint4 *slot = ring + here.slot * kChunk;
       if (touched >> (from / kChunk) & 1u) {
-        each_place([&](int, int place) {
+        each_place(reads, [&](int, int place) {
           if (place >= from * N && place < (from + kChunk) * N)
             Elem<E>::store(reinterpret_cast<E *>(slot) + (place - from * N), kNegInf);
         });
@@ -783,23 +785,16 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     const Terms x(a, of.ahead, m, s, false);
     const RowGrad g = {ref_of(m), k, 0.f, x.f};
     const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(sl.row)) & 15u) == 0;
-    // Where the gradient's rows sit at other offsets, warps write each other's elements: all have struck
-    // theirs out before, and the listed tokens' places come after all have written.
-    auto all_here = [&] {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&step);
-      const bool met = mbar_wait(&step, steps & 1);
-      ++steps;
-      return __all_sync(0xffffffffu, met);
-    };
-    if (!same && !all_here()) break;
+    // Where the gradient's rows sit at other offsets, a warp's output pieces take elements of other warps'
+    // pieces.  One of those that is struck out there may be read before or after that: the listed tokens'
+    // own values come after the piece, by the warp that wrote it.
     uint4 *dst = reinterpret_cast<uint4 *>(out + sl.head) + sl.v0;
     for (int from = 0; from < nv; from += kChunk, at.next()) {
       const int n = min(kChunk, nv - from);
       const uint4 *src = ring + at.slot * kChunk;
       if (!same) {
         const int e = first + from * N;                  // the chunk's first element
-        grad_words<E, kWork>(out, reinterpret_cast<const E *>(src) - e, e, e + n * N, -1, g);
+        grad_shifted<E, kWork>(out, reinterpret_cast<const E *>(src) - e, e, e + n * N, g);
       } else if (n == kChunk) {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) __stcs(dst + from + tid + u * kWork, g.piece<E>(src[tid + u * kWork]));
@@ -813,10 +808,16 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) held_kernel(HeldDis
     }
     if (at_head || at_tail) Elem<E>::store(out + edge_at, g(edge));
     __syncwarp();
-    if (!same && !all_here()) break;
-    if (touched) each_place([&](int i, int place) {
+    const int r = (int)(-reinterpret_cast<uintptr_t>(out + first) & 15u) / (int)sizeof(E);
+    auto writes = [&](int place) {                         // as grad_shifted shares out a chunk: r elements, n - 1 pieces, the rest
+      const int p = place % (kChunk * N) - r, n = min(kChunk, nv - place / (kChunk * N) * kChunk);
+      return p < 0 || p >= (n - 1) * N ? 0 : p / N % kWork / 32;
+    };
+    auto own = [&](int i, int place) {
       Elem<E>::store(out + first + place, x.dz(i * 32 + lane, of.e[i * 32 + lane], of.x[i * 32 + lane]));
-    });
+    };
+    if (!same) each_place(writes, own);
+    else if (touched) each_place(reads, own);
     if (warp == 0 && of.edges)
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
@@ -982,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 5) row_kernel(Distill a, int C, int 
   const RowGrad g = {m_of, k, 0.f, f_of};
   const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
   if (!same) {
-    grad_words<E, kThreads>(out, row, e0, e1, -1, g);
+    grad_shifted<E, kThreads>(out, row, e0, e1, g);
   } else {
     const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
     uint4 *dst = reinterpret_cast<uint4 *>(out + sp.head);

@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "f32x2.cuh"
 
@@ -325,6 +327,73 @@ struct RowGrad {
     return Elem<E>::pack_pairs(v);
   }
 };
+
+// The 16 bytes that begin `words` words and `bits` bits (0 or 16) behind the start of two pieces.
+// (4-byte elements: bits are 0.)
+template <typename E>
+__device__ __forceinline__ uint4 shifted(const uint4 &a, const uint4 &b, int words, unsigned bits) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int j = 0; j < 6; ++j) w[j] = words & 2 ? w[j + 2] : w[j];
+#pragma unroll
+  for (int j = 0; j < 5; ++j) w[j] = words & 1 ? w[j + 1] : w[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = sizeof(E) == 4 ? w[j] : __funnelshift_r(w[j], w[j + 1], bits);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Stores pieces that the first `have` lanes (1 to 32) of a warp hold where the output sits at another offset
+// to a 16-byte boundary; `to`: where a lane's piece begins.  2-byte elements: have - 1 whole pieces of the
+// output, the kVec elements at both ends one by one; 4-byte elements one by one.
+template <typename E>
+__device__ __forceinline__ void store_run(E *to, const uint4 &q, int have) {
+  constexpr int N = Elem<E>::kVec;
+  const int lane = lane_id();
+  const E *e = reinterpret_cast<const E *>(&q);
+  if (sizeof(E) == 4) {
+    if (lane < have)
+#pragma unroll
+      for (int j = 0; j < N; ++j) to[j] = e[j];
+    return;
+  }
+  const int bytes = (int)(-reinterpret_cast<uintptr_t>(to) & 15u), r = bytes / (int)sizeof(E);
+  const uint4 next = make_uint4(__shfl_down_sync(0xffffffffu, q.x, 1), __shfl_down_sync(0xffffffffu, q.y, 1),
+                                __shfl_down_sync(0xffffffffu, q.z, 1), __shfl_down_sync(0xffffffffu, q.w, 1));
+  if (lane < have - 1) __stcs(reinterpret_cast<uint4 *>(to + r), shifted<E>(q, next, bytes >> 2, bytes & 2 ? 16 : 0));
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if ((lane == 0 && j < r) || (lane == have - 1 && j >= r)) to[j] = e[j];
+}
+
+// Elements [e0, e1) of the output row where it sits at another offset to a 16-byte boundary than the
+// logits, by whole 16-byte pieces of the output, each from two of the input: element i of the row at
+// src[i], of which nothing outside [e0, e1) is read.
+template <typename E, int kThreads, typename G>
+__device__ __forceinline__ void grad_shifted(E *out, const E *src, int e0, int e1, const G &g) {
+  constexpr int N = Elem<E>::kVec, kSize = (int)sizeof(E);
+  const int tid = threadIdx.x;
+  const int bytes = (int)((reinterpret_cast<uintptr_t>(src) - reinterpret_cast<uintptr_t>(out)) & 15u), r = bytes / kSize;
+  int b = e0 + (int)(-reinterpret_cast<uintptr_t>(out + e0) & 15u) / kSize;      // an output piece starts here
+  if (b - r < e0) b += N;
+  const int n = max(0, (e1 - b + r - N) / N);            // pieces
+  const uint4 *from = reinterpret_cast<const uint4 *>(src + b - r);
+  uint4 *to = reinterpret_cast<uint4 *>(out + b);
+  auto pieces = [&](auto words) {
+#pragma unroll 2
+    for (int i = tid; i < n; i += kThreads)
+      __stcs(to + i, g.template piece<E>(shifted<E>(from[i], from[i + 1], decltype(words)::value, bytes & 2 ? 16 : 0)));
+  };
+  switch (bytes >> 2) {
+    case 0: pieces(std::integral_constant<int, 0>()); break;
+    case 1: pieces(std::integral_constant<int, 1>()); break;
+    case 2: pieces(std::integral_constant<int, 2>()); break;
+    default: pieces(std::integral_constant<int, 3>());
+  }
+  // the ends, fewer than 2 N elements each
+  auto one = [&](int i) { Elem<E>::store(out + i, g(Elem<E>::load(src + i))); };
+  if (tid < min(b, e1) - e0) one(e0 + tid);
+  if (tid < e1 - b - n * N) one(b + n * N + tid);
+}
 
 // Elements [e0, e1) of the output row where it sits at another offset to a
 // 16-byte boundary than the logits: 4-byte words of the output, their elements

@@ -685,12 +685,13 @@ struct TopGradRow {
 };
 
 // Bound by HBM: 2731 rows of 128256 bf16, K = 8, 20 % ignored (0.56 GB read, 0.70 GB written) 193 us,
-// 6.5 TB/s, 96 % of the copy rate.  Where logits and gradient lie at other offsets within 16 bytes it
-// writes words: 333 rows of 32001 fp32 18 us, 4.7 TB/s.
+// 6.5 TB/s, 96 % of the copy rate.  Where logits and gradient lie at other offsets within 16 bytes each
+// output piece takes two of the input: 2000 rows of 128257 bf16, K = 17, 289 us with the forward pass, by
+// words of the output 385; 333 rows of 32001 fp32 31 and 37.
 constexpr int kGradThreads = 256;
 
 template <typename E>
-__global__ void __launch_bounds__(kGradThreads) top_grad_kernel(TopGradRow h, int parts, int slice) {
+__global__ void __launch_bounds__(kGradThreads, 8) top_grad_kernel(TopGradRow h, int parts, int slice) {
   __shared__ int ids[kMaxTop + 1];               // -1: none; the label after the listed tokens
   __shared__ float add[kMaxTop + 1];
   __shared__ int64_t label_of;
@@ -757,7 +758,7 @@ __global__ void __launch_bounds__(kGradThreads) top_grad_kernel(TopGradRow h, in
   const bool same = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
   __syncthreads();
   if (!same) {
-    grad_words<E, kGradThreads>(out, row, e0, e1, -1, g);
+    grad_shifted<E, kGradThreads>(out, row, e0, e1, g);
   } else {
     const uint4 *src = reinterpret_cast<const uint4 *>(row + sp.head);
     uint4 *dst = reinterpret_cast<uint4 *>(out + sp.head);

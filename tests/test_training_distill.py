@@ -330,6 +330,23 @@ def test_long_runs_of_ignored_rows(V, dtype):
     close(loss[0], (w.double() * row.double()).sum().cpu(), 1e-6 * float((w * row).abs().sum()))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("V", [1, 7, 8, 17, 40, 257, 1901, 4099, 20011, 52003, 450003])
+def test_gradients_at_any_offset(V, dtype):
+    """Rows of the gradient at every offset within 16 bytes to those of the logits: the same values, and nothing beside them."""
+    T, K = 3, 6
+    _, x, ids, top, rest, w = make(T, V, K, dtype, seed=V, pad=1, first=2)
+    ids[1] = torch.tensor([0, V - 1, V // 2, 1, V - 2, V // 2 + 1], device=DEV)     # the ends too
+    d = torch.empty_like(x)                                                          # rows as the logits' up to a shift
+    call(x, ids, top, rest, w, "forward", d)
+    check(*call(x, ids, top, rest, w, "forward"), d, oracle(x, ids, top, rest, w, "forward"))
+    for first in range(16 // x.element_size()):
+        out = torch.full((T, V + 16), 55.0, dtype=dtype, device=DEV)
+        call(x, ids, top, rest, w, "forward", out[:, first:first + V])
+        assert torch.equal(out[:, first:first + V], d), first
+        assert bool((out[:, :first] == 55).all()) and bool((out[:, first + V:] == 55).all())
+
+
 def test_results_that_lie_beside_the_inputs():
     """One buffer of weights, row losses, the loss and the rest, with no gap between them."""
     T, V, K = 37, 500, 9

@@ -361,6 +361,25 @@ def test_captured_and_replayed():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,V", [(3, 1), (3, 7), (2, 17), (3, 40), (2, 1901), (2, 20011), (400, 9001)])
+def test_gradients_at_any_offset(T, V, dtype):
+    """Rows of the gradient at every offset within 16 bytes to those of the logits: the same values, and nothing beside them."""
+    K = 6
+    _, x, labels = make(T, V, dtype, seed=V, pad=1, first=2)
+    near = call(x, K, labels)
+    g, gt = torch.randn(T, device=DEV), torch.randn(T, K, device=DEV)
+    back = lambda d: training.lora_top_logps_backward(  # noqa: E731
+        x, near["stats"], d, labels=labels, top_ids=near["ids"], entropy=near["H"], dlogps=g, dentropy=g, dtop_logps=gt)
+    d = torch.full((T, V + 3), 55.0, dtype=dtype, device=DEV)[:, 2:2 + V]      # at the logits' own offsets
+    back(d)
+    for first in range(16 // x.element_size()):
+        out = torch.full((T, V + 16), 55.0, dtype=dtype, device=DEV)
+        back(out[:, first:first + V])
+        assert torch.equal(out[:, first:first + V], d), first
+        assert bool((out[:, :first] == 55).all()) and bool((out[:, first + V:] == 55).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("V", [300, 40001])
 def test_rows_far_apart(V, dtype):
     """Offsets of rows and of their gradients beyond 2^31 elements."""
