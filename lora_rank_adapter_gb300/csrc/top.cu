@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, kSplit ? 2 : kThreads == 256 ? 3 : 8
         }
         __syncthreads();
         bar = sh.bar;
-        next *= K > 32 ? 2 : 4;
+        next *= K > 32 || kThreads == 128 ? 2 : 4;       // (the small block has fewer places, and short rounds)
       }
       if (__any_sync(0xffffffffu, g >= bar)) {
 #pragma unroll
@@ -656,7 +656,6 @@ __global__ void __launch_bounds__(kThreads, kSplit ? 2 : kThreads == 256 ? 3 : 8
 // d = e (a + b u) for a token that no gradient comes from by itself.
 struct TopGrad {
   float m, k, a, b;
-  static constexpr float c = 0.f;
   __device__ __forceinline__ float operator()(float v) const {
     const float u = fmaxf((v - m) * k, kLeast);
     return ex2(u) * fmaf(b, u, a);
@@ -845,12 +844,17 @@ int clusters_at_once(int size) {
 // A row goes to one block, of fewer threads where it is short; rows that leave SMs idle that way are cut
 // over the blocks of a cluster, down to 4 KB a block, one block an SM: rows of 128256 bf16, K = 20, one block
 // an SM / two: 32 rows 10.3 us / 13.5, 76 rows 12.6 / 13.8; 97 rows over three blocks each 20.5, over one 15.2.
+// Rows of up to 128 KB go to small blocks too where there are two full waves of the larger ones: eight small
+// blocks an SM hide a row's short steps better than three large ones.  Large / small: 1080 rows of 16320 bf16,
+// K = 20, 22.4 / 16.6 us, 2000 of 32000 50.6 / 44.9, 4000 of 60001 137 / 124; but 700 rows of 32000 18.5 / 22.9,
+// 2049 of 50001 fp32 85 / 96; and above 48 the small block's places run out (1080 rows, K = 96: 33 / 120).
 template <typename E>
 cudaError_t launch_top(const TopRow &r, int64_t bytes, cudaStream_t st) {
   if (bytes > 8 << 10)
     for (int c = (int)std::min<int64_t>({kMaxCluster, bytes / (4 << 10), num_sms() / r.T}); c > 1; --c)
       if (r.T <= clusters_at_once<E>(c)) return launch_top_as<E, 256, true>(r, c, slice_of(bytes, c), st);
-  if (bytes <= 16 << 10) return launch_top_as<E, 128, false>(r, 1, slice_of(bytes, 1), st);
+  const bool many = r.T > 6 * (int64_t)num_sms() && r.K <= 48 && bytes <= 128 << 10;
+  if (bytes <= 16 << 10 || many) return launch_top_as<E, 128, false>(r, 1, slice_of(bytes, 1), st);
   return launch_top_as<E, 256, false>(r, 1, slice_of(bytes, 1), st);
 }
 

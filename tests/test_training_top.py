@@ -397,6 +397,20 @@ def test_rows_far_apart(V, dtype):
     assert torch.equal(far, d)
 
 
+@pytest.mark.parametrize("V,dtype", [(9001, BF16), (16000, F32), (30011, F32), (64001, BF16)])
+def test_many_rows(V, dtype):
+    """More rows than the device holds large blocks twice: random, ascending ones, and ones of one value but for some."""
+    T = 1000
+    _, x, labels = make(T, V, dtype, seed=V, pad=1)
+    x[10] = torch.arange(V, device=DEV) / V
+    x[11], x[12] = x[10].flip(0), x[10] * 100
+    x[13] = 1.0
+    x[14, 5:] = -INF
+    x[15] = torch.linspace(-4, 4, V, device=DEV) + x[16] / 3
+    for K in (1, 20, 48, 49):
+        check(call(x, K, labels), oracle(x, K, labels))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T", [2, 160])
 def test_long_vocabulary(T, dtype):
