@@ -249,11 +249,20 @@ def lora_policy_loss(logits, labels, old_logps, advantages, weights, token_logps
     return metrics
 
 
+def _width(top_ids):
+    shape = top_ids.shape
+    if len(shape) != 2:
+        raise ValueError("top_ids have to be [T, K]")
+    return shape[1]
+
+
 def _entries(t, T, K, dtype, name, device):
     """The address of a contiguous [T, K] tensor."""
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != K:
+    if t.shape != (T, K):
         raise ValueError(f"{name} have to be [{T}, {K}], not {tuple(t.shape)}")
-    return _vector(t, T * K, dtype, name, device)
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, T * K, dtype, name, device)
+    return t.data_ptr()
 
 
 def lora_top_logps(logits, top_ids, top_logps, labels=None, logps=None, entropy=None, rest_logps=None, stats=None,
@@ -268,9 +277,7 @@ def lora_top_logps(logits, top_ids, top_logps, labels=None, logps=None, entropy=
     dev, f32 = logits.get_device(), torch.float32
     if (labels is None) != (logps is None):
         raise ValueError("labels and logps go together")
-    if top_ids.dim() != 2:
-        raise ValueError("top_ids have to be [T, K]")
-    K = top_ids.shape[1]
+    K = _width(top_ids)
     entry = _entry(lib().lora_top_logps, dev)
     st = entry(_dtype(logits), T, V, K, x, ld, _optional(labels, T, torch.int64, "labels", dev), temperature,
                _optional(logps, T, f32, "logps", dev), _optional(entropy, T, f32, "entropy", dev),
@@ -297,9 +304,7 @@ def lora_top_logps_backward(logits, stats, dlogits, labels=None, top_ids=None, e
     d, ldd = _gradient(dlogits, logits)
     K, ids, dtop = 0, None, None
     if dtop_logps is not None:
-        if top_ids.dim() != 2:
-            raise ValueError("top_ids have to be [T, K]")
-        K = top_ids.shape[1]
+        K = _width(top_ids)
         ids = _entries(top_ids, T, K, torch.int64, "top_ids", dev)
         dtop = _entries(dtop_logps, T, K, f32, "dtop_logps", dev)
     entry = _entry(lib().lora_top_logps_backward, dev)
@@ -323,9 +328,7 @@ def lora_distill_loss(logits, top_ids, top_logps, row_loss, loss, rest_logps=Non
     dev, f32 = logits.get_device(), torch.float32
     if kind not in DISTILL_KINDS:
         raise ValueError(f"kind has to be one of {sorted(DISTILL_KINDS)}")
-    if top_ids.dim() != 2:
-        raise ValueError("top_ids have to be [T, K]")
-    K = top_ids.shape[1]
+    K = _width(top_ids)
     d, ldd = _gradient(dlogits, logits)
     entry = _entry(lib().lora_distill_loss, dev)
     st = entry(_dtype(logits), T, V, K, x, ld, _entries(top_ids, T, K, torch.int64, "top_ids", dev),
