@@ -683,10 +683,11 @@ struct TopGradRow {
   int64_t lddl;
 };
 
-// Bound by HBM: 2731 rows of 128256 bf16, K = 8, 20 % ignored (0.56 GB read, 0.70 GB written) 193 us,
-// 6.5 TB/s, 96 % of the copy rate.  Where logits and gradient lie at other offsets within 16 bytes each
-// output piece takes two of the input: 2000 rows of 128257 bf16, K = 17, 289 us with the forward pass, by
-// words of the output 385; 333 rows of 32001 fp32 31 and 37.
+// Bound by HBM: 2731 rows of 128256 bf16, K = 8, 20 % ignored (0.56 GB read, 0.70 GB written) 189 us,
+// 6.7 TB/s, 98 % of the copy rate; smaller ones by the chain before a block's first piece, so all that it
+// depends on is loaded at once (350 rows of 128256 fp32 with the forward pass 94 us; label first, 101).  Where logits and gradient lie at other offsets within 16 bytes each
+// output piece takes two of the input: 2000 rows of 128257 bf16, K = 17, 283 us with the forward pass, by
+// words of the output 385; 333 rows of 32001 fp32 30 and 37.
 constexpr int kGradThreads = 256;
 
 template <typename E>
@@ -699,10 +700,6 @@ __global__ void __launch_bounds__(kGradThreads, 8) top_grad_kernel(TopGradRow h,
   const int64_t t = a.T - 1 - blockIdx.x / parts;      // the rows that were read last come first
   const int rank = (int)(blockIdx.x % parts), tid = threadIdx.x, V = (int)a.V, K = h.dtop ? a.K : 0;
   constexpr int N = Elem<E>::kVec;
-  if (tid == 0) label_of = a.labels ? a.labels[t] : 0;      // read once for the block
-  __syncthreads();
-  const int64_t label = label_of;
-  const bool counts = !a.labels || (label >= 0 && label < V);
   E *out = static_cast<E *>(h.dlogits) + t * h.lddl;
   const E *row = static_cast<const E *>(a.logits) + t * a.ldl;
   const RowSpan<E> sp(row, V);
@@ -714,15 +711,22 @@ __global__ void __launch_bounds__(kGradThreads, 8) top_grad_kernel(TopGradRow h,
     if (tid < K) {
       id = a.ids[t * K + tid];
       g = h.dtop[t * K + tid];
-    } else if (a.labels && h.dlogps) {
-      id = label;
-      g = h.dlogps[t];
+    } else {
+      const int64_t label = a.labels ? a.labels[t] : 0;      // read once for the block
+      label_of = label;
+      if (a.labels && h.dlogps) {
+        id = label;
+        g = h.dlogps[t];
+      }
     }
-    const bool there = counts && id >= 0 && id < V;
+    const bool there = id >= 0 && id < V;
     ids[tid] = there ? (int)id : -1;
     add[tid] = there ? g : 0.f;
   }
+  const float2 st = a.stats[t];
+  const float dh = h.dentropy ? h.dentropy[t] : 0.f, entropy = h.dentropy ? a.entropy[t] : 0.f;
   __syncthreads();
+  const bool counts = !a.labels || (label_of >= 0 && label_of < V);
   float G = 0.f;
   bool any = false;
   for (int j = lane_id(); j <= K; j += 32) {
@@ -731,17 +735,15 @@ __global__ void __launch_bounds__(kGradThreads, 8) top_grad_kernel(TopGradRow h,
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) G += __shfl_xor_sync(0xffffffffu, G, o);
-  const float dh = counts && h.dentropy ? h.dentropy[t] : 0.f;
   if (!counts || (dh == 0.f && !__any_sync(0xffffffffu, any))) {      // the same for all warps
     zero_span<E, kGradThreads>(out, e0, e1, tid);
     return;
   }
-  const float2 st = a.stats[t];
   const float log_s = logf(st.y), f = a.scale.hi / st.y;
   TopGrad g;
   g.m = st.x;
   g.k = a.scale.k;
-  g.a = -f * (dh != 0.f ? G + dh * (a.entropy[t] - log_s) : G);
+  g.a = -f * (dh != 0.f ? G + dh * (entropy - log_s) : G);
   g.b = -f * dh * kLn2;
   // a listed token's own gradient, once for each time that it is listed; its logit
   // before the gradient may replace it
